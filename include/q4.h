@@ -34,6 +34,19 @@
  *                 E4M3(clamp(x/scale, +-448)).  ("Quantization in
  *                 deployment", formats.py fp8() per row; "Quantization
  *                 chains", "One outlier sets the scale".)
+ *   Q4_MXINT8, Q4_MXFP8  activations saved for the backward pass, not an
+ *                 operand of a W4 product: one byte per value and one
+ *                 power-of-two scale per 32 values, stored as the byte b of
+ *                 2^(b-127).  scale = the least 2^e >= 2^-111 with
+ *                 max|x| <= top * 2^e; code = rne(x / scale) as a two's
+ *                 complement byte (MXINT8, top = 127) or an E4M3 byte (MXFP8,
+ *                 top = 448).  Integers err by up to 1/256 of (nearly) the
+ *                 block's largest value everywhere; E4M3 by up to 2^-4 of each
+ *                 value: integers suit ordinary blocks, E4M3 blocks in which
+ *                 one outlier would leave the rest few codes.  A block with
+ *                 an infinity or a NaN has b = 255 and reads back as NaN
+ *                 throughout; a code whose value would reach 2^128 is stored
+ *                 one lower.  8.25 bits per value.
  * Every rounding is to nearest, ties to the even code; E2M1 and E4M3 keep
  * the sign bit of the input; a block whose stored scale is 0 has magnitude
  * codes 0.
@@ -78,6 +91,9 @@
  *              16..31 at 1024 + 16l.  Padding rows hold code 0.
  *   scales     fp32 [rows] in both layouts; global_scale is NULL.
  *
+ * Q4_MXINT8 and Q4_MXFP8 (row-major only, cols % 32 == 0): codes uint8
+ *   [rows][cols], scales uint8 [rows][cols/32]; global_scale is NULL.
+ *
  *   global_scale  NVFP4 only: device fp32[1], the multiplier gs; else NULL.
  *
  * Conventions for every call:
@@ -112,7 +128,9 @@ typedef enum q4_format {
     Q4_MXFP4 = 1,
     Q4_NVFP4 = 2,
     Q4_FP8_ROW = 3,
-    Q4_INT4_ZP_G128 = 4
+    Q4_INT4_ZP_G128 = 4,
+    Q4_MXFP8 = 5,
+    Q4_MXINT8 = 6
 } q4_format;
 
 typedef enum q4_layout {
@@ -168,7 +186,7 @@ q4_status q4_sizes(int fmt, int layout, int64_t rows, int64_t cols, size_t* code
  * kilobytes; "Low-bit inference for very large MoE", "A few details":
  * pre-shuffled weights), so weights quantized or packed row-major are worth
  * converting once, when they are loaded.
- *   src, dst  the same fmt (not Q4_FP8_ROW: Q4_ERR_FORMAT), rows and cols
+ *   src, dst  the same weight format (else Q4_ERR_FORMAT), rows and cols
  *             (else Q4_ERR_SHAPE); each validated like any q4_tensor (the
  *             tiled one needs cols % 512 == 0).  Equal layouts: a copy.
  *   dst must not overlap src.  Empty tensors: only the NVFP4 global scale
@@ -344,11 +362,164 @@ q4_status q4_swiglu(const void* gu_bf16, int64_t ld_gu, int64_t P, int64_t I, vo
 /*
  * Gated combine: out[t][n] = bf16(sum_j weights[t][j] * y[inv[t][j]][n]),
  * fp32 accumulation in choice order.  y_bf16 [P][ldy] (expert outputs in
- * routed-row order), inv/weights [T][k] as q4_moe_route writes them,
- * out_bf16 [T][ldo]; N % 8 == 0.
+ * routed-row order), inv/weights [T][k] as q4_moe_route or q4_moe_sort write
+ * them (a choice with inv < 0 was dropped and adds nothing), out_bf16
+ * [T][ldo]; N % 8 == 0.
  */
 q4_status q4_moe_combine(const void* y_bf16, int64_t ldy, const int32_t* inv, const float* weights,
                          int64_t T, int32_t k, int64_t N, void* out_bf16, int64_t ldo, void* stream);
+
+/*
+ * The backward pass of the products and of the MoE layer on 4-bit weights:
+ * gradients for activations through frozen weights, gradients for the
+ * full-precision weights that a quantization-aware run trains ("Low-bit
+ * inference for very large MoE", "Why quantization-aware training": the
+ * straight-through gradient of a fake-quantized weight is that of the weight),
+ * activations saved in 8 bits in between, and tokens sorted by expert and back.
+ * A training step of one layer is
+ *   q4_moe_topk -> q4_moe_sort -> q4_grouped_gemm (gate/up) ->
+ *   q4_swiglu_save -> q4_grouped_gemm (down) -> q4_moe_combine
+ * and backwards
+ *   q4_moe_combine_backward -> q4_grouped_gemm_dgrad (down) ->
+ *   q4_swiglu_backward -> q4_grouped_gemm_dgrad (gate/up) ->
+ *   q4_moe_permute_backward, with q4_grouped_gemm_wgrad for the weights and
+ *   q4_moe_topk_backward for the router.
+ *
+ * Results do not vary from run to run: sums are in fp32 in an order that the
+ * sizes alone decide, with no floating-point atomics.  Workspaces are the
+ * caller's, 16-byte aligned, of at least the size the matching *_workspace
+ * call gives (host arithmetic only; 0 for many sizes, then NULL may be passed),
+ * without contents to keep; two calls that may run at once (two streams, two
+ * captured graphs) need one each.  The per-token calls need T < 2^23 and
+ * T * ceil(columns/1024) < 2^25, the products a launch within 2^32 threads
+ * (else Q4_ERR_SHAPE).
+ */
+
+/*
+ * The first half of q4_moe_route, for any number of tokens: the k largest
+ * logits' ids and softmax gates.  T < 2^26.
+ */
+q4_status q4_moe_topk(const float* logits, int64_t ld, int64_t T, int32_t E, int32_t k,
+                      int32_t* topk_ids, float* topk_weights, void* stream);
+
+/*
+ * Gradient of the softmax gates for the router logits: with p = softmax of
+ * token t's logits and d[e] the sum of dweights[t][j] over the choices j with
+ * topk_ids[t][j] == e (ids outside 0 .. E-1 take no part),
+ *     dlogits[t][e] = p[e] * (d[e] - sum_e' p[e'] d[e']).
+ * A token whose logits are all -inf gets 0.  logits [T][ld], dlogits
+ * [T][lddl] fp32; topk_ids, dweights [T][k].  E <= 1024, 1 <= k <= 32.
+ */
+q4_status q4_moe_topk_backward(const float* logits, int64_t ld, int64_t T, int32_t E, int32_t k,
+                               const int32_t* topk_ids, const float* dweights, float* dlogits,
+                               int64_t lddl, void* stream);
+
+/*
+ * Tokens sorted by expert, for choices from any router and any number of
+ * tokens: a stable sort of topk_ids [T][k] (read as T*k choices in order) by
+ * expert.  Writes expert_offsets [E+1], gather (the token of each row) and inv
+ * [T][k] (the row of each choice), as q4_moe_route does for its own ids.  A
+ * choice with an id outside 0 .. E-1 is dropped (an expert of another rank, one
+ * over capacity): its inv is -1, it has no row, and gather's entries from
+ * expert_offsets[E] on are left as they were.  The same expert twice in a token
+ * gives two rows.  gather holds T*k entries.  1 <= E <= 1024, 1 <= k <= 32,
+ * T*k < 2^31.
+ */
+q4_status q4_moe_sort_workspace(int64_t T, int32_t k, int32_t E, size_t* bytes);
+q4_status q4_moe_sort(const int32_t* topk_ids, int64_t T, int32_t k, int32_t E,
+                      int32_t* expert_offsets, int32_t* gather, int32_t* inv, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
+ * The tokens' rows in expert order: xs[inv[t][j]] = x[t] for every choice with
+ * 0 <= inv[t][j] < P; other rows of xs are left as they were.  x_bf16 [T][ldx],
+ * xs_bf16 [P][ldxs], K % 8 == 0; no row may be named by two choices.  (The
+ * grouped products read tokens through gather by themselves; the copy is for
+ * sending rows to other ranks and for operators that want them in order.)
+ * Backward: dx[t] = bf16(sum_j dxs[inv[t][j]]), fp32 in choice order, 0 for a
+ * token without rows.
+ */
+q4_status q4_moe_permute(const void* x_bf16, int64_t ldx, const int32_t* inv, int64_t T, int32_t k,
+                         int64_t K, int64_t P, void* xs_bf16, int64_t ldxs, void* stream);
+q4_status q4_moe_permute_backward(const void* dxs_bf16, int64_t lddxs, const int32_t* inv, int64_t T,
+                                  int32_t k, int64_t K, int64_t P, void* dx_bf16, int64_t lddx,
+                                  void* stream);
+
+/*
+ * Gradients of q4_moe_combine: for every choice with 0 <= inv[t][j] < P
+ *     dy[inv[t][j]] = bf16(weights[t][j] * dout[t])
+ *     dweights[t][j] = sum_n dout[t][n] * y[inv[t][j]][n]      (fp32)
+ * and dweights[t][j] = 0 for the others; rows of dy that no choice names are
+ * left as they were.  dout_bf16 [T][ldo], y_bf16 [P][ldy], dy_bf16 [P][lddy],
+ * N % 8 == 0.  dweights may be NULL (gates without gradient); y is then not
+ * read and may be NULL too.
+ */
+q4_status q4_moe_combine_backward(const void* dout_bf16, int64_t ldo, const void* y_bf16, int64_t ldy,
+                                  const int32_t* inv, const float* weights, int64_t T, int32_t k,
+                                  int64_t N, int64_t P, void* dy_bf16, int64_t lddy, float* dweights,
+                                  void* stream);
+
+/*
+ * q4_swiglu that also saves its input in 8 bits for the backward pass, in the
+ * same pass over it: h as in q4_swiglu (exp and reciprocal in hardware
+ * precision: h may differ from q4_swiglu's in the last bf16 place) and gu_q
+ * (Q4_MXINT8 or Q4_MXFP8, [P][2I]) exactly what q4_quantize writes for gu.
+ * I % 32 == 0.
+ * Backward, with g, u the values gu_q stands for (or gu itself in bf16; exactly
+ * one of gu_bf16 / gu_q is given) and s = 1 / (1 + exp(-g)):
+ *     dgu[p][n]     = bf16(dh * u * s * (1 + g * (1 - s)))
+ *     dgu[p][I + n] = bf16(dh * g * s)
+ * and, if h_bf16 is not NULL, h = bf16(g * s * u) again (the down projection's
+ * input, so that it need not be kept).  I % 32 == 0 (8 with gu_bf16).
+ */
+q4_status q4_swiglu_save(const void* gu_bf16, int64_t ld_gu, int64_t P, int64_t I, void* h_bf16,
+                         int64_t ldh, const q4_tensor* gu_q, void* stream);
+q4_status q4_swiglu_backward(const void* gu_bf16, int64_t ld_gu, const q4_tensor* gu_q,
+                             const void* dh_bf16, int64_t lddh, int64_t P, int64_t I, void* dgu_bf16,
+                             int64_t lddgu, void* h_bf16, int64_t ldh, void* stream);
+
+/*
+ * Gradient of the W4 products for their activations:
+ *     dA[p][k] = sum_n dC[p][n] * w'[e*N + n][k]
+ * over the rows p of expert e (q4_gemm_dgrad: one dense weight, all rows).
+ * bf16 matrix cores, fp32 sums, bf16 output.  W: any weight format, either
+ * layout, as the forward call takes it; INT4 weights (with or without a zero
+ * point) are rounded to bf16 as in the forward products, MXFP4 and NVFP4 enter
+ * exactly.  dC_bf16 [P][lddc], dA_bf16 [P][ldda]; N % 8 == 0 (16 for the
+ * grouped call in the tiled layout), K % 128 == 0.  expert_offsets as in
+ * q4_grouped_gemm; rows of dA outside every expert's range are left as they
+ * were.  N == 0 writes zeros.
+ */
+q4_status q4_dgrad_workspace(int64_t P, int32_t E, int64_t N, int64_t K, size_t* bytes);
+q4_status q4_gemm_dgrad(int64_t M, const void* dC_bf16, int64_t lddc, const q4_tensor* W,
+                        void* dA_bf16, int64_t ldda, void* workspace, size_t workspace_bytes,
+                        void* stream);
+q4_status q4_grouped_gemm_dgrad(const void* dC_bf16, int64_t lddc, const int32_t* expert_offsets,
+                                int32_t E, int64_t P, const q4_tensor* W, int64_t N, void* dA_bf16,
+                                int64_t ldda, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of the products for the weight, from activations kept in bf16
+ * (A_bf16) or in 8 bits (A_q, Q4_MXINT8 or Q4_MXFP8; exactly one is given):
+ *     dW[e*N + n][k] (+)= sum over expert e's rows p of dC[p][n] * a[gather[p]][k]
+ * (q4_gemm_wgrad: one dense weight, all M rows, row p reads a[p]).  The 8-bit
+ * values enter the bf16 matrix cores exactly; fp32 sums.  dC_bf16 [P][lddc],
+ * A [T][lda] (gather NULL: row p reads a[p], T >= P; an index outside [0, T)
+ * reads zeros), dW [E*N][lddw] bf16 (dw_dtype 0) or fp32 (1), written whole:
+ * an expert without rows gets zeros.  accumulate != 0 (fp32 only, else
+ * Q4_ERR_FORMAT) adds to what dW holds.  N % 8 == 0, K % 8 == 0 (32 with A_q);
+ * dW 16-byte aligned, lddw a multiple of 8 (4 for fp32).
+ */
+q4_status q4_wgrad_workspace(int64_t P, int32_t E, int64_t N, int64_t K, size_t* bytes);
+q4_status q4_gemm_wgrad(int64_t M, const void* dC_bf16, int64_t lddc, const void* A_bf16, int64_t lda,
+                        const q4_tensor* A_q, int64_t N, int64_t K, void* dW, int dw_dtype,
+                        int64_t lddw, int accumulate, void* workspace, size_t workspace_bytes,
+                        void* stream);
+q4_status q4_grouped_gemm_wgrad(const void* dC_bf16, int64_t lddc, const void* A_bf16, int64_t lda,
+                                const q4_tensor* A_q, int64_t T, const int32_t* gather,
+                                const int32_t* expert_offsets, int32_t E, int64_t P, int64_t N,
+                                int64_t K, void* dW, int dw_dtype, int64_t lddw, int accumulate,
+                                void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Measurement helper, not a step of the method: reads `bytes` of device

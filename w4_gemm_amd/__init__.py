@@ -23,14 +23,15 @@ __all__ = [
     "lib", "q4_version", "q4_sizes", "q4_quantize", "q4_dequant", "q4_relayout", "relayout", "q4_gemv", "q4_gemm", "q4_gemm_quantized",
     "q4_grouped_gemm", "q4_grouped_gemm_swiglu", "q4_moe_route", "q4_swiglu", "q4_moe_combine",
     "moe_layer", "interleave_gate_up", "q4_read_probe", "q4_mfma_probe", "PROBE_KINDS", "PROBE_MIX_SINK",
-    "empty_q4", "quantize", "LIB_PATH",
+    "empty_q4", "quantize", "LIB_PATH", "MXFP8", "MXINT8",
 ]
 
-INT4_G128, MXFP4, NVFP4, FP8_ROW, INT4_ZP = 0, 1, 2, 3, 4
-FORMAT_NAMES = {"int4": INT4_G128, "mxfp4": MXFP4, "nvfp4": NVFP4, "fp8_row": FP8_ROW, "int4_zp": INT4_ZP}
+INT4_G128, MXFP4, NVFP4, FP8_ROW, INT4_ZP, MXFP8, MXINT8 = 0, 1, 2, 3, 4, 5, 6
+FORMAT_NAMES = {"int4": INT4_G128, "mxfp4": MXFP4, "nvfp4": NVFP4, "fp8_row": FP8_ROW, "int4_zp": INT4_ZP,
+                "mxfp8": MXFP8, "mxint8": MXINT8}
 LAYOUT_ROWS, LAYOUT_TILED = 0, 1
 LAYOUT_NAMES = {"rows": LAYOUT_ROWS, "tiled": LAYOUT_TILED}
-GROUP = {INT4_G128: 128, MXFP4: 32, NVFP4: 16, FP8_ROW: 16, INT4_ZP: 128}
+GROUP = {INT4_G128: 128, MXFP4: 32, NVFP4: 16, FP8_ROW: 16, INT4_ZP: 128, MXFP8: 32, MXINT8: 32}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libq4.so")
@@ -70,6 +71,7 @@ def _lib_handle():
         L = ctypes.CDLL(LIB_PATH)
         i64, vp, i32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32
         P = ctypes.POINTER(_Q4TensorC)
+        sz, SZ = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
         sig = {
             "q4_version": ([], ctypes.c_int),
             "q4_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -89,6 +91,23 @@ def _lib_handle():
             "q4_moe_route": ([vp, i64, i64, i32, i32, vp, vp, vp, vp, vp, vp], ctypes.c_int),
             "q4_swiglu": ([vp, i64, i64, i64, vp, i64, vp], ctypes.c_int),
             "q4_moe_combine": ([vp, i64, vp, vp, i64, i32, i64, vp, i64, vp], ctypes.c_int),
+            "q4_moe_topk": ([vp, i64, i64, i32, i32, vp, vp, vp], ctypes.c_int),
+            "q4_moe_topk_backward": ([vp, i64, i64, i32, i32, vp, vp, vp, i64, vp], ctypes.c_int),
+            "q4_moe_sort_workspace": ([i64, i32, i32, SZ], ctypes.c_int),
+            "q4_moe_sort": ([vp, i64, i32, i32, vp, vp, vp, vp, sz, vp], ctypes.c_int),
+            "q4_moe_permute": ([vp, i64, vp, i64, i32, i64, i64, vp, i64, vp], ctypes.c_int),
+            "q4_moe_permute_backward": ([vp, i64, vp, i64, i32, i64, i64, vp, i64, vp], ctypes.c_int),
+            "q4_moe_combine_backward": ([vp, i64, vp, i64, vp, vp, i64, i32, i64, i64, vp, i64, vp, vp], ctypes.c_int),
+            "q4_swiglu_save": ([vp, i64, i64, i64, vp, i64, P, vp], ctypes.c_int),
+            "q4_swiglu_backward": ([vp, i64, P, vp, i64, i64, i64, vp, i64, vp, i64, vp], ctypes.c_int),
+            "q4_dgrad_workspace": ([i64, i32, i64, i64, SZ], ctypes.c_int),
+            "q4_wgrad_workspace": ([i64, i32, i64, i64, SZ], ctypes.c_int),
+            "q4_gemm_dgrad": ([i64, vp, i64, P, vp, i64, vp, sz, vp], ctypes.c_int),
+            "q4_grouped_gemm_dgrad": ([vp, i64, vp, i32, i64, P, i64, vp, i64, vp, sz, vp], ctypes.c_int),
+            "q4_gemm_wgrad": ([i64, vp, i64, vp, i64, P, i64, i64, vp, ctypes.c_int, i64, ctypes.c_int, vp, sz, vp],
+                              ctypes.c_int),
+            "q4_grouped_gemm_wgrad": ([vp, i64, vp, i64, P, i64, vp, vp, i32, i64, i64, i64, vp, ctypes.c_int, i64,
+                                       ctypes.c_int, vp, sz, vp], ctypes.c_int),
             "q4_read_probe": ([vp, i64, vp, vp], ctypes.c_int),
             "q4_mfma_probe": ([ctypes.c_int32, i64, ctypes.c_uint32, vp, ctypes.POINTER(ctypes.c_double), vp],
                               ctypes.c_int),
@@ -197,6 +216,8 @@ class Q4Tensor:
     global_scale  NVFP4: float32 [1] (dequant multiplier); else None
     FP8_ROW (W4A8 activations): codes uint8 [rows, cols] E4M3 (flat when
       tiled), scales float32 [rows].
+    MXFP8, MXINT8 (saved activations, row-major only): codes uint8
+      [rows, cols], scales uint8 [rows, cols/32].
     """
     fmt: int
     rows: int
@@ -245,6 +266,9 @@ def empty_q4(fmt, rows: int, cols: int, device="cuda", layout=LAYOUT_ROWS) -> Q4
         return Q4Tensor(f, rows, cols, codes, torch.empty(rows, dtype=torch.float32, device=device),
                         None, lay)
     g = GROUP[f]
+    if f in (MXFP8, MXINT8):
+        return Q4Tensor(f, rows, cols, torch.empty((rows, cols), dtype=torch.uint8, device=device),
+                        torch.empty((rows, cols // g), dtype=torch.uint8, device=device), None, lay)
     sdt = torch.int16 if f == INT4_G128 else torch.int32 if f == INT4_ZP else torch.uint8
     if lay == LAYOUT_ROWS:
         codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=device)
@@ -557,3 +581,15 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, k: int, W_gu: Q4Tensor, W_d
     y = torch.empty((P, K), dtype=torch.bfloat16, device=x.device)
     q4_grouped_gemm(h, None, r.offsets, W_down, K, y, stream)
     return q4_moe_combine(y, r, stream=stream), r
+
+
+from .grad import (  # noqa: E402  (uses the helpers above)
+    MoESaved, moe_layer_backward, moe_layer_save, q4_gemm_dgrad, q4_gemm_wgrad, q4_grouped_gemm_dgrad,
+    q4_grouped_gemm_wgrad, q4_moe_combine_backward, q4_moe_permute, q4_moe_permute_backward, q4_moe_sort, q4_moe_topk,
+    q4_moe_topk_backward, q4_swiglu_backward, q4_swiglu_save)
+
+__all__ += [
+    "MoESaved", "moe_layer_backward", "moe_layer_save", "q4_gemm_dgrad", "q4_gemm_wgrad", "q4_grouped_gemm_dgrad",
+    "q4_grouped_gemm_wgrad", "q4_moe_combine_backward", "q4_moe_permute", "q4_moe_permute_backward", "q4_moe_sort",
+    "q4_moe_topk", "q4_moe_topk_backward", "q4_swiglu_backward", "q4_swiglu_save",
+]

@@ -12,6 +12,7 @@ namespace {
 thread_local int g_last_hip_error = 0;
 
 constexpr int64_t kMaxDim = (int64_t)1 << 31;  // kernels index rows/cols in int
+constexpr int64_t kMaxTopkTokens = (int64_t)1 << 26;  // a wave per token, within 2^32 threads
 
 int block_of(int fmt) {
   switch (fmt) {
@@ -20,9 +21,15 @@ int block_of(int fmt) {
     case Q4_NVFP4: return 16;
     case Q4_FP8_ROW: return 16;  // row-major rows are stored in 16-byte pieces
     case Q4_INT4_ZP_G128: return 128;
+    case Q4_MXFP8:
+    case Q4_MXINT8: return 32;
     default: return 0;
   }
 }
+
+// The saved-activation formats: row-major only, no operand of a W4 product.
+bool is_mx8(int fmt) { return fmt == Q4_MXFP8 || fmt == Q4_MXINT8; }
+bool is_weight(int fmt) { return fmt != Q4_FP8_ROW && !is_mx8(fmt); }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -39,6 +46,7 @@ q4_status check_tensor(const q4_tensor* t) {
   if (!t) return Q4_ERR_NULL;
   const int g = block_of(t->fmt);
   if (!g || (t->layout != Q4_LAYOUT_ROWS && t->layout != Q4_LAYOUT_TILED)) return Q4_ERR_FORMAT;
+  if (is_mx8(t->fmt) && t->layout != Q4_LAYOUT_ROWS) return Q4_ERR_FORMAT;
   if (t->rows < 0 || t->cols < 0 || t->rows >= kMaxDim || t->cols >= kMaxDim) return Q4_ERR_SHAPE;
   if (t->cols % (t->layout == Q4_LAYOUT_TILED ? 512 : g)) return Q4_ERR_SHAPE;
   if (t->fmt == Q4_NVFP4) {
@@ -74,13 +82,28 @@ q4_status check_out_bf16(const void* p, int64_t rows, int64_t cols, int64_t ld) 
   return Q4_OK;
 }
 
+// Token counts of the per-token kernels: a workgroup of up to 512 threads per
+// token, or one of 128 per token and 1024 columns, within 2^32 threads.
+q4_status check_tokens(int64_t T, int32_t k, int64_t cols) {
+  if (T < 0 || cols < 0 || T >= ((int64_t)1 << 23) || cols >= kMaxDim || k < 1 || k > 32) return Q4_ERR_SHAPE;
+  if (T * ((cols + 1023) / 1024) >= ((int64_t)1 << 25)) return Q4_ERR_SHAPE;
+  return cols % 8 ? Q4_ERR_SHAPE : Q4_OK;
+}
+
+// The arguments q4_gemm_dgrad and q4_grouped_gemm_dgrad share.
+q4_status dgrad(const void* dC, int64_t lddc, const int32_t* offsets, int32_t E, int64_t P, const q4_tensor* W,
+                int64_t N, void* dA, int64_t ldda, void* workspace, size_t workspace_bytes, void* stream);
+q4_status wgrad(const void* dC, int64_t lddc, const void* A_bf16, int64_t lda, const q4_tensor* A_q, int64_t T,
+                const int32_t* gather, const int32_t* offsets, int32_t E, int64_t P, int64_t N, int64_t K, void* dW,
+                int dw_dtype, int64_t lddw, int accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
 hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
 }  // namespace
 
 extern "C" {
 
-int q4_version(void) { return 102; }
+int q4_version(void) { return 103; }
 
 const char* q4_status_string(int status) {
   switch (status) {
@@ -100,6 +123,7 @@ q4_status q4_sizes(int fmt, int layout, int64_t rows, int64_t cols, size_t* code
                    size_t* scales_bytes) {
   const int g = block_of(fmt);
   if (!g || (layout != Q4_LAYOUT_ROWS && layout != Q4_LAYOUT_TILED)) return Q4_ERR_FORMAT;
+  if (is_mx8(fmt) && layout != Q4_LAYOUT_ROWS) return Q4_ERR_FORMAT;
   if (rows < 0 || cols < 0 || rows >= kMaxDim || cols >= kMaxDim) return Q4_ERR_SHAPE;
   if (cols % (layout == Q4_LAYOUT_TILED ? 512 : g)) return Q4_ERR_SHAPE;
   // the tiled layout stores whole 16-row tiles; per stored row both layouts
@@ -108,6 +132,11 @@ q4_status q4_sizes(int fmt, int layout, int64_t rows, int64_t cols, size_t* code
   if (fmt == Q4_FP8_ROW) {  // one byte per value, one fp32 scale per row
     if (codes_bytes) *codes_bytes = srows * (size_t)cols;
     if (scales_bytes) *scales_bytes = (size_t)rows * 4;
+    return Q4_OK;
+  }
+  if (is_mx8(fmt)) {  // one byte per value, one scale byte per 32
+    if (codes_bytes) *codes_bytes = srows * (size_t)cols;
+    if (scales_bytes) *scales_bytes = srows * (size_t)(cols / g);
     return Q4_OK;
   }
   if (codes_bytes) *codes_bytes = srows * (size_t)cols / 2;
@@ -129,6 +158,10 @@ q4_status q4_quantize(const void* src_bf16, int64_t ld, const q4_tensor* dst,
     return hip_status(q4::launch_fp8_rows_quantize(dst->layout, static_cast<const uint16_t*>(src_bf16), ld,
                                                    dst->rows, dst->cols, static_cast<uint8_t*>(dst->codes),
                                                    static_cast<float*>(dst->scales), as_stream(stream)));
+  if (is_mx8(dst->fmt))
+    return hip_status(q4::launch_mx8_quantize(dst->fmt, static_cast<const uint16_t*>(src_bf16), ld, dst->rows,
+                                              dst->cols, static_cast<uint8_t*>(dst->codes),
+                                              static_cast<uint8_t*>(dst->scales), as_stream(stream)));
   return hip_status(q4::launch_quantize(
       dst->fmt, dst->layout, static_cast<const uint16_t*>(src_bf16), ld, dst->rows, dst->cols,
       static_cast<uint8_t*>(dst->codes), dst->scales, dst->global_scale, nv_global_in,
@@ -147,6 +180,10 @@ q4_status q4_dequant(const q4_tensor* src, void* dst, int dst_dtype, int64_t ld,
     return hip_status(q4::launch_fp8_rows_dequant(src->layout, static_cast<const uint8_t*>(src->codes),
                                                   static_cast<const float*>(src->scales), src->rows,
                                                   src->cols, dst, dst_dtype, ld, as_stream(stream)));
+  if (is_mx8(src->fmt))
+    return hip_status(q4::launch_mx8_dequant(src->fmt, static_cast<const uint8_t*>(src->codes),
+                                             static_cast<const uint8_t*>(src->scales), src->rows, src->cols, dst,
+                                             dst_dtype, ld, as_stream(stream)));
   return hip_status(q4::launch_dequant(src->fmt, src->layout, static_cast<const uint8_t*>(src->codes),
                                        src->scales, src->global_scale, src->rows, src->cols, dst,
                                        dst_dtype, ld, as_stream(stream)));
@@ -157,7 +194,7 @@ q4_status q4_relayout(const q4_tensor* src, const q4_tensor* dst, void* stream) 
   if (st != Q4_OK) return st;
   st = check_tensor(dst);
   if (st != Q4_OK) return st;
-  if (src->fmt != dst->fmt || src->fmt == Q4_FP8_ROW) return Q4_ERR_FORMAT;
+  if (src->fmt != dst->fmt || !is_weight(src->fmt)) return Q4_ERR_FORMAT;
   if (src->rows != dst->rows || src->cols != dst->cols) return Q4_ERR_SHAPE;
   hipStream_t s = as_stream(stream);
   if (src->fmt == Q4_NVFP4 && (src->rows == 0 || src->cols == 0 || src->layout == dst->layout)) {
@@ -182,7 +219,7 @@ q4_status q4_gemv(const q4_tensor* W, const void* x_bf16, int64_t B, int64_t ldx
                   int64_t ldy, void* stream) {
   q4_status st = check_tensor(W);
   if (st != Q4_OK) return st;
-  if (W->fmt == Q4_FP8_ROW) return Q4_ERR_FORMAT;
+  if (!is_weight(W->fmt)) return Q4_ERR_FORMAT;
   if (B < 0 || B > 16) return Q4_ERR_SHAPE;
   if (W->cols % 128) return Q4_ERR_SHAPE;
   if (B == 0 || W->rows == 0) return Q4_OK;
@@ -201,7 +238,7 @@ q4_status q4_gemm(int64_t M, const void* A_bf16, int64_t lda, const q4_tensor* A
                   const q4_tensor* W, void* C_bf16, int64_t ldc, void* stream) {
   q4_status st = check_tensor(W);
   if (st != Q4_OK) return st;
-  if (W->fmt == Q4_FP8_ROW) return Q4_ERR_FORMAT;
+  if (!is_weight(W->fmt)) return Q4_ERR_FORMAT;
   if (M < 0 || M >= kMaxDim || M > (int64_t)65535 * 64) return Q4_ERR_SHAPE;
   if ((A_bf16 == nullptr) == (A_q == nullptr)) return A_bf16 ? Q4_ERR_FORMAT : Q4_ERR_NULL;
   const int64_t N = W->rows, K = W->cols;
@@ -251,7 +288,7 @@ q4_status q4_gemm_quantized(int64_t M, const void* A_bf16, int64_t lda, const q4
   if (st != Q4_OK) return st;
   st = check_tensor(C_q);
   if (st != Q4_OK) return st;
-  if (W->fmt == Q4_FP8_ROW || W->layout != Q4_LAYOUT_TILED) return Q4_ERR_FORMAT;
+  if (!is_weight(W->fmt) || W->layout != Q4_LAYOUT_TILED) return Q4_ERR_FORMAT;
   if (C_q->fmt != Q4_MXFP4 && C_q->fmt != Q4_NVFP4) return Q4_ERR_FORMAT;
   if (C_q->fmt == Q4_NVFP4) {
     if (!nv_global_in) return Q4_ERR_NULL;
@@ -295,7 +332,7 @@ q4_status q4_grouped_gemm(const void* A_bf16, int64_t lda, int64_t T, const int3
                           void* stream) {
   q4_status st = check_tensor(W);
   if (st != Q4_OK) return st;
-  if (W->fmt == Q4_FP8_ROW) return Q4_ERR_FORMAT;
+  if (!is_weight(W->fmt)) return Q4_ERR_FORMAT;
   if (E < 0 || E > 65535 || N < 0 || T < 0 || P < 0 || P >= kMaxDim || T >= kMaxDim)
     return Q4_ERR_SHAPE;
   if (W->rows != (int64_t)E * N) return Q4_ERR_SHAPE;
@@ -323,7 +360,7 @@ q4_status q4_grouped_gemm_swiglu(const void* A_bf16, int64_t lda, int64_t T, con
                                  int64_t I, void* H_bf16, int64_t ldh, void* stream) {
   q4_status st = check_tensor(W);
   if (st != Q4_OK) return st;
-  if (W->fmt == Q4_FP8_ROW || W->layout != Q4_LAYOUT_TILED) return Q4_ERR_FORMAT;
+  if (!is_weight(W->fmt) || W->layout != Q4_LAYOUT_TILED) return Q4_ERR_FORMAT;
   if (E < 0 || E > 65535 || I < 0 || T < 0 || P < 0 || P >= kMaxDim || T >= kMaxDim) return Q4_ERR_SHAPE;
   if (I % 16 || W->rows != (int64_t)E * 2 * I) return Q4_ERR_SHAPE;
   const int64_t K = W->cols;
@@ -415,4 +452,291 @@ q4_status q4_read_probe(const void* src, int64_t bytes, uint32_t* sink, void* st
   return hip_status(q4::launch_read_probe(static_cast<const uint8_t*>(src), bytes, sink, as_stream(stream)));
 }
 
+q4_status q4_moe_topk(const float* logits, int64_t ld, int64_t T, int32_t E, int32_t k, int32_t* topk_ids,
+                      float* topk_weights, void* stream) {
+  if (T < 0 || T >= kMaxTopkTokens || E < 1 || E > 1024 || k < 1 || k > 32 || k > E) return Q4_ERR_SHAPE;
+  if (T == 0) return Q4_OK;
+  if (!logits || !topk_ids || !topk_weights) return Q4_ERR_NULL;
+  if (ld < E) return Q4_ERR_SHAPE;
+  if (!aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4)) return Q4_ERR_ALIGN;
+  return hip_status(q4::launch_moe_topk(logits, ld, T, E, k, topk_ids, topk_weights, as_stream(stream)));
+}
+
+q4_status q4_moe_topk_backward(const float* logits, int64_t ld, int64_t T, int32_t E, int32_t k,
+                               const int32_t* topk_ids, const float* dweights, float* dlogits, int64_t lddl,
+                               void* stream) {
+  if (T < 0 || T >= kMaxTopkTokens || E < 1 || E > 1024 || k < 1 || k > 32) return Q4_ERR_SHAPE;
+  if (T == 0) return Q4_OK;
+  if (!logits || !topk_ids || !dweights || !dlogits) return Q4_ERR_NULL;
+  if (ld < E || lddl < E) return Q4_ERR_SHAPE;
+  if (!aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(dweights, 4) || !aligned(dlogits, 4))
+    return Q4_ERR_ALIGN;
+  return hip_status(q4::launch_moe_topk_backward(logits, ld, T, E, k, topk_ids, dweights, dlogits, lddl,
+                                                 as_stream(stream)));
+}
+
+q4_status q4_moe_sort_workspace(int64_t T, int32_t k, int32_t E, size_t* bytes) {
+  if (!bytes) return Q4_ERR_NULL;
+  if (T < 0 || T >= kMaxDim || E < 1 || E > 1024 || k < 1 || k > 32 || T * k >= kMaxDim) return Q4_ERR_SHAPE;
+  *bytes = q4::moe_sort_workspace(T * k, E);
+  return Q4_OK;
+}
+
+q4_status q4_moe_sort(const int32_t* topk_ids, int64_t T, int32_t k, int32_t E, int32_t* expert_offsets,
+                      int32_t* gather, int32_t* inv, void* workspace, size_t workspace_bytes, void* stream) {
+  size_t need = 0;
+  const q4_status st = q4_moe_sort_workspace(T, k, E, &need);
+  if (st != Q4_OK) return st;
+  if (!expert_offsets || (T > 0 && (!topk_ids || !gather || !inv)) || (need && !workspace)) return Q4_ERR_NULL;
+  if (workspace_bytes < need) return Q4_ERR_SHAPE;
+  if (!aligned(expert_offsets, 4) || !aligned(topk_ids, 4) || !aligned(gather, 4) || !aligned(inv, 4) ||
+      (need && !aligned(workspace, 4)))
+    return Q4_ERR_ALIGN;
+  return hip_status(q4::launch_moe_sort(topk_ids, T, k, E, expert_offsets, gather, inv,
+                                        static_cast<uint32_t*>(workspace), as_stream(stream)));
+}
+
+q4_status q4_moe_permute(const void* x_bf16, int64_t ldx, const int32_t* inv, int64_t T, int32_t k, int64_t K,
+                         int64_t P, void* xs_bf16, int64_t ldxs, void* stream) {
+  q4_status st = check_tokens(T, k, K);
+  if (st != Q4_OK) return st;
+  if (P < 0 || P >= kMaxDim) return Q4_ERR_SHAPE;
+  if (T == 0 || K == 0 || P == 0) return Q4_OK;
+  if (!inv) return Q4_ERR_NULL;
+  if (!aligned(inv, 4)) return Q4_ERR_ALIGN;
+  st = check_bf16(x_bf16, T, K, ldx);
+  if (st != Q4_OK) return st;
+  st = check_bf16(xs_bf16, P, K, ldxs);
+  if (st != Q4_OK) return st;
+  return hip_status(q4::launch_moe_permute(static_cast<const uint16_t*>(x_bf16), ldx, inv, T, k, K, P,
+                                           static_cast<uint16_t*>(xs_bf16), ldxs, as_stream(stream)));
+}
+
+q4_status q4_moe_permute_backward(const void* dxs_bf16, int64_t lddxs, const int32_t* inv, int64_t T, int32_t k,
+                                  int64_t K, int64_t P, void* dx_bf16, int64_t lddx, void* stream) {
+  q4_status st = check_tokens(T, k, K);
+  if (st != Q4_OK) return st;
+  if (P < 0 || P >= kMaxDim) return Q4_ERR_SHAPE;
+  if (T == 0 || K == 0) return Q4_OK;
+  if (!inv) return Q4_ERR_NULL;
+  if (!aligned(inv, 4)) return Q4_ERR_ALIGN;
+  st = check_bf16(dxs_bf16, P, K, lddxs);
+  if (st != Q4_OK) return st;
+  st = check_bf16(dx_bf16, T, K, lddx);
+  if (st != Q4_OK) return st;
+  return hip_status(q4::launch_moe_permute_backward(static_cast<const uint16_t*>(dxs_bf16), lddxs, inv, T, k, K, P,
+                                                    static_cast<uint16_t*>(dx_bf16), lddx, as_stream(stream)));
+}
+
+q4_status q4_moe_combine_backward(const void* dout_bf16, int64_t ldo, const void* y_bf16, int64_t ldy,
+                                  const int32_t* inv, const float* weights, int64_t T, int32_t k, int64_t N,
+                                  int64_t P, void* dy_bf16, int64_t lddy, float* dweights, void* stream) {
+  q4_status st = check_tokens(T, k, N);
+  if (st != Q4_OK) return st;
+  if (P < 0 || P >= kMaxDim) return Q4_ERR_SHAPE;
+  if (T == 0) return Q4_OK;
+  if (!inv || !weights) return Q4_ERR_NULL;
+  if (!aligned(inv, 4) || !aligned(weights, 4) || !aligned(dweights, 4)) return Q4_ERR_ALIGN;
+  st = check_bf16(dout_bf16, T, N, ldo);
+  if (st != Q4_OK) return st;
+  st = check_bf16(dy_bf16, P, N, lddy);
+  if (st != Q4_OK) return st;
+  if (dweights) {
+    st = check_bf16(y_bf16, P, N, ldy);
+    if (st != Q4_OK) return st;
+  }
+  return hip_status(q4::launch_moe_combine_backward(static_cast<const uint16_t*>(dout_bf16), ldo,
+                                                    static_cast<const uint16_t*>(y_bf16), ldy, inv, weights, T, k, N,
+                                                    P, static_cast<uint16_t*>(dy_bf16), lddy, dweights,
+                                                    as_stream(stream)));
+}
+
+q4_status q4_swiglu_save(const void* gu_bf16, int64_t ld_gu, int64_t P, int64_t I, void* h_bf16, int64_t ldh,
+                         const q4_tensor* gu_q, void* stream) {
+  q4_status st = check_tensor(gu_q);
+  if (st != Q4_OK) return st;
+  if (!is_mx8(gu_q->fmt)) return Q4_ERR_FORMAT;
+  if (P < 0 || I < 0 || P >= kMaxDim || I >= kMaxDim / 2 || I % 32) return Q4_ERR_SHAPE;
+  if (gu_q->rows != P || gu_q->cols != 2 * I) return Q4_ERR_SHAPE;
+  if (P == 0 || I == 0) return Q4_OK;
+  st = check_bf16(gu_bf16, P, 2 * I, ld_gu);
+  if (st != Q4_OK) return st;
+  st = check_bf16(h_bf16, P, I, ldh);
+  if (st != Q4_OK) return st;
+  return hip_status(q4::launch_swiglu_save(gu_q->fmt, static_cast<const uint16_t*>(gu_bf16), ld_gu, P, I,
+                                           static_cast<uint16_t*>(h_bf16), ldh, static_cast<uint8_t*>(gu_q->codes),
+                                           static_cast<uint8_t*>(gu_q->scales), as_stream(stream)));
+}
+
+q4_status q4_swiglu_backward(const void* gu_bf16, int64_t ld_gu, const q4_tensor* gu_q, const void* dh_bf16,
+                             int64_t lddh, int64_t P, int64_t I, void* dgu_bf16, int64_t lddgu, void* h_bf16,
+                             int64_t ldh, void* stream) {
+  q4_status st;
+  if ((gu_bf16 == nullptr) == (gu_q == nullptr)) return gu_bf16 ? Q4_ERR_FORMAT : Q4_ERR_NULL;
+  if (P < 0 || I < 0 || P >= kMaxDim || I >= kMaxDim / 2 || I % (gu_q ? 32 : 8)) return Q4_ERR_SHAPE;
+  if (gu_q) {
+    st = check_tensor(gu_q);
+    if (st != Q4_OK) return st;
+    if (!is_mx8(gu_q->fmt)) return Q4_ERR_FORMAT;
+    if (gu_q->rows != P || gu_q->cols != 2 * I) return Q4_ERR_SHAPE;
+  }
+  if (P == 0 || I == 0) return Q4_OK;
+  if (!gu_q) {
+    st = check_bf16(gu_bf16, P, 2 * I, ld_gu);
+    if (st != Q4_OK) return st;
+  }
+  st = check_bf16(dh_bf16, P, I, lddh);
+  if (st != Q4_OK) return st;
+  st = check_bf16(dgu_bf16, P, 2 * I, lddgu);
+  if (st != Q4_OK) return st;
+  if (h_bf16) {
+    st = check_bf16(h_bf16, P, I, ldh);
+    if (st != Q4_OK) return st;
+  }
+  return hip_status(q4::launch_swiglu_backward(
+      gu_q ? gu_q->fmt : 0, gu_q ? gu_q->codes : gu_bf16, gu_q ? static_cast<const uint8_t*>(gu_q->scales) : nullptr,
+      ld_gu, P, I, static_cast<const uint16_t*>(dh_bf16), lddh, static_cast<uint16_t*>(dgu_bf16), lddgu,
+      static_cast<uint16_t*>(h_bf16), ldh, as_stream(stream)));
+}
+
+q4_status q4_dgrad_workspace(int64_t P, int32_t E, int64_t N, int64_t K, size_t* bytes) {
+  if (!bytes) return Q4_ERR_NULL;
+  if (P < 0 || E < 0 || E > 65535 || N < 0 || K < 0 || P >= kMaxDim || N >= kMaxDim || K >= kMaxDim)
+    return Q4_ERR_SHAPE;
+  *bytes = P && E && K ? q4::dgrad_workspace(P, E, N, K) : 0;
+  return Q4_OK;
+}
+
+q4_status q4_wgrad_workspace(int64_t P, int32_t E, int64_t N, int64_t K, size_t* bytes) {
+  if (!bytes) return Q4_ERR_NULL;
+  if (P < 0 || E < 0 || E > 65535 || N < 0 || K < 0 || P >= kMaxDim || N >= kMaxDim || K >= kMaxDim)
+    return Q4_ERR_SHAPE;
+  *bytes = E && N && K ? q4::wgrad_workspace(P, E, N, K) : 0;
+  return Q4_OK;
+}
+
+q4_status q4_gemm_dgrad(int64_t M, const void* dC_bf16, int64_t lddc, const q4_tensor* W, void* dA_bf16, int64_t ldda,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  if (!W) return Q4_ERR_NULL;
+  return dgrad(dC_bf16, lddc, nullptr, 1, M, W, W->rows, dA_bf16, ldda, workspace, workspace_bytes, stream);
+}
+
+q4_status q4_grouped_gemm_dgrad(const void* dC_bf16, int64_t lddc, const int32_t* expert_offsets, int32_t E, int64_t P,
+                                const q4_tensor* W, int64_t N, void* dA_bf16, int64_t ldda, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  if (E > 0 && P > 0 && !expert_offsets) return Q4_ERR_NULL;
+  return dgrad(dC_bf16, lddc, expert_offsets, E, P, W, N, dA_bf16, ldda, workspace, workspace_bytes, stream);
+}
+
+q4_status q4_gemm_wgrad(int64_t M, const void* dC_bf16, int64_t lddc, const void* A_bf16, int64_t lda,
+                        const q4_tensor* A_q, int64_t N, int64_t K, void* dW, int dw_dtype, int64_t lddw,
+                        int accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+  return wgrad(dC_bf16, lddc, A_bf16, lda, A_q, M, nullptr, nullptr, 1, M, N, K, dW, dw_dtype, lddw, accumulate,
+               workspace, workspace_bytes, stream);
+}
+
+q4_status q4_grouped_gemm_wgrad(const void* dC_bf16, int64_t lddc, const void* A_bf16, int64_t lda,
+                                const q4_tensor* A_q, int64_t T, const int32_t* gather, const int32_t* expert_offsets,
+                                int32_t E, int64_t P, int64_t N, int64_t K, void* dW, int dw_dtype, int64_t lddw,
+                                int accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+  if (E > 0 && !expert_offsets) return Q4_ERR_NULL;
+  return wgrad(dC_bf16, lddc, A_bf16, lda, A_q, T, gather, expert_offsets, E, P, N, K, dW, dw_dtype, lddw, accumulate,
+               workspace, workspace_bytes, stream);
+}
+
 }  // extern "C"
+
+namespace {
+
+q4_status dgrad(const void* dC, int64_t lddc, const int32_t* offsets, int32_t E, int64_t P, const q4_tensor* W,
+                int64_t N, void* dA, int64_t ldda, void* workspace, size_t workspace_bytes, void* stream) {
+  q4_status st = check_tensor(W);
+  if (st != Q4_OK) return st;
+  if (!is_weight(W->fmt)) return Q4_ERR_FORMAT;
+  size_t need = 0;
+  const int64_t K = W->cols;
+  st = q4_dgrad_workspace(P, E, N, K, &need);
+  if (st != Q4_OK) return st;
+  if (W->rows != (int64_t)E * N || N % 8 || K % 128) return Q4_ERR_SHAPE;
+  if (offsets && W->layout == Q4_LAYOUT_TILED && N % 16) return Q4_ERR_SHAPE;  // experts own whole tiles
+  if (E == 0 || P == 0 || K == 0) return Q4_OK;
+  if (!q4::dgrad_fits(P, E, N, K)) return Q4_ERR_SHAPE;
+  if (!aligned(offsets, 4)) return Q4_ERR_ALIGN;
+  st = check_bf16(dC, P, N, lddc);
+  if (st != Q4_OK) return st;
+  st = check_bf16(dA, P, K, ldda);
+  if (st != Q4_OK) return st;
+  if (need && !workspace) return Q4_ERR_NULL;
+  if (workspace_bytes < need) return Q4_ERR_SHAPE;
+  if (need && !aligned(workspace, 16)) return Q4_ERR_ALIGN;
+  q4::GradArgs g{};
+  g.dc = static_cast<const uint16_t*>(dC);
+  g.lddc = lddc;
+  g.offsets = offsets;
+  g.E = E;
+  g.P = P;
+  g.N = N;
+  g.K = K;
+  g.b = static_cast<const uint8_t*>(W->codes);
+  g.b_scales = static_cast<const uint8_t*>(W->scales);
+  g.gs = W->global_scale;
+  g.out = dA;
+  g.ldo = ldda;
+  g.workspace = static_cast<float*>(workspace);
+  return hip_status(q4::launch_dgrad(W->fmt, W->layout, g, as_stream(stream)));
+}
+
+q4_status wgrad(const void* dC, int64_t lddc, const void* A_bf16, int64_t lda, const q4_tensor* A_q, int64_t T,
+                const int32_t* gather, const int32_t* offsets, int32_t E, int64_t P, int64_t N, int64_t K, void* dW,
+                int dw_dtype, int64_t lddw, int accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+  size_t need = 0;
+  q4_status st = q4_wgrad_workspace(P, E, N, K, &need);
+  if (st != Q4_OK) return st;
+  if (dw_dtype != 0 && dw_dtype != 1) return Q4_ERR_FORMAT;
+  if (accumulate && dw_dtype != 1) return Q4_ERR_FORMAT;
+  if ((A_bf16 == nullptr) == (A_q == nullptr)) return A_bf16 ? Q4_ERR_FORMAT : Q4_ERR_NULL;
+  if (T < 0 || T >= kMaxDim || N % 8 || K % (A_q ? 32 : 8)) return Q4_ERR_SHAPE;
+  if (A_q) {
+    st = check_tensor(A_q);
+    if (st != Q4_OK) return st;
+    if (!is_mx8(A_q->fmt)) return Q4_ERR_FORMAT;
+    if (A_q->rows != T || A_q->cols != K) return Q4_ERR_SHAPE;
+  }
+  if (E == 0 || N == 0 || K == 0) return Q4_OK;
+  if (!q4::wgrad_fits(P, E, N, K)) return Q4_ERR_SHAPE;
+  if (!gather && T < P) return Q4_ERR_SHAPE;  // row p of dC goes with row p of A
+  if (!aligned(gather, 4) || !aligned(offsets, 4)) return Q4_ERR_ALIGN;
+  st = check_bf16(dC, P, N, lddc);
+  if (st != Q4_OK) return st;
+  if (!A_q) {
+    st = check_bf16(A_bf16, T, K, lda);
+    if (st != Q4_OK) return st;
+  }
+  if (!dW) return Q4_ERR_NULL;
+  if (lddw < K) return Q4_ERR_SHAPE;
+  if (!aligned(dW, 16) || lddw % (dw_dtype ? 4 : 8)) return Q4_ERR_ALIGN;
+  if (need && !workspace) return Q4_ERR_NULL;
+  if (workspace_bytes < need) return Q4_ERR_SHAPE;
+  if (need && !aligned(workspace, 16)) return Q4_ERR_ALIGN;
+  q4::GradArgs g{};
+  g.dc = static_cast<const uint16_t*>(dC);
+  g.lddc = lddc;
+  g.offsets = offsets;
+  g.gather = gather;
+  g.E = E;
+  g.P = P;
+  g.N = N;
+  g.K = K;
+  g.T = T;
+  g.b = static_cast<const uint8_t*>(A_q ? A_q->codes : A_bf16);
+  g.b_scales = A_q ? static_cast<const uint8_t*>(A_q->scales) : nullptr;
+  g.ldb = lda;
+  g.out = dW;
+  g.ldo = lddw;
+  g.out_f32 = dw_dtype;
+  g.accumulate = accumulate;
+  g.workspace = static_cast<float*>(workspace);
+  return hip_status(q4::launch_wgrad(A_q ? A_q->fmt : 7, g, as_stream(stream)));
+}
+
+}  // namespace

@@ -227,8 +227,9 @@ swiglu_kernel(const uint16_t* __restrict__ gu, int64_t ld_gu, int64_t P, int64_t
   }
 }
 
-// out[t][n] = bf16(sum_j w[t][j] * y[inv[t][j]][n]), fp32 in choice order;
-// one workgroup per (token, 2048-column slice), 8 columns per thread.
+// out[t][n] = bf16(sum_j w[t][j] * y[inv[t][j]][n]), fp32 in choice order,
+// without the choices that were dropped (inv < 0); one workgroup per (token,
+// 2048-column slice), 8 columns per thread.
 __global__ void __launch_bounds__(kThreads)
 moe_combine_kernel(const uint16_t* __restrict__ y, int64_t ldy, const int32_t* __restrict__ inv,
                    const float* __restrict__ w, int k, int64_t N, uint16_t* __restrict__ out,
@@ -240,6 +241,7 @@ moe_combine_kernel(const uint16_t* __restrict__ y, int64_t ldy, const int32_t* _
   float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   for (int j = 0; j < k; ++j) {
     const int64_t p = inv[t * k + j];
+    if (p < 0) continue;
     const float g = w[t * k + j];
     const uint4 v = *reinterpret_cast<const uint4*>(y + p * ldy + n0);
     const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
@@ -261,16 +263,22 @@ size_t moe_dispatch_lds_bytes(int64_t T, int32_t E) {
   return (size_t)4 * (2 * (size_t)E + 2 * (size_t)E * (size_t)((T + 31) / 32));
 }
 
+hipError_t launch_moe_topk(const float* logits, int64_t ld, int64_t T, int32_t E, int32_t k, int32_t* ids,
+                           float* weights, hipStream_t stream) {
+  if (T == 0) return hipSuccess;
+  const unsigned grid = (unsigned)((T + kRouteWaves - 1) / kRouteWaves);
+  if (E <= 64)
+    moe_topk64_kernel<<<grid, 64 * kRouteWaves, 0, stream>>>(logits, ld, (int)T, E, k, ids, weights);
+  else
+    moe_topk_kernel<<<grid, 64 * kRouteWaves, 0, stream>>>(logits, ld, (int)T, E, k, ids, weights);
+  return hipGetLastError();
+}
+
 hipError_t launch_moe_route(const float* logits, int64_t ld, int64_t T, int32_t E, int32_t k,
                             int32_t* ids, float* weights, int32_t* offsets, int32_t* gather,
                             int32_t* inv, hipStream_t stream) {
-  if (T > 0) {
-    const unsigned grid = (unsigned)((T + kRouteWaves - 1) / kRouteWaves);
-    if (E <= 64)
-      moe_topk64_kernel<<<grid, 64 * kRouteWaves, 0, stream>>>(logits, ld, (int)T, E, k, ids, weights);
-    else
-      moe_topk_kernel<<<grid, 64 * kRouteWaves, 0, stream>>>(logits, ld, (int)T, E, k, ids, weights);
-  }
+  const hipError_t topk = launch_moe_topk(logits, ld, T, E, k, ids, weights, stream);
+  if (topk != hipSuccess) return topk;
   const size_t lds = moe_dispatch_lds_bytes(T, E);
   const hipError_t attr = set_max_lds<&moe_dispatch_kernel>(kMoeDispatchMaxLds);
   if (attr != hipSuccess) return attr;

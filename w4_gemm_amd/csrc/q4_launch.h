@@ -162,4 +162,67 @@ hipError_t launch_grouped(int fmt, int layout, const uint16_t* A, int64_t lda, i
                           const uint8_t* codes, const void* scales, const float* gs, int64_t N,
                           int64_t K, uint16_t* C, int64_t ldc, hipStream_t stream);
 
+// ---- saved activations and gradients ----------------------------------------
+
+// The 8-bit block formats (fmt 5 MXFP8, 6 MXINT8), row-major, cols % 32 == 0.
+hipError_t launch_mx8_quantize(int fmt, const uint16_t* src, int64_t ld, int64_t rows, int64_t cols, uint8_t* codes,
+                               uint8_t* scales, hipStream_t stream);
+hipError_t launch_mx8_dequant(int fmt, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                              void* dst, int dst_dtype, int64_t ld, hipStream_t stream);
+
+// SwiGLU that also saves gu [P][2I] in 8 bits, and its gradient from what was
+// saved (fmt 5, 6) or from gu in bf16 (fmt 0); h may be NULL there.  I % 32 == 0
+// (8 for bf16).
+hipError_t launch_swiglu_save(int fmt, const uint16_t* gu, int64_t ld_gu, int64_t P, int64_t I, uint16_t* h,
+                              int64_t ldh, uint8_t* codes, uint8_t* scales, hipStream_t stream);
+hipError_t launch_swiglu_backward(int fmt, const void* gu, const uint8_t* scales, int64_t ld_gu, int64_t P, int64_t I,
+                                  const uint16_t* dh, int64_t lddh, uint16_t* dgu, int64_t lddgu, uint16_t* h,
+                                  int64_t ldh, hipStream_t stream);
+
+// The first half of launch_moe_route: ids and gates alone.
+hipError_t launch_moe_topk(const float* logits, int64_t ld, int64_t T, int32_t E, int32_t k, int32_t* ids,
+                           float* weights, hipStream_t stream);
+hipError_t launch_moe_topk_backward(const float* logits, int64_t ld, int64_t T, int32_t E, int32_t k,
+                                    const int32_t* ids, const float* dw, float* dl, int64_t lddl, hipStream_t stream);
+
+// Bytes of workspace of launch_moe_sort for P = T * k choices (0 for few).
+size_t moe_sort_workspace(int64_t P, int32_t E);
+hipError_t launch_moe_sort(const int32_t* ids, int64_t T, int32_t k, int32_t E, int32_t* offsets, int32_t* gather,
+                           int32_t* inv, uint32_t* workspace, hipStream_t stream);
+hipError_t launch_moe_permute(const uint16_t* x, int64_t ldx, const int32_t* inv, int64_t T, int32_t k, int64_t K,
+                              int64_t P, uint16_t* xs, int64_t ldxs, hipStream_t stream);
+hipError_t launch_moe_permute_backward(const uint16_t* dxs, int64_t lddxs, const int32_t* inv, int64_t T, int32_t k,
+                                       int64_t K, int64_t P, uint16_t* dx, int64_t lddx, hipStream_t stream);
+// dw NULL: the gates' gradient is not wanted (y is not read).
+hipError_t launch_moe_combine_backward(const uint16_t* dout, int64_t ldo, const uint16_t* y, int64_t ldy,
+                                       const int32_t* inv, const float* w, int64_t T, int32_t k, int64_t N, int64_t P,
+                                       uint16_t* dy, int64_t lddy, float* dw, hipStream_t stream);
+
+// The gradient products of gemm_grad.hip.  offsets NULL: one expert with all P
+// rows.  dgrad: b is the weight [E*N][K]; wgrad: the activations [T][K], read
+// through gather (NULL: row p).  N % 8 == 0, K % 32 == 0.
+struct GradArgs {
+  const uint16_t* dc;       // [P][lddc], N columns
+  int64_t lddc;
+  const int32_t* offsets;   // [E + 1] or NULL
+  const int32_t* gather;    // [P] or NULL (wgrad)
+  int32_t E;
+  int64_t P, N, K, T;
+  const uint8_t* b;         // codes, or the bf16 activations
+  const uint8_t* b_scales;
+  const float* gs;          // NVFP4 weights
+  int64_t ldb;              // bf16 activations
+  void* out;                // dgrad: bf16 [P][ldo]; wgrad: fp32 or bf16 [E*N][ldo]
+  int64_t ldo;
+  int out_f32, accumulate;
+  float* workspace;
+};
+size_t dgrad_workspace(int64_t P, int32_t E, int64_t N, int64_t K);
+size_t wgrad_workspace(int64_t P, int32_t E, int64_t N, int64_t K);
+// whether the launch stays within 2^32 threads
+bool dgrad_fits(int64_t P, int32_t E, int64_t N, int64_t K);
+bool wgrad_fits(int64_t P, int32_t E, int64_t N, int64_t K);
+hipError_t launch_dgrad(int fmt, int layout, const GradArgs& g, hipStream_t stream);
+hipError_t launch_wgrad(int kind, const GradArgs& g, hipStream_t stream);   // kind 5, 6 or 7 (bf16)
+
 }  // namespace q4
