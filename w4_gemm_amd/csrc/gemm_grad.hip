@@ -5,169 +5,406 @@
 //   wgrad  dW_e[n][k] = sum_{p in e} dC[p][n] a[gather[p]][k]
 //
 // Both are bf16 matrix products (v_mfma_f32_16x16x32_bf16, fp32 sums) whose
-// second operand -- the 4-bit weight, the saved activation -- is stored with
-// the summed index as its rows, so its fragments are read column-wise from
-// bf16 rows in LDS (q4_piece.h converts it once per workgroup).
+// second operand B -- the 4-bit weight, the saved activation -- is stored with
+// the summed index as its rows; in wgrad so is the first operand A = dC.
+//
+//   * B is converted once per workgroup: a thread loads 32 columns of one row
+//     (q4_piece.h), converts them to bf16 and writes them to LDS as rows; the
+//     fragments are read column-wise from there by ds_read_b64_tr_b16, which
+//     hands lane i of 16 the column i of four rows.  A transposes the same way
+//     in wgrad; in dgrad its rows hold the summed index already.
+//   * A goes to LDS by direct copies (buffer loads to LDS: unlike global_load_lds
+//     they leave the compiler's load counts exact, so that B's loads are not
+//     waited for as a whole).  Rows and columns past the sum's end are filled
+//     with zeros by the buffer's range check, so that whatever B holds there
+//     (clamped to existing rows) adds nothing.
+//   * The 16-byte chunks of an LDS row are permuted (XOR with bits of the row)
+//     so that the 16 or 32 lanes that LDS serves at once never meet on a bank.
+//   * A workgroup of kWM x kWK waves makes a block of C of 16 kMT kWM rows by
+//     256 columns and takes R = 8 kWM kWK summed rows per stage (one piece of B
+//     per thread).  A is copied two stages ahead (three buffers), B is loaded
+//     into registers two stages ahead and converted one ahead (two buffers).
 #include "q4_launch.h"
+#include "q4_lds.h"
 #include "q4_piece.h"
+
+#include <type_traits>
 
 namespace q4 {
 namespace {
 
-constexpr int kT = 64;        // tile of C: 64 x 64, a wave 32 x 32 of it
-constexpr int kR = 32;        // summed rows per stage
-constexpr int kPad = 8;
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4_t* trptr_t;
+typedef const __attribute__((address_space(3))) u32x4_t* u32x4_lds_t;
+
+constexpr int kBK = 256;              // columns of a block of C
+constexpr int kBRow = kBK * 2;        // bytes of a row of B in LDS
+constexpr int kABufs = 3, kBBufs = 2;
+
+// Range of the buffers that A is copied from: an offset of kPast is past the
+// end, where a buffer load gives zeros; every other offset is checked here to
+// lie in the matrix.
+constexpr int kPast = 0x7FFFFFF0;
 
 // Segment of an expert, clamped to [0, P]; offsets NULL: all rows.
-__device__ __forceinline__ void segment(const int32_t* offsets, int e, int64_t P, int64_t& lo, int64_t& hi) {
+__device__ __forceinline__ void segment(const int32_t* offsets, int e, int P, int& lo, int& hi) {
   lo = 0;
   hi = P;
   if (offsets) {
-    lo = min(max((int64_t)offsets[e], (int64_t)0), P);
-    hi = min(max((int64_t)offsets[e + 1], lo), P);
+    lo = min(max(offsets[e], 0), P);
+    hi = min(max(offsets[e + 1], lo), P);
   }
 }
 
-// Row tile number `slot` over all experts: its expert and first row; false if
-// there are fewer tiles.
-__device__ __forceinline__ bool find_tile(const int32_t* offsets, int E, int64_t P, int64_t slot, int& e, int64_t& lo,
-                                          int64_t& hi) {
-  for (e = 0; e < E; ++e) {
-    segment(offsets, e, P, lo, hi);
-    const int64_t tiles = (hi - lo + kT - 1) / kT;
-    if (slot < tiles) {
-      lo += slot * kT;
+// Row tile number `slot` over all experts: its expert, first row and the
+// expert's end; false if there are fewer tiles.  Each wave looks at 64 experts
+// at a time.
+template <int BM>
+__device__ __forceinline__ bool find_tile(const int32_t* offsets, int E, int P, int slot, int& e, int& lo, int& hi) {
+  if (!offsets) {
+    e = 0;
+    lo = slot * BM;
+    hi = P;
+    return lo < P;
+  }
+  const int lane = threadIdx.x & 63;
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    int l = 0, h = 0;
+    if (e0 + lane < E) segment(offsets, e0 + lane, P, l, h);
+    const int tiles = (h - l + BM - 1) / BM;
+    int x = tiles;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int y = __shfl_up(x, off);
+      if (lane >= off) x += y;
+    }
+    const uint64_t at = __ballot(slot < x);
+    if (at) {
+      const int first = __builtin_ctzll(at);
+      e = e0 + first;
+      lo = __shfl(l + (slot - (x - tiles)) * BM, first);
+      hi = __shfl(h, first);
       return true;
     }
-    slot -= tiles;
+    slot -= __shfl(x, 63);
   }
   return false;
 }
 
-template <bool WGRAD, int KIND, int LAYOUT>
-__global__ void __launch_bounds__(256)
-grad_simple_kernel(GradArgs g) {
-  __shared__ uint16_t sa[kR][kT + kPad], sb[kR][kT + kPad];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const PieceSrc src{g.b, g.b_scales, g.K, g.ldb};
-  const int64_t k0 = (int64_t)blockIdx.x * kT;
-  int e;
-  int64_t lo, hi, m0;     // the segment's rows; m0: first row (dgrad) / first n (wgrad) of the tile
+// Chunk permutation of a row that is read column-wise: four rows r .. r+3 of a
+// read get different pairs of chunks (bits 1, 2), the two halves of a fragment
+// (bit 0) and rows 8 apart (bit 3) others, so that 16 rows in a row have 16
+// different values and a piece's chunks are written without conflicts too.
+__device__ __forceinline__ int swizzle(int r) { return ((r & 3) << 1) | ((r >> 2) & 1) | (r & 8); }
+
+// Eight values along the summed index for lane l's column of a 16-column tile:
+// rows 8 (l / 16) + 0..7 of 32, from the lane's addresses for the two halves.
+// (restrict: the reads do not alias a copy in flight, which the kernel waits
+// for by count; without it every read would wait for all copies.)
+__device__ __forceinline__ bf16x8_t read_columns(const trptr_t __restrict__ p0, const trptr_t __restrict__ p1) {
+  const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p0);
+  const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p1);
+  typedef short s16x8_t __attribute__((ext_vector_type(8)));
+  const s16x8_t v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  return __builtin_bit_cast(bf16x8_t, v);
+}
+
+template <bool WGRAD, int KIND, int LAYOUT, bool GATHER, int kWM, int kWK, int kMT>
+struct Kern {
+  static constexpr int kWaves = kWM * kWK, kThreads = 64 * kWaves, R = 8 * kWaves;
+  static constexpr int kKT = kBK / 16 / kWK;              // 16-column tiles per wave
+  static constexpr int BM = 16 * kMT * kWM;
+  static constexpr int kSteps = R / 32;                   // matrix steps per stage
+  static constexpr int kABytes = R * BM * 2, kBBytes = R * kBRow;
+  static constexpr int kSmem = kABufs * kABytes + kBBufs * kBBytes;
+  static constexpr int kCopies = kABytes / 1024;          // copy instructions per stage
+  static constexpr int kCPW = (kCopies + kWaves - 1) / kWaves;
+  static constexpr int kBLoads = (KIND == kBf16Piece ? 4 : (KIND == kMxFp8 || KIND == kMxInt8) ? 3 : 2);
+};
+
+template <bool WGRAD, int KIND, int LAYOUT, bool GATHER, int kWM, int kWK, int kMT>
+__global__ void __launch_bounds__(64 * kWM * kWK, 2)
+grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles) {
+  using C = Kern<WGRAD, KIND, LAYOUT, GATHER, kWM, kWK, kMT>;
+  constexpr int R = C::R, BM = C::BM;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  uint8_t* const abase = smem;
+  uint8_t* const bbase = smem + kABufs * C::kABytes;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / kWK, wk = wave % kWK;
+
+  // block of C: XCD-major, then groups of 4 row tiles
+  const int b = blockIdx.x, per = gridDim.x >> 3;
+  const int lin = (b & 7) * per + (b >> 3);
+  if (lin >= tiles) return;
+  const int P = (int)g.P, N = (int)g.N, K = (int)g.K;
+  const int per_e = WGRAD ? mtiles * ktiles : tiles;
+  int e = WGRAD ? lin / per_e : 0;
+  const int in_e = lin - e * per_e;
+  const int gsz = 4 * ktiles, first_m = (in_e / gsz) * 4, gm = min(mtiles - first_m, 4);
+  const int mt = first_m + (in_e % gsz) % gm, k0 = ((in_e % gsz) / gm) * kBK;
+  int lo, hi, m0;     // the expert's rows; first row (dgrad) / first n (wgrad) of the block
   if constexpr (WGRAD) {
-    e = blockIdx.z;
-    segment(g.offsets, e, g.P, lo, hi);
-    m0 = (int64_t)blockIdx.y * kT;
+    segment(g.offsets, e, P, lo, hi);
+    m0 = mt * BM;
   } else {
-    if (!find_tile(g.offsets, g.E, g.P, blockIdx.y, e, lo, hi)) return;
+    if (!find_tile<BM>(g.offsets, g.E, P, mt, e, lo, hi)) return;
+    e = __builtin_amdgcn_readfirstlane(e);
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    hi = __builtin_amdgcn_readfirstlane(hi);
     m0 = lo;
   }
-  const int64_t m_end = WGRAD ? g.N : hi, r_begin = WGRAD ? lo : 0, r_end = WGRAD ? hi : g.N;
-  f32x4_t acc[2][2] = {};
-  for (int64_t r0 = r_begin; r0 < r_end; r0 += kR) {
-    __syncthreads();
+  const int r_begin = WGRAD ? lo : 0, r_end = WGRAD ? hi : N;
+  const int stages = (r_end - r_begin + R - 1) / R;
+  const int m_end = WGRAD ? N : hi;
+
+  // ---- A: this lane's part of each copy, as a byte offset from the stage's
+  // first row or column; a lane with nothing to copy takes an offset past the
+  // buffer's end and gets zeros
+  int aoff[C::kCPW];
+#pragma unroll
+  for (int q = 0; q < C::kCPW; ++q) {
+    const int ci = wave + C::kWaves * q;              // copy instruction: 1 KB
     if constexpr (WGRAD) {
-      const int r = tid >> 3, c = (tid & 7) * 8;
-      u32x4_t v{0u, 0u, 0u, 0u};
-      if (r0 + r < r_end && m0 + c < g.N) v = *reinterpret_cast<const u32x4_t*>(g.dc + (r0 + r) * g.lddc + m0 + c);
-      *reinterpret_cast<u32x4_t*>(&sa[r][c]) = v;
+      constexpr int AC = BM / 8, RPC = 64 / AC;       // chunks per row, rows per copy
+      const int r = ci * RPC + lane / AC, c = (lane % AC) ^ (swizzle(r) & (AC - 1));
+      aoff[q] = m0 + 8 * c < N ? (r * (int)g.lddc + 8 * c) * 2 : kPast;
     } else {
-      const int m = tid >> 2, c = (tid & 3) * 8;
-      u32x4_t v{0u, 0u, 0u, 0u};
-      if (m0 + m < hi && r0 + c < g.N) v = *reinterpret_cast<const u32x4_t*>(g.dc + (m0 + m) * g.lddc + r0 + c);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sa[c + i][m] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+      constexpr int AC = R / 8, RPC = 64 / AC, RPL = 16 / AC;   // RPL: rows per 256 bytes
+      const int m = ci * RPC + lane / AC, c = (lane % AC) ^ ((m / RPL) & (AC - 1));
+      aoff[q] = (min(m, hi - 1 - m0) * (int)g.lddc + 8 * c) * 2;
     }
-    if (tid < 64) {
-      const int r = tid >> 1, c = (tid & 1) * 32;
-      bool ok = r0 + r < r_end && k0 + c < g.K;
-      int64_t row = WGRAD ? r0 + r : (int64_t)e * g.N + r0 + r;
-      if constexpr (WGRAD) {
-        if (ok && g.gather) row = g.gather[row];
-        ok = ok && row >= 0 && row < g.T;
-      }
-      Piece<KIND> p;
-      u32x4_t o[4];
-      piece_load<KIND, LAYOUT>(p, src, row, k0 + c, ok);
-      piece_convert<KIND>(p, o);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<u32x4_t*>(&sb[r][c + 8 * i]) = ok ? o[i] : u32x4_t{0u, 0u, 0u, 0u};
-    }
-    __syncthreads();
-    bf16x8_t fa[2], fb[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      uint16_t xa[8], xb[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        xa[i] = sa[8 * (lane >> 4) + i][32 * (wave >> 1) + 16 * t + (lane & 15)];
-        xb[i] = sb[8 * (lane >> 4) + i][32 * (wave & 1) + 16 * t + (lane & 15)];
-      }
-      fa[t] = __builtin_bit_cast(bf16x8_t, xa);
-      fb[t] = __builtin_bit_cast(bf16x8_t, xb);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = mma16x16x32(fb[j], fa[i], acc[i][j]);
   }
+  const uint16_t* const adata = g.dc + (WGRAD ? (int64_t)r_begin * g.lddc + m0 : (int64_t)m0 * g.lddc);
+  auto copy_a = [&](int u, int buf) {
+    const int r0 = u * R;
+    const uint16_t* base = adata + (WGRAD ? (int64_t)r0 * g.lddc : (int64_t)r0);
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), 0, kPast, 0x00020000);
+    uint8_t* dst = abase + buf * C::kABytes;
+#pragma unroll
+    for (int q = 0; q < C::kCPW; ++q) {
+      const int ci = wave + C::kWaves * q;
+      if (C::kCopies % C::kWaves != 0 && ci >= C::kCopies) continue;
+      int off = aoff[q];
+      if constexpr (WGRAD) {
+        constexpr int AC = BM / 8, RPC = 64 / AC;
+        if (r0 + ci * RPC + lane / AC >= r_end - r_begin) off = kPast;
+      } else {
+        constexpr int AC = R / 8, RPC = 64 / AC, RPL = 16 / AC;
+        const int m = ci * RPC + lane / AC, c = (lane % AC) ^ ((m / RPL) & (AC - 1));
+        if (r0 + 8 * c >= N) off = kPast;
+      }
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lptr_t)(dst + ci * 1024), 16, off, 0, 0, 0);
+    }
+  };
+
+  // ---- B: this thread's row of a stage and its 32 columns.  Tiled weights:
+  // a wave loads one 16-row x 128-column tile, contiguous; otherwise eight
+  // lanes load 256 columns of a row.
+  const PieceSrc src{g.b, g.b_scales, g.K, g.ldb};
+  int br, bp;
+  if constexpr (!WGRAD && LAYOUT == kLayoutTiled) {
+    br = 16 * (wave >> 1) + (lane & 15);
+    bp = 4 * (wave & 1) + (lane >> 4);
+  } else {
+    br = tid >> 3;
+    bp = tid & 7;
+  }
+  const int bcol = min(k0 + 32 * bp, ((K + 31) / 32 - 1) * 32);
+  uint8_t* const bdst = bbase + br * kBRow;
+  int bchunk[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bchunk[i] = ((4 * bp + i) ^ swizzle(br)) * 16;
+  auto row_index = [&](int u) -> int {                 // gather's entry for stage u
+    const int p = min(r_begin + u * R + br, r_end - 1);
+    return GATHER ? g.gather[p] : p;
+  };
+  auto load_b = [&](Piece<KIND>& p, int u, int idx, bool& ok) {
+    if constexpr (WGRAD) {
+      ok = r_begin + u * R + br < r_end && idx >= 0 && idx < (int)g.T;
+      piece_load<KIND, LAYOUT>(p, src, ok ? idx : 0, bcol);
+    } else {
+      ok = true;
+      piece_load<KIND, LAYOUT>(p, src, (int64_t)e * N + min(u * R + br, N - 1), bcol);
+    }
+  };
+  auto store_b = [&](Piece<KIND>& p, bool ok, int buf) {
+    if constexpr (WGRAD) piece_clear(p, !ok);
+    u32x4_t o[4];
+    piece_convert<KIND>(p, o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4_t*>(bdst + buf * C::kBBytes + bchunk[i]) = o[i];
+  };
+
+  // ---- fragment addresses in LDS.  A 16-column tile is 32 bytes on, in chunk
+  // bits that the permutation XORs: tile j of the wave is at address ^ (j << 5)
+  // (rows are multiples of 64 bytes kMT or kKT tiles wide, buffers of 1 KB).
+  const int i16 = lane & 15, gq = lane >> 4;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lptr_t)smem;
+  uint32_t bcols[2], acols[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = 8 * gq + 4 * h + (i16 >> 2), s = swizzle(r), x = (i16 & 3) >> 1, y = (i16 & 1) * 8;
+    bcols[h] = lds0 + kABufs * C::kABytes + r * kBRow + (((2 * wk * C::kKT + x) ^ s) << 4) + y;
+    if constexpr (WGRAD) {
+      acols[h] = lds0 + r * (BM * 2) + (((2 * wm * kMT + x) ^ (s & (BM / 8 - 1))) << 4) + y;
+    } else {   // A's rows hold the summed index: chunk 4 h + l / 16 for matrix step h
+      constexpr int AC = R / 8, RPL = 16 / AC;
+      const int m = 16 * kMT * wm + i16;
+      acols[h] = lds0 + m * (R * 2) + (((4 * h + gq) ^ (m / RPL)) & (AC - 1)) * 16;
+    }
+  }
+
+  f32x4_t acc[kMT][C::kKT];
+#pragma unroll
+  for (int t = 0; t < kMT; ++t)
+#pragma unroll
+    for (int j = 0; j < C::kKT; ++j) acc[t][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+  auto multiply = [&](int abuf, int bbuf) {
+    const uint32_t A0 = acols[0] + abuf * C::kABytes, A1 = acols[1] + abuf * C::kABytes;
+    const uint32_t B0 = bcols[0] + bbuf * C::kBBytes, B1 = bcols[1] + bbuf * C::kBBytes;
+#pragma unroll
+    for (int s = 0; s < C::kSteps; ++s) {
+      bf16x8_t fb[C::kKT];
+#pragma unroll
+      for (int j = 0; j < C::kKT; ++j)
+        fb[j] = read_columns((trptr_t)((B0 ^ (j << 5)) + s * 32 * kBRow), (trptr_t)((B1 ^ (j << 5)) + s * 32 * kBRow));
+#pragma unroll
+      for (int t = 0; t < kMT; ++t) {
+        bf16x8_t fa;
+        if constexpr (WGRAD)
+          fa = read_columns((trptr_t)((A0 ^ (t << 5)) + s * 64 * BM), (trptr_t)((A1 ^ (t << 5)) + s * 64 * BM));
+        else
+          fa = as_bf16x8(*(u32x4_lds_t)((s == 0 ? A0 : A1) + t * 32 * R));
+#pragma unroll
+        for (int j = 0; j < C::kKT; ++j) acc[t][j] = mma16x16x32(fb[j], fa, acc[t][j]);
+      }
+    }
+  };
+
+  if (stages > 0) {
+    Piece<KIND> raw[2];
+    bool ok[2];
+    int idx[4] = {0, 0, 0, 0};
+    if constexpr (WGRAD) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) idx[i] = row_index(i);
+      asm volatile("" : "+v"(idx[2]), "+v"(idx[3]));   // loaded here, ahead of the copies that the loop counts
+    }
+    // loads run two stages ahead; past the last stage they read the last rows
+    // again (their results are not used)
+    copy_a(0, 0);
+    load_b(raw[0], 0, idx[0], ok[0]);
+    copy_a(min(1, stages - 1), 1);
+    load_b(raw[1], 1, idx[1], ok[1]);
+    idx[0] = idx[2];
+    idx[1] = idx[3];
+    store_b(raw[0], ok[0], 0);
+    int abuf = 0;
+    auto stage = [&](int u, auto par) {
+      constexpr int J = decltype(par)::value;          // u % 2
+      // copy_a(u) is done once at most copy_a(u + 1) and the loads after it
+      // are outstanding
+      wait_vmcnt_lgkm0<C::kCPW + C::kBLoads>();
+      stage_barrier();
+      const int nbuf = abuf == 0 ? 2 : abuf - 1;       // (u + 2) % 3
+      copy_a(min(u + 2, stages - 1), nbuf);
+      load_b(raw[J], u + 2, idx[J], ok[J]);
+      if constexpr (WGRAD) idx[J] = row_index(u + 4);
+      __builtin_amdgcn_sched_barrier(0);               // (the loads go first: nothing is waited for before them)
+      multiply(abuf, J);
+      store_b(raw[1 - J], ok[1 - J], 1 - J);           // stage u + 1
+      abuf = abuf == 2 ? 0 : abuf + 1;
+    };
+    int u = 0;
+    for (; u + 1 < stages; u += 2) {
+      stage(u, std::integral_constant<int, 0>());
+      stage(u + 1, std::integral_constant<int, 1>());
+    }
+    if (u < stages) stage(u, std::integral_constant<int, 0>());
+    wait_vmcnt_lgkm0<0>();  // no copy into LDS may still be running at exit
+  }
+
   // register q of lane l: column 4 (l / 16) + q, row l % 16 of a 16 x 16 tile
   const float gs = KIND == 2 ? *g.gs : 1.0f;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int t = 0; t < kMT; ++t) {
+    const int m = m0 + 16 * (wm * kMT + t) + i16;
+    if (m >= m_end) continue;
+    const int64_t row = WGRAD ? (int64_t)e * N + m : m;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int64_t m = m0 + 32 * (wave >> 1) + 16 * i + (lane & 15);
-      const int64_t k = k0 + 32 * (wave & 1) + 16 * j + 4 * (lane >> 4);
-      if (m >= m_end || k >= g.K) continue;
-      const f32x4_t v = acc[i][j] * gs;
-      const int64_t row = WGRAD ? (int64_t)e * g.N + m : m;
+    for (int j = 0; j < C::kKT; ++j) {
+      const int k = k0 + 16 * (wk * C::kKT + j) + 4 * gq;
+      if (k >= K) continue;
+      f32x4_t v = acc[t][j];
+      if constexpr (KIND == 2) v *= gs;
       if (WGRAD && g.out_f32) {
-        float* o = static_cast<float*>(g.out) + row * g.ldo + k;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = g.accumulate ? o[q] + v[q] : v[q];
+        f32x4_t* o = reinterpret_cast<f32x4_t*>(static_cast<float*>(g.out) + row * g.ldo + k);
+        if (g.accumulate) v += *o;
+        *o = v;
       } else {
-        store_bf16x4(static_cast<uint16_t*>(g.out) + row * g.ldo + k, v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.out) + row * g.ldo + k) =
+            make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
       }
     }
+  }
 }
 
-template <bool WGRAD, int KIND, int LAYOUT>
+template <bool WGRAD, int KIND, int LAYOUT, bool GATHER, int kWM, int kWK, int kMT>
 hipError_t run(const GradArgs& g, hipStream_t stream) {
-  const unsigned kt = (unsigned)((g.K + kT - 1) / kT);
-  const dim3 grid = WGRAD ? dim3(kt, (unsigned)((g.N + kT - 1) / kT), (unsigned)g.E)
-                          : dim3(kt, (unsigned)((g.P + kT - 1) / kT + g.E - 1), 1u);
-  grad_simple_kernel<WGRAD, KIND, LAYOUT><<<grid, 256, 0, stream>>>(g);
+  using C = Kern<WGRAD, KIND, LAYOUT, GATHER, kWM, kWK, kMT>;
+  const int64_t kt = (g.K + kBK - 1) / kBK;
+  const int64_t mt = WGRAD ? (g.N + C::BM - 1) / C::BM : (g.P + C::BM - 1) / C::BM + g.E - 1;
+  const int64_t tiles = mt * kt * (WGRAD ? g.E : 1);
+  const hipError_t attr = set_max_lds<&grad_kernel<WGRAD, KIND, LAYOUT, GATHER, kWM, kWK, kMT>>(C::kSmem);
+  if (attr != hipSuccess) return attr;
+  grad_kernel<WGRAD, KIND, LAYOUT, GATHER, kWM, kWK, kMT>
+      <<<(unsigned)((tiles + 7) / 8 * 8), C::kThreads, C::kSmem, stream>>>(g, (int)mt, (int)kt, (int)tiles);
   return hipGetLastError();
 }
+
+template <int KIND, int LAYOUT>
+hipError_t run_dgrad(const GradArgs& g, hipStream_t stream) {
+  return run<false, KIND, LAYOUT, false, 1, 4, 8>(g, stream);
+}
+
+template <int KIND>
+hipError_t run_wgrad(const GradArgs& g, hipStream_t stream) {
+  return g.gather ? run<true, KIND, kLayoutRows, true, 1, 4, 8>(g, stream)
+                  : run<true, KIND, kLayoutRows, false, 1, 4, 8>(g, stream);
+}
+
+constexpr int64_t kMaxTiles = ((int64_t)1 << 22);
 
 }  // namespace
 
 size_t dgrad_workspace(int64_t, int32_t, int64_t, int64_t) { return 0; }
 size_t wgrad_workspace(int64_t, int32_t, int64_t, int64_t) { return 0; }
 
+// (32-row tiles, the smallest of any variant)
 bool dgrad_fits(int64_t P, int32_t E, int64_t, int64_t K) {
-  return (P + kT - 1) / kT + E <= 65535 && (K + kT - 1) / kT < ((int64_t)1 << 24);
+  return ((P + 31) / 32 + E) * ((K + kBK - 1) / kBK) <= kMaxTiles;
 }
-bool wgrad_fits(int64_t, int32_t, int64_t N, int64_t K) {
-  return (N + kT - 1) / kT <= 65535 && (K + kT - 1) / kT < ((int64_t)1 << 24);
+bool wgrad_fits(int64_t, int32_t E, int64_t N, int64_t K) {
+  return E * ((N + 31) / 32) * ((K + kBK - 1) / kBK) <= kMaxTiles;
 }
 
 hipError_t launch_dgrad(int fmt, int layout, const GradArgs& g, hipStream_t stream) {
   const bool t = layout == kLayoutTiled;
   switch (fmt) {
-    case 0: return t ? run<false, 0, kLayoutTiled>(g, stream) : run<false, 0, kLayoutRows>(g, stream);
-    case 1: return t ? run<false, 1, kLayoutTiled>(g, stream) : run<false, 1, kLayoutRows>(g, stream);
-    case 4: return t ? run<false, 4, kLayoutTiled>(g, stream) : run<false, 4, kLayoutRows>(g, stream);
-    default: return t ? run<false, 2, kLayoutTiled>(g, stream) : run<false, 2, kLayoutRows>(g, stream);
+    case 0: return t ? run_dgrad<0, kLayoutTiled>(g, stream) : run_dgrad<0, kLayoutRows>(g, stream);
+    case 1: return t ? run_dgrad<1, kLayoutTiled>(g, stream) : run_dgrad<1, kLayoutRows>(g, stream);
+    case 4: return t ? run_dgrad<4, kLayoutTiled>(g, stream) : run_dgrad<4, kLayoutRows>(g, stream);
+    default: return t ? run_dgrad<2, kLayoutTiled>(g, stream) : run_dgrad<2, kLayoutRows>(g, stream);
   }
 }
 
 hipError_t launch_wgrad(int kind, const GradArgs& g, hipStream_t stream) {
   switch (kind) {
-    case kMxFp8: return run<true, kMxFp8, kLayoutRows>(g, stream);
-    case kMxInt8: return run<true, kMxInt8, kLayoutRows>(g, stream);
-    default: return run<true, kBf16Piece, kLayoutRows>(g, stream);
+    case kMxFp8: return run_wgrad<kMxFp8>(g, stream);
+    case kMxInt8: return run_wgrad<kMxInt8>(g, stream);
+    default: return run_wgrad<kBf16Piece>(g, stream);
   }
 }
 

@@ -34,20 +34,16 @@ struct Piece {
 };
 
 // Row r, columns c .. c + 31 (c % 32 == 0, c < K; the K of a bf16 matrix may end
-// inside the piece, at a multiple of 8).  ok = false: nothing is read and the
-// piece is zeros.
+// inside the piece, at a multiple of 8: the columns past it repeat others).
 template <int KIND, int LAYOUT>
-__device__ __forceinline__ void piece_load(Piece<KIND>& p, const PieceSrc& src, int64_t r, int64_t c, bool ok) {
+__device__ __forceinline__ void piece_load(Piece<KIND>& p, const PieceSrc& src, int64_t r, int64_t c) {
   constexpr int W = Piece<KIND>::kWords;
-#pragma unroll
-  for (int i = 0; i < W; ++i) p.q[i] = u32x4_t{0u, 0u, 0u, 0u};
-  p.s = 0u;
-  if (!ok) return;
   if constexpr (KIND == kBf16Piece) {
     const uint16_t* row = reinterpret_cast<const uint16_t*>(src.data) + r * src.ld + c;
 #pragma unroll
-    for (int i = 0; i < W; ++i)
-      if (c + 8 * i < src.cols) p.q[i] = *reinterpret_cast<const u32x4_t*>(row + 8 * i);
+    for (int i = 0; i < W; ++i)      // (always W loads: the kernels count them)
+      p.q[i] = *reinterpret_cast<const u32x4_t*>(row + min((int64_t)8 * i, src.cols - 8 - c));
+    p.s = 0u;
   } else if constexpr (KIND == kMxFp8 || KIND == kMxInt8) {
     const uint8_t* row = src.data + r * src.cols + c;
     p.q[0] = *reinterpret_cast<const u32x4_t*>(row);
@@ -63,14 +59,31 @@ __device__ __forceinline__ void piece_load(Piece<KIND>& p, const PieceSrc& src, 
   }
 }
 
-// The piece as four times eight bf16 (out[i] holds columns 8i .. 8i + 7).  A
-// piece that was not loaded gives zeros.
+// A row without values: zeros, whatever was loaded in its place.
+template <int KIND>
+__device__ __forceinline__ void piece_clear(Piece<KIND>& p, bool clear) {
+#pragma unroll
+  for (int i = 0; i < Piece<KIND>::kWords; ++i) p.q[i] = clear ? u32x4_t{0u, 0u, 0u, 0u} : p.q[i];
+  p.s = clear ? 0u : p.s;
+}
+
+// The piece as four times eight bf16 (out[i] holds columns 8i .. 8i + 7).
 template <int KIND>
 __device__ __forceinline__ void piece_convert(const Piece<KIND>& p, u32x4_t (&out)[4]) {
   if constexpr (KIND == kBf16Piece) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) out[i] = p.q[i];
-  } else if constexpr (KIND == kMxFp8 || KIND == kMxInt8) {
+  } else if constexpr (KIND == kMxFp8) {
+    const float s = e8m0_value(p.s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t w = p.q[i >> 1][2 * (i & 1) + h];
+        out[i][2 * h] = as_u32(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false));
+        out[i][2 * h + 1] = as_u32(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true));
+      }
+  } else if constexpr (KIND == kMxInt8) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float x[8];
