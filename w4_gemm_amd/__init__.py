@@ -11,6 +11,7 @@ library cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -134,9 +135,14 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# the current stream's handle of a device, without an object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream(stream):
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -248,12 +254,16 @@ def q4_version() -> int:
     return lib().q4_version()
 
 
+@functools.lru_cache(maxsize=4096)
+def _sizes(fmt: int, layout: int, rows: int, cols: int):
+    cb, sb = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().q4_sizes(fmt, layout, rows, cols, ctypes.byref(cb), ctypes.byref(sb)), "q4_sizes")
+    return cb.value, sb.value
+
+
 def q4_sizes(fmt, rows: int, cols: int, layout=LAYOUT_ROWS):
     """(codes bytes, scales bytes) of a rows x cols tensor."""
-    cb, sb = ctypes.c_size_t(), ctypes.c_size_t()
-    _check(lib().q4_sizes(_fmt(fmt), _layout(layout), rows, cols, ctypes.byref(cb),
-                          ctypes.byref(sb)), "q4_sizes")
-    return cb.value, sb.value
+    return _sizes(_fmt(fmt), _layout(layout), rows, cols)
 
 
 def empty_q4(fmt, rows: int, cols: int, device="cuda", layout=LAYOUT_ROWS) -> Q4Tensor:

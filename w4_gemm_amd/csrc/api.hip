@@ -12,7 +12,7 @@ namespace {
 thread_local int g_last_hip_error = 0;
 
 constexpr int64_t kMaxDim = (int64_t)1 << 31;  // kernels index rows/cols in int
-constexpr int64_t kMaxGradLd = (int64_t)1 << 21;      // the gradient products address 256 rows of dC in 2^30 bytes
+constexpr int64_t kMaxGradLd = (int64_t)1 << 21;      // the gradient products address 256 rows in 2^30 bytes
 constexpr int64_t kMaxTopkTokens = (int64_t)1 << 26;  // a wave per token, within 2^32 threads
 
 int block_of(int fmt) {
@@ -665,7 +665,7 @@ q4_status dgrad(const void* dC, int64_t lddc, const int32_t* offsets, int32_t E,
   if (!aligned(offsets, 4)) return Q4_ERR_ALIGN;
   st = check_bf16(dC, P, N, lddc);
   if (st != Q4_OK) return st;
-  if (P > 1 && lddc > kMaxGradLd) return Q4_ERR_SHAPE;
+  if ((P > 1 && lddc > kMaxGradLd) || K > kMaxGradLd) return Q4_ERR_SHAPE;
   st = check_bf16(dA, P, K, ldda);
   if (st != Q4_OK) return st;
   if (need && !workspace) return Q4_ERR_NULL;
@@ -710,10 +710,11 @@ q4_status wgrad(const void* dC, int64_t lddc, const void* A_bf16, int64_t lda, c
   if (!aligned(gather, 4) || !aligned(offsets, 4)) return Q4_ERR_ALIGN;
   st = check_bf16(dC, P, N, lddc);
   if (st != Q4_OK) return st;
-  if (P > 1 && lddc > kMaxGradLd) return Q4_ERR_SHAPE;
+  if ((P > 1 && lddc > kMaxGradLd) || K > kMaxGradLd) return Q4_ERR_SHAPE;
   if (!A_q) {
     st = check_bf16(A_bf16, T, K, lda);
     if (st != Q4_OK) return st;
+    if (T > 1 && lda > kMaxGradLd) return Q4_ERR_SHAPE;
   }
   if (!dW) return Q4_ERR_NULL;
   if (lddw < K) return Q4_ERR_SHAPE;

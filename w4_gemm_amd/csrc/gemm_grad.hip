@@ -45,6 +45,14 @@ constexpr int kABufs = 3, kBBufs = 2;
 // end, where a buffer load gives zeros; every other offset is checked here to
 // lie in the matrix.
 constexpr int kPast = 0x7FFFFFF0;
+constexpr int kRsrcFlags = 0x00020000;   // a raw buffer of 32-bit words
+
+// A buffer at p (wave-uniform) of the first `rows` of R rows of `bytes` bytes,
+// the last of them `tail` bytes short; empty for rows <= 0.
+__device__ __forceinline__ rsrc_t rows_buffer(const uint8_t* p, int rows, int R, int bytes, int tail = 0) {
+  const int n = rows >= R ? R * bytes - tail : rows > 0 ? rows * bytes - tail : 0;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, __builtin_amdgcn_readfirstlane(n), kRsrcFlags);
+}
 
 // Segment of an expert, clamped to [0, P]; offsets NULL: all rows.
 __device__ __forceinline__ void segment(const int32_t* offsets, int e, int P, int& lo, int& hi) {
@@ -97,6 +105,15 @@ __device__ __forceinline__ bool find_tile(const int32_t* offsets, int E, int P, 
 // different values and a piece's chunks are written without conflicts too.
 __device__ __forceinline__ int swizzle(int r) { return ((r & 3) << 1) | ((r >> 2) & 1) | (r & 8); }
 
+// Chunk permutation of dgrad's A, whose rows of R summed values are read by
+// ds_read_b128, lane l row l % 16 and chunk l / 16.  LDS serves lanes 0-3, 12-15
+// and 20-27 at once, and 4-11, 16-19 and 28-31 (measured): rows four apart take
+// the chunks 0, 3, 2, 1 (R = 32), pairs of rows consecutive ones (R = 64).
+template <int R>
+__device__ __forceinline__ int swizzle_rows(int m) {
+  return R == 32 ? -(m >> 2) & 3 : (m >> 1) & 7;
+}
+
 // Eight values along the summed index for lane l's column of a 16-column tile:
 // rows 8 (l / 16) + 0..7 of 32, from the lane's addresses for the two halves.
 // (restrict: the reads do not alias a copy in flight, which the kernel waits
@@ -119,7 +136,6 @@ struct Kern {
   static constexpr int kSmem = kABufs * kABytes + kBBufs * kBBytes;
   static constexpr int kCopies = kABytes / 1024;          // copy instructions per stage
   static constexpr int kCPW = (kCopies + kWaves - 1) / kWaves;
-  static constexpr int kBLoads = (KIND == kBf16Piece ? 4 : (KIND == kMxFp8 || KIND == kMxInt8) ? 3 : 2);
 };
 
 template <bool WGRAD, int KIND, int LAYOUT, bool GATHER, int kWM, int kWK, int kMT>
@@ -170,70 +186,73 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles) {
       const int r = ci * RPC + lane / AC, c = (lane % AC) ^ (swizzle(r) & (AC - 1));
       aoff[q] = m0 + 8 * c < N ? (r * (int)g.lddc + 8 * c) * 2 : kPast;
     } else {
-      constexpr int AC = R / 8, RPC = 64 / AC, RPL = 16 / AC;   // RPL: rows per 256 bytes
-      const int m = ci * RPC + lane / AC, c = (lane % AC) ^ ((m / RPL) & (AC - 1));
+      constexpr int AC = R / 8, RPC = 64 / AC;
+      const int m = ci * RPC + lane / AC, c = (lane % AC) ^ swizzle_rows<R>(m);
       aoff[q] = (min(m, hi - 1 - m0) * (int)g.lddc + 8 * c) * 2;
     }
   }
-  const uint16_t* const adata = g.dc + (WGRAD ? (int64_t)r_begin * g.lddc + m0 : (int64_t)m0 * g.lddc);
-  auto copy_a = [&](int u, int buf) {
-    const int r0 = u * R;
-    const uint16_t* base = adata + (WGRAD ? (int64_t)r0 * g.lddc : (int64_t)r0);
-    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), 0, kPast, 0x00020000);
+  // the copies run through the stages in order: position and summed rows left
+  // (0 or less past the last stage: the buffer is empty)
+  const uint8_t* apos = reinterpret_cast<const uint8_t*>(
+      g.dc + (WGRAD ? (int64_t)r_begin * g.lddc + m0 : (int64_t)m0 * g.lddc));
+  const int64_t astep = WGRAD ? (int64_t)R * g.lddc * 2 : R * 2;
+  int aleft = r_end - r_begin;
+  auto copy_a = [&](int buf) {
+    const rsrc_t rsrc = rows_buffer(apos, WGRAD ? aleft : aleft > 0 ? R : 0, R, WGRAD ? (int)g.lddc * 2 : kPast / R);
     uint8_t* dst = abase + buf * C::kABytes;
 #pragma unroll
     for (int q = 0; q < C::kCPW; ++q) {
       const int ci = wave + C::kWaves * q;
       if (C::kCopies % C::kWaves != 0 && ci >= C::kCopies) continue;
       int off = aoff[q];
-      if constexpr (WGRAD) {
-        constexpr int AC = BM / 8, RPC = 64 / AC;
-        if (r0 + ci * RPC + lane / AC >= r_end - r_begin) off = kPast;
-      } else {
-        constexpr int AC = R / 8, RPC = 64 / AC, RPL = 16 / AC;
-        const int m = ci * RPC + lane / AC, c = (lane % AC) ^ ((m / RPL) & (AC - 1));
-        if (r0 + 8 * c >= N) off = kPast;
+      if constexpr (!WGRAD) {
+        constexpr int AC = R / 8, RPC = 64 / AC;
+        const int m = ci * RPC + lane / AC, c = (lane % AC) ^ swizzle_rows<R>(m);
+        if (8 * c >= aleft) off = kPast;
       }
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lptr_t)(dst + ci * 1024), 16, off, 0, 0, 0);
     }
+    apos += astep;
+    aleft -= R;
   };
 
-  // ---- B: this thread's row of a stage and its 32 columns.  Tiled weights:
-  // a wave loads one 16-row x 128-column tile, contiguous; otherwise eight
-  // lanes load 256 columns of a row.
-  const PieceSrc src{g.b, g.b_scales, g.K, g.ldb};
-  int br, bp;
-  if constexpr (!WGRAD && LAYOUT == kLayoutTiled) {
-    br = 16 * (wave >> 1) + (lane & 15);
-    bp = 4 * (wave & 1) + (lane >> 4);
-  } else {
-    br = tid >> 3;
-    bp = tid & 7;
-  }
-  const int bcol = min(k0 + 32 * bp, ((K + 31) / 32 - 1) * 32);
+  // ---- B: a thread's 32 values of a stage (q4_piece.h).  The buffers start at
+  // the stage's first row and end with the expert's last, so that rows past the
+  // sum's end are zeros.
+  const int br = piece_row<KIND>(tid);
+  const PieceCols<KIND> bcols_at = piece_cols<KIND>(tid, k0, K);
+  const PieceAt<KIND> at = piece_at<KIND, LAYOUT>(br, bcols_at, K, (int)g.ldb);
+  const int drow = KIND == kBf16Piece ? 2 * (int)g.ldb : WGRAD ? K : K / 2;     // bytes of a row
+  const int srow = KIND == kBf16Piece ? 0 : K / PieceScale<KIND>::kCols * PieceScale<KIND>::kBytes;
+  const int64_t row0 = WGRAD ? r_begin : (int64_t)e * N;
+  const uint8_t *bpos = g.b + row0 * drow, *spos = g.b_scales + row0 * srow;
+  int bleft = WGRAD ? r_end - r_begin : LAYOUT == kLayoutTiled ? (N + 15) / 16 * 16 : N;
   uint8_t* const bdst = bbase + br * kBRow;
   int bchunk[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) bchunk[i] = ((4 * bp + i) ^ swizzle(br)) * 16;
+  for (int i = 0; i < 4; ++i) bchunk[i] = (piece_chunk<KIND>(tid, i) ^ swizzle(br)) * 16;
   auto row_index = [&](int u) -> int {                 // gather's entry for stage u
-    const int p = min(r_begin + u * R + br, r_end - 1);
-    return GATHER ? g.gather[p] : p;
+    return GATHER ? g.gather[min(r_begin + u * R + br, r_end - 1)] : 0;
   };
-  auto load_b = [&](Piece<KIND>& p, int u, int idx, bool& ok) {
-    if constexpr (WGRAD) {
-      ok = r_begin + u * R + br < r_end && idx >= 0 && idx < (int)g.T;
-      piece_load<KIND, LAYOUT>(p, src, ok ? idx : 0, bcol);
+  auto load_b = [&](Piece<KIND>& p, int idx, bool& ok) {   // stage after stage, like copy_a
+    if constexpr (GATHER) {
+      ok = br < bleft && idx >= 0 && idx < (int)g.T;
+      piece_load_row<KIND>(p, g.b, g.b_scales, ok ? idx : 0, bcols_at, K, g.ldb);
     } else {
+      // (a bf16 matrix ends with its last row's K columns)
+      const int tail = KIND == kBf16Piece ? drow - 2 * K : 0;
+      piece_load<KIND>(p, rows_buffer(bpos, bleft, R, drow, tail), rows_buffer(spos, bleft, R, srow), at);
       ok = true;
-      piece_load<KIND, LAYOUT>(p, src, (int64_t)e * N + min(u * R + br, N - 1), bcol);
+      bpos += (int64_t)R * drow;
+      spos += (int64_t)R * srow;
     }
+    bleft -= R;
   };
-  auto store_b = [&](Piece<KIND>& p, bool ok, int buf) {
-    if constexpr (WGRAD) piece_clear(p, !ok);
-    u32x4_t o[4];
-    piece_convert<KIND>(p, o);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4_t*>(bdst + buf * C::kBBytes + bchunk[i]) = o[i];
+  // eight values (of four times eight) of a piece, converted and written
+  auto store_b = [&](Piece<KIND>& p, bool ok, int buf, int i) {
+    if constexpr (GATHER)
+      if (i == 0) piece_clear(p, !ok);
+    *reinterpret_cast<u32x4_t*>(bdst + buf * C::kBBytes + bchunk[i]) = piece_convert<KIND>(p, i);
   };
 
   // ---- fragment addresses in LDS.  A 16-column tile is 32 bytes on, in chunk
@@ -249,9 +268,8 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles) {
     if constexpr (WGRAD) {
       acols[h] = lds0 + r * (BM * 2) + (((2 * wm * kMT + x) ^ (s & (BM / 8 - 1))) << 4) + y;
     } else {   // A's rows hold the summed index: chunk 4 h + l / 16 for matrix step h
-      constexpr int AC = R / 8, RPL = 16 / AC;
       const int m = 16 * kMT * wm + i16;
-      acols[h] = lds0 + m * (R * 2) + (((4 * h + gq) ^ (m / RPL)) & (AC - 1)) * 16;
+      acols[h] = lds0 + m * (R * 2) + (((4 * h + gq) ^ swizzle_rows<R>(m)) & (R / 8 - 1)) * 16;
     }
   }
 
@@ -261,61 +279,116 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles) {
 #pragma unroll
     for (int j = 0; j < C::kKT; ++j) acc[t][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  auto multiply = [&](int abuf, int bbuf) {
-    const uint32_t A0 = acols[0] + abuf * C::kABytes, A1 = acols[1] + abuf * C::kABytes;
-    const uint32_t B0 = bcols[0] + bbuf * C::kBBytes, B1 = bcols[1] + bbuf * C::kBBytes;
+  // ---- a stage is kGroups groups of kGT row tiles by all of the wave's
+  // column tiles; the fragments of a group are read under the group before
+  constexpr int kGT = 2, kG = kMT / kGT, kGroups = C::kSteps * kG;
+  bf16x8_t fa[2][kGT], fb[2][C::kKT];
+  auto read_a = [&](int buf, int gi) {
+    const int s = gi / kG;
 #pragma unroll
-    for (int s = 0; s < C::kSteps; ++s) {
-      bf16x8_t fb[C::kKT];
-#pragma unroll
-      for (int j = 0; j < C::kKT; ++j)
-        fb[j] = read_columns((trptr_t)((B0 ^ (j << 5)) + s * 32 * kBRow), (trptr_t)((B1 ^ (j << 5)) + s * 32 * kBRow));
-#pragma unroll
-      for (int t = 0; t < kMT; ++t) {
-        bf16x8_t fa;
-        if constexpr (WGRAD)
-          fa = read_columns((trptr_t)((A0 ^ (t << 5)) + s * 64 * BM), (trptr_t)((A1 ^ (t << 5)) + s * 64 * BM));
-        else
-          fa = as_bf16x8(*(u32x4_lds_t)((s == 0 ? A0 : A1) + t * 32 * R));
-#pragma unroll
-        for (int j = 0; j < C::kKT; ++j) acc[t][j] = mma16x16x32(fb[j], fa, acc[t][j]);
-      }
+    for (int q = 0; q < kGT; ++q) {
+      const int t = kGT * (gi % kG) + q;
+      const uint32_t a0 = acols[0] + buf * C::kABytes, a1 = acols[1] + buf * C::kABytes;
+      if constexpr (WGRAD)
+        fa[gi & 1][q] = read_columns((trptr_t)((a0 ^ (t << 5)) + s * 64 * BM), (trptr_t)((a1 ^ (t << 5)) + s * 64 * BM));
+      else
+        fa[gi & 1][q] = as_bf16x8(*(u32x4_lds_t)((s == 0 ? a0 : a1) + t * 32 * R));
     }
+  };
+  auto read_b = [&](int buf, int s, int set) {
+    const uint32_t b0 = bcols[0] + buf * C::kBBytes, b1 = bcols[1] + buf * C::kBBytes;
+#pragma unroll
+    for (int j = 0; j < C::kKT; ++j)
+      fb[set][j] = read_columns((trptr_t)((b0 ^ (j << 5)) + s * 32 * kBRow), (trptr_t)((b1 ^ (j << 5)) + s * 32 * kBRow));
   };
 
   if (stages > 0) {
-    Piece<KIND> raw[2];
-    bool ok[2];
+    // R = 32: two pieces, loaded two stages ahead.  R = 64: one, loaded again
+    // right after its conversion (a second would not fit the registers).
+    constexpr int kSets = C::kSteps == 1 ? 2 : 1;
+    Piece<KIND> raw[kSets];
+    bool ok[kSets];
     int idx[4] = {0, 0, 0, 0};
-    if constexpr (WGRAD) {
+    if constexpr (GATHER) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) idx[i] = row_index(i);
       asm volatile("" : "+v"(idx[2]), "+v"(idx[3]));   // loaded here, ahead of the copies that the loop counts
     }
-    // loads run two stages ahead; past the last stage they read the last rows
-    // again (their results are not used)
-    copy_a(0, 0);
-    load_b(raw[0], 0, idx[0], ok[0]);
-    copy_a(min(1, stages - 1), 1);
-    load_b(raw[1], 1, idx[1], ok[1]);
+    // loads run two stages ahead, past the last stage without reading anything
+    copy_a(0);
+    load_b(raw[0], idx[0], ok[0]);
+    if constexpr (kSets == 2) {
+      copy_a(1);
+      load_b(raw[kSets - 1], idx[1], ok[kSets - 1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) store_b(raw[0], ok[0], 0, i);
+    if constexpr (kSets == 1) {
+      copy_a(1);
+      load_b(raw[0], idx[1], ok[0]);
+    }
     idx[0] = idx[2];
     idx[1] = idx[3];
-    store_b(raw[0], ok[0], 0);
+    wait_vmcnt_lgkm0<C::kCPW + Piece<KIND>::kLoads>();
+    stage_barrier();
+    read_b(0, 0, 0);
+    read_a(0, 0);
     int abuf = 0;
     auto stage = [&](int u, auto par) {
       constexpr int J = decltype(par)::value;          // u % 2
-      // copy_a(u) is done once at most copy_a(u + 1) and the loads after it
-      // are outstanding
-      wait_vmcnt_lgkm0<C::kCPW + C::kBLoads>();
-      stage_barrier();
+      constexpr int kNext = kSets == 2 ? 1 - J : 0, kLoad = kSets == 2 ? J : 0;   // pieces of stages u + 1, u + 2
+      // groups that convert the piece of stage u + 1, and how many eights each
+      constexpr int kConv0 = kSets == 2 ? 1 : 0, kPer = 2, kLoadAt = kSets == 2 ? 0 : 2;
       const int nbuf = abuf == 0 ? 2 : abuf - 1;       // (u + 2) % 3
-      copy_a(min(u + 2, stages - 1), nbuf);
-      load_b(raw[J], u + 2, idx[J], ok[J]);
-      if constexpr (WGRAD) idx[J] = row_index(u + 4);
-      __builtin_amdgcn_sched_barrier(0);               // (the loads go first: nothing is waited for before them)
-      multiply(abuf, J);
-      store_b(raw[1 - J], ok[1 - J], 1 - J);           // stage u + 1
-      abuf = abuf == 2 ? 0 : abuf + 1;
+      const int abuf1 = abuf == 2 ? 0 : abuf + 1;      // (u + 1) % 3
+#pragma unroll
+      for (int gi = 0; gi < kGroups; ++gi) {
+        if (gi == kGroups - 1) {
+          // copy_a(u + 1) is done once at most copy_a(u + 2) and the loads
+          // after it are outstanding; this wave has read all of stage u and
+          // written its part of stage u + 1.  Behind the barrier the buffers of
+          // stage u are free and those of stage u + 1 whole.
+          wait_vmcnt_lgkm0<C::kCPW + Piece<KIND>::kLoads>();
+          stage_barrier();
+          read_b(1 - J, 0, C::kSteps == 1 ? 1 - J : 0);
+          read_a(abuf1, 0);
+        } else {
+          if ((gi + 1) % kG == 0) read_b(J, (gi + 1) / kG, (gi + 1) / kG);
+          read_a(abuf, gi + 1);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (gi == kLoadAt) {
+          copy_a(nbuf);
+          load_b(raw[kLoad], idx[J], ok[kLoad]);
+          if constexpr (GATHER) idx[J] = row_index(u + 4);
+        }
+        // the group's products, and a part of stage u + 1's B converted in
+        // their shadow: a product occupies the matrix pipe for 16 cycles, in
+        // which three or four vector instructions issue
+        const int set = C::kSteps == 1 ? J : gi / kG;
+#pragma unroll
+        for (int q = 0; q < kGT; ++q)
+#pragma unroll
+          for (int j = 0; j < C::kKT; ++j)
+            acc[kGT * (gi % kG) + q][j] = mma16x16x32(fb[set][j], fa[gi & 1][q], acc[kGT * (gi % kG) + q][j]);
+        const bool conv = gi >= kConv0 && gi < kConv0 + 4 / kPer;
+        if (conv) {
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) store_b(raw[kNext], ok[kNext], 1 - J, kPer * (gi - kConv0) + i);
+        }
+#pragma unroll
+        for (int q = 0; q < kGT * C::kKT; ++q) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                  // a product
+          if (gi == kLoadAt) {
+            __builtin_amdgcn_sched_group_barrier(0x006, 6, 0);                // addresses
+            __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);                // loads
+          } else if (conv) {
+            __builtin_amdgcn_sched_group_barrier(0x002, 3 * kPer, 0);         // conversions
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      abuf = abuf1;
     };
     int u = 0;
     for (; u + 1 < stages; u += 2) {

@@ -12,47 +12,100 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 from dataclasses import dataclass
 from typing import Optional, Tuple, Union
 
 import torch
 
-from . import (MXFP8, MXINT8, Q4Tensor, _check, _matrix, _on_gpu, _ptr, _q4, _vector, empty_q4, lib,
+from . import (MXFP8, MXINT8, Q4Tensor, _check, _matrix, _q4, _raw_stream, _vector, empty_q4, lib,
                q4_grouped_gemm, q4_moe_combine, q4_quantize, Routing)
 
 BF16, F32, I32 = torch.bfloat16, torch.float32, torch.int32
 
 
-@contextlib.contextmanager
-def _place(stream, *args):
-    """Checks that every (name, tensor) is on the GPU, all on one, and enters
-    that device and the stream the call runs on; yields (device, stream as the
-    library takes it)."""
-    _on_gpu(*args)
-    where = None
+class _Here:
+    """The call runs on the current device's current stream: nothing to enter."""
+    __slots__ = ("device", "stream")
+
+    def __init__(self, device: int, stream: int):
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        return self.device, self.stream
+
+    def __exit__(self, *exc):
+        return False
+
+
+class _There:
+    """Another device than the current one, or a stream that was asked for."""
+    __slots__ = ("device", "stream", "outer")
+
+    def __init__(self, device: int, stream):
+        self.device, self.outer = device, contextlib.ExitStack()
+        with torch.cuda.device(device):
+            self.stream = stream if stream is not None else torch.cuda.current_stream()
+
+    def __enter__(self):
+        self.outer.enter_context(torch.cuda.device(self.device))
+        self.outer.enter_context(torch.cuda.stream(self.stream))
+        return self.device, self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        return self.outer.__exit__(*exc)
+
+
+def _tensors(args):
     for name, t in args:
-        for x in ((t.codes, t.scales, t.global_scale) if isinstance(t, Q4Tensor) else (t,)):
-            if x is None:
-                continue
-            if where is not None and x.device != where:
-                raise ValueError(f"{name} must be on {where} like the other tensors (got {x.device})")
-            where = x.device
-    if isinstance(stream, torch.cuda.Stream):
-        if stream.device != where:
-            raise ValueError(f"stream must be of {where} (got {stream.device})")
-        s = stream
-    else:
-        with torch.cuda.device(where):
-            s = torch.cuda.current_stream() if stream is None else torch.cuda.ExternalStream(int(stream), device=where)
-    with torch.cuda.device(where), torch.cuda.stream(s):
-        yield where, ctypes.c_void_p(s.cuda_stream)
+        if isinstance(t, Q4Tensor):
+            yield name + ".codes", t.codes
+            yield name + ".scales", t.scales
+            if t.global_scale is not None:
+                yield name + ".global_scale", t.global_scale
+        elif t is not None:
+            yield name, t
+
+
+def _place(stream, *args):
+    """Checks that every (name, tensor) is on the GPU, all on one; `with` it the
+    call is on that device and the stream it runs on, as (device, stream) ready
+    for torch and for the library."""
+    where = None
+    for name, t in _tensors(args):
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor (got device {t.device})")
+        i = t.get_device()
+        if where is None:
+            where = i
+        elif i != where:
+            raise ValueError(f"{name} must be on cuda:{where} like the other tensors (got cuda:{i})")
+    if stream is None:
+        if where == torch.cuda.current_device():
+            return _Here(where, _raw_stream(where))
+        return _There(where, None)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=where)
+    elif stream.device.index != where:
+        raise ValueError(f"stream must be of cuda:{where} (got {stream.device})")
+    return _There(where, stream)
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(fn: str, *sizes) -> int:
+    n = ctypes.c_size_t()
+    _check(getattr(lib(), fn)(*sizes, ctypes.byref(n)), fn)
+    return n.value
 
 
 def _workspace(fn: str, device, *sizes):
     """(tensor or None, bytes) of the workspace that a call's size query asks for."""
-    n = ctypes.c_size_t()
-    _check(getattr(lib(), fn)(*sizes, ctypes.byref(n)), fn)
-    return (torch.empty(n.value, dtype=torch.uint8, device=device) if n.value else None), n.value
+    n = _workspace_bytes(fn, *sizes)
+    return (torch.empty(n, dtype=torch.uint8, device=device) if n else None), n
 
 
 def _ld(t: torch.Tensor) -> int:
