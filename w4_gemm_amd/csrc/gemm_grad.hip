@@ -18,8 +18,8 @@
 //     waited for as a whole).  Rows and columns past the sum's end are filled
 //     with zeros by the buffer's range check, so that whatever B holds there
 //     (clamped to existing rows) adds nothing.
-//   * The 16-byte chunks of an LDS row are permuted (XOR with bits of the row)
-//     so that the 16 or 32 lanes that LDS serves at once never meet on a bank.
+//   * Rows and 16-byte chunks are placed in LDS so that the lanes that it serves
+//     at once never meet on a bank (column_place, swizzle_rows).
 //   * A workgroup of kWM x kWK waves makes a block of C of 16 kMT kWM rows by
 //     256 columns and takes R = 8 kWM kWK summed rows per stage (one piece of B
 //     per thread).  A is copied two stages ahead (three buffers), B is loaded
@@ -38,7 +38,6 @@ typedef __attribute__((address_space(3))) s16x4_t* trptr_t;
 typedef const __attribute__((address_space(3))) u32x4_t* u32x4_lds_t;
 
 constexpr int kBK = 256;              // columns of a block of C
-constexpr int kBRow = kBK * 2;        // bytes of a row of B in LDS
 constexpr int kABufs = 3, kBBufs = 2;
 
 // Range of the buffers that A is copied from: an offset of kPast is past the
@@ -99,11 +98,28 @@ __device__ __forceinline__ bool find_tile(const int32_t* offsets, int E, int P, 
   return false;
 }
 
-// Chunk permutation of a row that is read column-wise: four rows r .. r+3 of a
-// read get different pairs of chunks (bits 1, 2), the two halves of a fragment
-// (bit 0) and rows 8 apart (bit 3) others, so that 16 rows in a row have 16
-// different values and a piece's chunks are written without conflicts too.
-__device__ __forceinline__ int swizzle(int r) { return ((r & 3) << 1) | ((r >> 2) & 1) | (r & 8); }
+// Place of element (row r, 16-byte chunk c) of an operand that is read
+// column-wise: blocks of 32 columns (4 chunks, 64 bytes per row), in a block
+// every 32 rows of a matrix step in the order in which they are read.  A read
+// takes, for 16 lanes, 32 bytes of four rows 8 g + 4 h + 0..3 (g the lane group,
+// h the half of the fragment); LDS serves two groups at once, so the rows of a
+// pair of groups lie together (8 rows, 512 bytes) and one of their fours has
+// the halves of its 64 bytes swapped: 8 x 32 bytes on 256 bytes of banks; which
+// of them alternates with h, so that a wave that writes one chunk of rows 0..15
+// does not meet itself either.  Steps and (but for `turn`) pairs of tiles are
+// constant offsets; an odd tile and the second half are address ^ 32.  turn: the rows of block b are XORed with b % 4, so that
+// threads that write neighbouring blocks of one row meet no bank twice.
+__device__ __forceinline__ int row_place(int r) {        // r in 0..31 -> 0..31
+  return (r & 16) | ((r & 4) << 1) | ((r & 8) >> 1) | (r & 3);
+}
+__device__ __forceinline__ int place_row(int p) {        // its inverse
+  return (p & 16) | ((p & 4) << 1) | ((p & 8) >> 1) | (p & 3);
+}
+__device__ __forceinline__ int place_swap(int p) { return ((p >> 1) ^ (p >> 2)) & 2; }   // on the chunk's number
+__device__ __forceinline__ int column_place(int r, int c, int block_bytes, bool turn) {
+  const int p = row_place(r & 31) ^ (turn ? (c >> 2) & 3 : 0);
+  return (c >> 2) * block_bytes + ((r & ~31) + p) * 64 + (((c & 3) ^ place_swap(p)) << 4);
+}
 
 // Chunk permutation of dgrad's A, whose rows of R summed values are read by
 // ds_read_b128, lane l row l % 16 and chunk l / 16.  LDS serves lanes 0-3, 12-15
@@ -115,12 +131,13 @@ __device__ __forceinline__ int swizzle_rows(int m) {
 }
 
 // Eight values along the summed index for lane l's column of a 16-column tile:
-// rows 8 (l / 16) + 0..7 of 32, from the lane's addresses for the two halves.
+// rows 8 (l / 16) + 0..7 of 32, from the lane's address for the first half (p0)
+// and that of the other tile of the pair (p1).
 // (restrict: the reads do not alias a copy in flight, which the kernel waits
 // for by count; without it every read would wait for all copies.)
 __device__ __forceinline__ bf16x8_t read_columns(const trptr_t __restrict__ p0, const trptr_t __restrict__ p1) {
   const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p0);
-  const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p1);
+  const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p1 + 512 / sizeof(s16x4_t));
   typedef short s16x8_t __attribute__((ext_vector_type(8)));
   const s16x8_t v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   return __builtin_bit_cast(bf16x8_t, v);
@@ -132,7 +149,8 @@ struct Kern {
   static constexpr int kKT = kBK / 16 / kWK;              // 16-column tiles per wave
   static constexpr int BM = 16 * kMT * kWM;
   static constexpr int kSteps = R / 32;                   // matrix steps per stage
-  static constexpr int kABytes = R * BM * 2, kBBytes = R * kBRow;
+  static constexpr int kBlock = R * 64;                   // 32 columns of a stage
+  static constexpr int kABytes = R * BM * 2, kBBytes = R * kBK * 2;
   static constexpr int kSmem = kABufs * kABytes + kBBufs * kBBytes;
   static constexpr int kCopies = kABytes / 1024;          // copy instructions per stage
   static constexpr int kCPW = (kCopies + kWaves - 1) / kWaves;
@@ -182,8 +200,9 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles) {
   for (int q = 0; q < C::kCPW; ++q) {
     const int ci = wave + C::kWaves * q;              // copy instruction: 1 KB
     if constexpr (WGRAD) {
-      constexpr int AC = BM / 8, RPC = 64 / AC;       // chunks per row, rows per copy
-      const int r = ci * RPC + lane / AC, c = (lane % AC) ^ (swizzle(r) & (AC - 1));
+      // 16 rows of a block of 32 columns, in the order of column_place
+      const int at = ci * 16 + (lane >> 2), p = at % R, c = at / R * 4 + ((lane & 3) ^ place_swap(p));
+      const int r = (p & ~31) + place_row(p & 31);
       aoff[q] = m0 + 8 * c < N ? (r * (int)g.lddc + 8 * c) * 2 : kPast;
     } else {
       constexpr int AC = R / 8, RPC = 64 / AC;
@@ -227,10 +246,9 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles) {
   const int64_t row0 = WGRAD ? r_begin : (int64_t)e * N;
   const uint8_t *bpos = g.b + row0 * drow, *spos = g.b_scales + row0 * srow;
   int bleft = WGRAD ? r_end - r_begin : LAYOUT == kLayoutTiled ? (N + 15) / 16 * 16 : N;
-  uint8_t* const bdst = bbase + br * kBRow;
-  int bchunk[4];
+  int bdst[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) bchunk[i] = (piece_chunk<KIND>(tid, i) ^ swizzle(br)) * 16;
+  for (int i = 0; i < 4; ++i) bdst[i] = column_place(br, piece_chunk<KIND>(tid, i), C::kBlock, true);
   auto row_index = [&](int u) -> int {                 // gather's entry for stage u
     return GATHER ? g.gather[min(r_begin + u * R + br, r_end - 1)] : 0;
   };
@@ -252,22 +270,26 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles) {
   auto store_b = [&](Piece<KIND>& p, bool ok, int buf, int i) {
     if constexpr (GATHER)
       if (i == 0) piece_clear(p, !ok);
-    *reinterpret_cast<u32x4_t*>(bdst + buf * C::kBBytes + bchunk[i]) = piece_convert<KIND>(p, i);
+    *reinterpret_cast<u32x4_t*>(bbase + buf * C::kBBytes + bdst[i]) = piece_convert<KIND>(p, i);
   };
 
-  // ---- fragment addresses in LDS.  A 16-column tile is 32 bytes on, in chunk
-  // bits that the permutation XORs: tile j of the wave is at address ^ (j << 5)
-  // (rows are multiples of 64 bytes kMT or kKT tiles wide, buffers of 1 KB).
+  // ---- fragment addresses in LDS (of the first half in the first step): of
+  // B's tiles, of an even and an odd tile of wgrad's A, of the two steps of
+  // dgrad's A
   const int i16 = lane & 15, gq = lane >> 4;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lptr_t)smem;
-  uint32_t bcols[2], acols[2];
+  const uint32_t col0 = lds0 + column_place(8 * gq + (i16 >> 2), (i16 & 3) >> 1, 0, false) + (i16 & 1) * 8;
+  uint32_t acols[2], bcols[C::kKT];
+#pragma unroll
+  for (int j = 0; j < C::kKT; ++j) {
+    const int block = (wk * C::kKT + j) >> 1;
+    bcols[j] = (col0 ^ ((j & 1) << 5) ^ ((block & 3) << 6)) + kABufs * C::kABytes + block * C::kBlock;
+  }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int r = 8 * gq + 4 * h + (i16 >> 2), s = swizzle(r), x = (i16 & 3) >> 1, y = (i16 & 1) * 8;
-    bcols[h] = lds0 + kABufs * C::kABytes + r * kBRow + (((2 * wk * C::kKT + x) ^ s) << 4) + y;
     if constexpr (WGRAD) {
-      acols[h] = lds0 + r * (BM * 2) + (((2 * wm * kMT + x) ^ (s & (BM / 8 - 1))) << 4) + y;
-    } else {   // A's rows hold the summed index: chunk 4 h + l / 16 for matrix step h
+      acols[h] = (col0 ^ (h << 5)) + wm * (kMT / 2) * C::kBlock;
+    } else {
       const int m = 16 * kMT * wm + i16;
       acols[h] = lds0 + m * (R * 2) + (((4 * h + gq) ^ swizzle_rows<R>(m)) & (R / 8 - 1)) * 16;
     }
@@ -283,23 +305,24 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles) {
   // column tiles; the fragments of a group are read under the group before
   constexpr int kGT = 2, kG = kMT / kGT, kGroups = C::kSteps * kG;
   bf16x8_t fa[2][kGT], fb[2][C::kKT];
+  // (step s is 32 rows on, the second half of a fragment 8 places)
   auto read_a = [&](int buf, int gi) {
     const int s = gi / kG;
 #pragma unroll
     for (int q = 0; q < kGT; ++q) {
       const int t = kGT * (gi % kG) + q;
-      const uint32_t a0 = acols[0] + buf * C::kABytes, a1 = acols[1] + buf * C::kABytes;
       if constexpr (WGRAD)
-        fa[gi & 1][q] = read_columns((trptr_t)((a0 ^ (t << 5)) + s * 64 * BM), (trptr_t)((a1 ^ (t << 5)) + s * 64 * BM));
+        fa[gi & 1][q] = read_columns((trptr_t)(acols[t & 1] + buf * C::kABytes + (t >> 1) * C::kBlock + s * 2048),
+                                     (trptr_t)(acols[1 - (t & 1)] + buf * C::kABytes + (t >> 1) * C::kBlock + s * 2048));
       else
-        fa[gi & 1][q] = as_bf16x8(*(u32x4_lds_t)((s == 0 ? a0 : a1) + t * 32 * R));
+        fa[gi & 1][q] = as_bf16x8(*(u32x4_lds_t)(acols[s] + buf * C::kABytes + t * 32 * R));
     }
   };
   auto read_b = [&](int buf, int s, int set) {
-    const uint32_t b0 = bcols[0] + buf * C::kBBytes, b1 = bcols[1] + buf * C::kBBytes;
 #pragma unroll
     for (int j = 0; j < C::kKT; ++j)
-      fb[set][j] = read_columns((trptr_t)((b0 ^ (j << 5)) + s * 32 * kBRow), (trptr_t)((b1 ^ (j << 5)) + s * 32 * kBRow));
+      fb[set][j] = read_columns((trptr_t)(bcols[j] + buf * C::kBBytes + s * 2048),
+                                (trptr_t)(bcols[j ^ 1] + buf * C::kBBytes + s * 2048));
   };
 
   if (stages > 0) {
