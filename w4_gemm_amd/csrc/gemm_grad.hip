@@ -143,6 +143,41 @@ __device__ __forceinline__ bf16x8_t read_columns(const trptr_t __restrict__ p0, 
   return __builtin_bit_cast(bf16x8_t, v);
 }
 
+// Lanes with l % 16 < 8 (low) hold the rows 0..7 of two pieces a, b, the others
+// rows 8..15.  first: rows 0..7, of a in the low lanes and of b in the others;
+// second: rows 8..15 likewise.
+template <class V>
+__device__ __forceinline__ void exchange8(bool low, V a, V b, V& first, V& second) {
+  const u32x4_t x = __builtin_bit_cast(u32x4_t, a), y = __builtin_bit_cast(u32x4_t, b);
+  u32x4_t f, s;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t other = __builtin_amdgcn_update_dpp(0, low ? y[i] : x[i], 0x128, 0xF, 0xF, false);  // row_ror:8
+    f[i] = low ? x[i] : other;
+    s[i] = low ? other : y[i];
+  }
+  first = __builtin_bit_cast(V, f);
+  second = __builtin_bit_cast(V, s);
+}
+
+// Two bf16 tiles, lane group g = l / 16 with columns 4g .. 4g + 3 of each (two
+// words) -> eight columns: group 0 columns 0..7 of the first tile, 1 of the
+// second, 2 and 3 their columns 8..15.  v_permlane16_swap exchanges the odd
+// groups of one register with the even ones of the other.
+__device__ __forceinline__ u32x4_t exchange16(uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1) {
+  const auto lo = __builtin_amdgcn_permlane16_swap(a0, b0, false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap(a1, b1, false, false);
+  return u32x4_t{lo[0], hi[0], lo[1], hi[1]};
+}
+
+// fp32 weight gradients are far larger than the caches and read by a later
+// kernel: written past them (64 x 2048 x 7168: 1778 -> 1730 us).
+__device__ __forceinline__ void store_f32(float* p, f32x4_t v, int accumulate) {
+  f32x4_t* const o = reinterpret_cast<f32x4_t*>(p);
+  if (accumulate) v += *o;
+  __builtin_nontemporal_store(v, o);
+}
+
 template <bool WGRAD, int KIND, int LAYOUT, bool GATHER, int kWM, int kWK, int kMT>
 struct Kern {
   static constexpr int kWaves = kWM * kWK, kThreads = 64 * kWaves, R = 8 * kWaves;
@@ -162,8 +197,8 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles) {
   using C = Kern<WGRAD, KIND, LAYOUT, GATHER, kWM, kWK, kMT>;
   constexpr int R = C::R, BM = C::BM;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-  uint8_t* const abase = smem;
-  uint8_t* const bbase = smem + kABufs * C::kABytes;
+  uint8_t* const bbase = smem;                        // (first: its offsets fit the instructions)
+  uint8_t* const abase = smem + kBBufs * C::kBBytes;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / kWK, wk = wave % kWK;
 
@@ -283,15 +318,15 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles) {
 #pragma unroll
   for (int j = 0; j < C::kKT; ++j) {
     const int block = (wk * C::kKT + j) >> 1;
-    bcols[j] = (col0 ^ ((j & 1) << 5) ^ ((block & 3) << 6)) + kABufs * C::kABytes + block * C::kBlock;
+    bcols[j] = (col0 ^ ((j & 1) << 5) ^ ((block & 3) << 6)) + block * C::kBlock;
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if constexpr (WGRAD) {
-      acols[h] = (col0 ^ (h << 5)) + wm * (kMT / 2) * C::kBlock;
+      acols[h] = (col0 ^ (h << 5)) + kBBufs * C::kBBytes + wm * (kMT / 2) * C::kBlock;
     } else {
       const int m = 16 * kMT * wm + i16;
-      acols[h] = lds0 + m * (R * 2) + (((4 * h + gq) ^ swizzle_rows<R>(m)) & (R / 8 - 1)) * 16;
+      acols[h] = lds0 + kBBufs * C::kBBytes + m * (R * 2) + (((4 * h + gq) ^ swizzle_rows<R>(m)) & (R / 8 - 1)) * 16;
     }
   }
 
@@ -303,31 +338,38 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles) {
 
   // ---- a stage is kGroups groups of kGT row tiles by all of the wave's
   // column tiles; the fragments of a group are read under the group before
-  constexpr int kGT = 2, kG = kMT / kGT, kGroups = C::kSteps * kG;
-  bf16x8_t fa[2][kGT], fb[2][C::kKT];
+  constexpr int kGT = C::kSteps == 1 && kMT > 4 ? 2 : 1, kG = kMT / kGT, kGroups = C::kSteps * kG;
+  static_assert(kGroups == 2 || kGroups >= 4, "the loads, copies and conversions of a stage come before its last group");
+  bf16x8_t fa[2][kGT], fb[C::kKT];
   // (step s is 32 rows on, the second half of a fragment 8 places)
-  auto read_a = [&](int buf, int gi) {
+  // this lane's addresses in A's buffer of the stage being read (opaque, so
+  // that the constants below stay in the instructions' offsets)
+  uint32_t acur[2];
+  auto set_a = [&](int buf) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      acur[h] = acols[h] + buf * C::kABytes;
+      asm("" : "+v"(acur[h]));
+    }
+  };
+  auto read_a = [&](int gi) {
     const int s = gi / kG;
 #pragma unroll
     for (int q = 0; q < kGT; ++q) {
       const int t = kGT * (gi % kG) + q;
       if constexpr (WGRAD)
-        fa[gi & 1][q] = read_columns((trptr_t)(acols[t & 1] + buf * C::kABytes + (t >> 1) * C::kBlock + s * 2048),
-                                     (trptr_t)(acols[1 - (t & 1)] + buf * C::kABytes + (t >> 1) * C::kBlock + s * 2048));
+        fa[gi & 1][q] = read_columns((trptr_t)(acur[t & 1] + (t >> 1) * C::kBlock + s * 2048),
+                                     (trptr_t)(acur[1 - (t & 1)] + (t >> 1) * C::kBlock + s * 2048));
       else
-        fa[gi & 1][q] = as_bf16x8(*(u32x4_lds_t)(acols[s] + buf * C::kABytes + t * 32 * R));
+        fa[gi & 1][q] = as_bf16x8(*(u32x4_lds_t)(acur[s] + t * 32 * R));
     }
   };
-  auto read_b = [&](int buf, int s, int set) {
-#pragma unroll
-    for (int j = 0; j < C::kKT; ++j)
-      fb[set][j] = read_columns((trptr_t)(bcols[j] + buf * C::kBBytes + s * 2048),
-                                (trptr_t)(bcols[j ^ 1] + buf * C::kBBytes + s * 2048));
+  auto read_b = [&](int buf, int s, int j) {
+    fb[j] = read_columns((trptr_t)(bcols[j] + buf * C::kBBytes + s * 2048),
+                         (trptr_t)(bcols[j ^ 1] + buf * C::kBBytes + s * 2048));
   };
 
   if (stages > 0) {
-    // R = 32: two pieces, loaded two stages ahead.  R = 64: one, loaded again
-    // right after its conversion (a second would not fit the registers).
     constexpr int kSets = C::kSteps == 1 ? 2 : 1;
     Piece<KIND> raw[kSets];
     bool ok[kSets];
@@ -337,76 +379,91 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles) {
       for (int i = 0; i < 4; ++i) idx[i] = row_index(i);
       asm volatile("" : "+v"(idx[2]), "+v"(idx[3]));   // loaded here, ahead of the copies that the loop counts
     }
-    // loads run two stages ahead, past the last stage without reading anything
-    copy_a(0);
+    // Loads run two stages ahead, past the last stage without reading anything.
+    // Within a stage B's go first: loads complete in order, and B's are waited
+    // for a stage earlier than A's copies.
     load_b(raw[0], idx[0], ok[0]);
-    if constexpr (kSets == 2) {
-      copy_a(1);
-      load_b(raw[kSets - 1], idx[1], ok[kSets - 1]);
-    }
+    copy_a(0);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (kSets == 2) load_b(raw[kSets - 1], idx[1], ok[kSets - 1]);
+    else
 #pragma unroll
-    for (int i = 0; i < 4; ++i) store_b(raw[0], ok[0], 0, i);
-    if constexpr (kSets == 1) {
-      copy_a(1);
-      load_b(raw[0], idx[1], ok[0]);
-    }
+      for (int i = 0; i < 4; ++i) store_b(raw[0], ok[0], 0, i);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (kSets == 1) load_b(raw[0], idx[1], ok[0]);
+    __builtin_amdgcn_sched_barrier(0);
+    copy_a(1);
+    __builtin_amdgcn_sched_barrier(0);
     idx[0] = idx[2];
     idx[1] = idx[3];
+    if constexpr (kSets == 2)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) store_b(raw[0], ok[0], 0, i);
     wait_vmcnt_lgkm0<C::kCPW + Piece<KIND>::kLoads>();
     stage_barrier();
-    read_b(0, 0, 0);
-    read_a(0, 0);
+#pragma unroll
+    for (int j = 0; j < C::kKT; ++j) read_b(0, 0, j);
+    set_a(0);
+    read_a(0);
     int abuf = 0;
     auto stage = [&](int u, auto par) {
       constexpr int J = decltype(par)::value;          // u % 2
-      constexpr int kNext = kSets == 2 ? 1 - J : 0, kLoad = kSets == 2 ? J : 0;   // pieces of stages u + 1, u + 2
-      // groups that convert the piece of stage u + 1, and how many eights each
-      constexpr int kConv0 = kSets == 2 ? 1 : 0, kPer = 2, kLoadAt = kSets == 2 ? 0 : 2;
       const int nbuf = abuf == 0 ? 2 : abuf - 1;       // (u + 2) % 3
       const int abuf1 = abuf == 2 ? 0 : abuf + 1;      // (u + 1) % 3
 #pragma unroll
       for (int gi = 0; gi < kGroups; ++gi) {
         if (gi == kGroups - 1) {
-          // copy_a(u + 1) is done once at most copy_a(u + 2) and the loads
-          // after it are outstanding; this wave has read all of stage u and
+          // copy_a(u + 1) is done once at most the loads and copies of stage
+          // u + 2 are outstanding; this wave has read all of stage u and
           // written its part of stage u + 1.  Behind the barrier the buffers of
           // stage u are free and those of stage u + 1 whole.
           wait_vmcnt_lgkm0<C::kCPW + Piece<KIND>::kLoads>();
           stage_barrier();
-          read_b(1 - J, 0, C::kSteps == 1 ? 1 - J : 0);
-          read_a(abuf1, 0);
+          set_a(abuf1);
+          read_a(0);
         } else {
-          if ((gi + 1) % kG == 0) read_b(J, (gi + 1) / kG, (gi + 1) / kG);
-          read_a(abuf, gi + 1);
+          read_a(gi + 1);
         }
         __builtin_amdgcn_sched_barrier(0);
+        // pieces of stages u + 1 and u + 2; groups that load, copy and convert
+        constexpr int kNext = kSets == 2 ? 1 - J : 0, kLoad = kSets == 2 ? J : 0;
+        constexpr int kPer = kGroups == 2 ? 4 : 2, kConv = kSets == 2 && kGroups > 2 ? 1 : 0;
+        constexpr int kLoadAt = kSets == 2 ? 0 : 2, kCopyAt = kGroups == 2 ? 0 : kLoadAt + 1;
         if (gi == kLoadAt) {
-          copy_a(nbuf);
           load_b(raw[kLoad], idx[J], ok[kLoad]);
           if constexpr (GATHER) idx[J] = row_index(u + 4);
         }
-        // the group's products, and a part of stage u + 1's B converted in
-        // their shadow: a product occupies the matrix pipe for 16 cycles, in
-        // which three or four vector instructions issue
-        const int set = C::kSteps == 1 ? J : gi / kG;
+        if (gi == kCopyAt) copy_a(nbuf);
+        // The group's products.  A product occupies the matrix pipe for 16
+        // cycles, in which three or four other instructions issue: the loads'
+        // addresses, the conversion of a part of stage u + 1's B, and in a
+        // step's last group B's next fragments, each as soon as the products
+        // of the one before it are issued.
+        constexpr int kLast = kG - 1;
+        const bool conv = gi >= kConv && gi < kConv + 4 / kPer, last = gi % kG == kLast;
 #pragma unroll
-        for (int q = 0; q < kGT; ++q)
+        for (int j = 0; j < C::kKT; ++j) {
 #pragma unroll
-          for (int j = 0; j < C::kKT; ++j)
-            acc[kGT * (gi % kG) + q][j] = mma16x16x32(fb[set][j], fa[gi & 1][q], acc[kGT * (gi % kG) + q][j]);
-        const bool conv = gi >= kConv0 && gi < kConv0 + 4 / kPer;
+          for (int q = 0; q < kGT; ++q)
+            acc[kGT * (gi % kG) + q][j] = mma16x16x32(fb[j], fa[gi & 1][q], acc[kGT * (gi % kG) + q][j]);
+          if (last) read_b(gi == kGroups - 1 ? 1 - J : J, gi == kGroups - 1 ? 0 : gi / kG + 1, j);
+        }
         if (conv) {
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) store_b(raw[kNext], ok[kNext], 1 - J, kPer * (gi - kConv0) + i);
+          for (int i = 0; i < kPer; ++i) store_b(raw[kNext], ok[kNext], 1 - J, kPer * (gi - kConv) + i);
         }
+        if (last) {
 #pragma unroll
-        for (int q = 0; q < kGT * C::kKT; ++q) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                  // a product
-          if (gi == kLoadAt) {
-            __builtin_amdgcn_sched_group_barrier(0x006, 6, 0);                // addresses
-            __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);                // loads
-          } else if (conv) {
-            __builtin_amdgcn_sched_group_barrier(0x002, 3 * kPer, 0);         // conversions
+          for (int j = 0; j < C::kKT; ++j) {
+            __builtin_amdgcn_sched_group_barrier(0x008, kGT, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < kGT * C::kKT; ++q) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x006, 6, 0);
+            if (!conv) __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);
           }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -422,26 +479,45 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles) {
     wait_vmcnt_lgkm0<0>();  // no copy into LDS may still be running at exit
   }
 
-  // register q of lane l: column 4 (l / 16) + q, row l % 16 of a 16 x 16 tile
+  // register q of lane l holds column 4 (l / 16) + q, row l % 16 of a 16 x 16
+  // tile.  Lanes exchange pieces so that a store instruction covers 128
+  // consecutive bytes of 8 rows, not 64 or 32 of 16: whole cache lines.
   const float gs = KIND == 2 ? *g.gs : 1.0f;
+  const bool low = i16 < 8;
+  const int kw = k0 + 16 * wk * C::kKT;
 #pragma unroll
   for (int t = 0; t < kMT; ++t) {
-    const int m = m0 + 16 * (wm * kMT + t) + i16;
-    if (m >= m_end) continue;
+    const int m = m0 + 16 * (wm * kMT + t) + (i16 & 7);       // and m + 8
     const int64_t row = WGRAD ? (int64_t)e * N + m : m;
+    if (WGRAD && g.out_f32) {
+      float* const o = static_cast<float*>(g.out) + row * g.ldo;
 #pragma unroll
-    for (int j = 0; j < C::kKT; ++j) {
-      const int k = k0 + 16 * (wk * C::kKT + j) + 4 * gq;
-      if (k >= K) continue;
-      f32x4_t v = acc[t][j];
-      if constexpr (KIND == 2) v *= gs;
-      if (WGRAD && g.out_f32) {
-        f32x4_t* o = reinterpret_cast<f32x4_t*>(static_cast<float*>(g.out) + row * g.ldo + k);
-        if (g.accumulate) v += *o;
-        *o = v;
-      } else {
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.out) + row * g.ldo + k) =
-            make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
+      for (int j = 0; j < C::kKT; j += 2) {
+        f32x4_t first, second;                                 // of rows m, m + 8
+        exchange8(low, acc[t][j], acc[t][j + 1], first, second);
+        const int k = kw + 16 * (low ? j : j + 1) + 4 * gq;
+        if (k < K && m < m_end) store_f32(o + k, first, g.accumulate);
+        if (k < K && m + 8 < m_end) store_f32(o + 8 * g.ldo + k, second, g.accumulate);
+      }
+    } else {
+      uint16_t* const o = static_cast<uint16_t*>(g.out) + row * g.ldo;
+#pragma unroll
+      for (int j = 0; j < C::kKT; j += 4) {
+        u32x4_t v[2];                                          // tiles j, j + 1 and j + 2, j + 3
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          f32x4_t a = acc[t][j + 2 * h], c = acc[t][j + 2 * h + 1];
+          if constexpr (KIND == 2) {
+            a *= gs;
+            c *= gs;
+          }
+          v[h] = exchange16(pk_bf16(a[0], a[1]), pk_bf16(a[2], a[3]), pk_bf16(c[0], c[1]), pk_bf16(c[2], c[3]));
+        }
+        u32x4_t first, second;
+        exchange8(low, v[0], v[1], first, second);
+        const int k = kw + 16 * j + (low ? 0 : 32) + 16 * (gq & 1) + 8 * (gq >> 1);
+        if (k < K && m < m_end) *reinterpret_cast<u32x4_t*>(o + k) = first;
+        if (k < K && m + 8 < m_end) *reinterpret_cast<u32x4_t*>(o + 8 * g.ldo + k) = second;
       }
     }
   }
