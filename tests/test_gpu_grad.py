@@ -425,6 +425,72 @@ def test_wgrad_grouped(E, T, P, N, K, seg, kind, gathered):
     _close(dW, 2 * ref, 2 * bound + 2.0 ** -22 * np.abs(ref), "dW twice")
 
 
+@pytest.mark.parametrize("layout", ("rows", "tiled"))
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_dgrad_large_blocks(fmt, layout):
+    """Sizes whose blocks fill the GPU: no part sums, the largest block; ragged rows, two experts and one."""
+    log("dgrad large", fmt, layout)
+    rng = _rng("dgradl")
+    for E, P, N, K in ((1, 2101, 40, 7680), (2, 4211, 48, 4608)):
+        off = np.array([0, 2107, P] if E == 2 else [0, P], np.int32)
+        w, dc = _bf16(rng, E * N, K, std=0.02), _bf16(rng, P, N)
+        W = q4.quantize(w.to(DEV), fmt, layout=layout)
+        wd = oracle.dequant(oracle.quantize(fmt, to_f32(w)))
+        got = (q4.q4_gemm_dgrad(dc.to(DEV), W) if E == 1 else
+               q4.q4_grouped_gemm_dgrad(dc.to(DEV), torch.from_numpy(off).to(DEV), W, N))
+        ref = grad.dgrad(to_f32(dc), off, wd, N)
+        _close(got, ref, _dgrad_bound(to_f32(dc), off, wd, N, ref, fmt in ("mxfp4", "nvfp4")), (E, "dA"))
+
+
+@pytest.mark.parametrize("kind", ("bf16", "mxint8", "mxfp8"))
+def test_wgrad_large_blocks(kind):
+    log("wgrad large", kind)
+    rng = _rng("wgradl")
+    for E, T, P, N, K, gathered in ((1, 301, 301, 4104, 4128, False), (3, 400, 931, 2568, 2336, True)):
+        dc = _bf16(rng, P, N)
+        x = _bf16(rng, T, K)
+        A = x.to(DEV) if kind == "bf16" else q4.quantize(x.to(DEV), kind)
+        a = to_f32(x) if kind == "bf16" else to_f32(q4.q4_dequant(A, torch.empty(T, K, device=DEV)))
+        off = np.array([0, 299, 640, P] if E == 3 else [0, P], np.int32)
+        gather = rng.integers(0, T, P).astype(np.int32) if gathered else None
+        got = (q4.q4_gemm_wgrad(dc.to(DEV), A) if E == 1 else
+               q4.q4_grouped_gemm_wgrad(dc.to(DEV), A, torch.from_numpy(gather).to(DEV), torch.from_numpy(off).to(DEV)))
+        ref = grad.wgrad(to_f32(dc), a, gather, off)
+        _close(got, ref, _wgrad_bound(to_f32(dc), a, gather, off), (E, "dW"))
+
+
+@pytest.mark.parametrize("P,N,K", [(2, 4096, 512), (33, 1040, 1024), (1500, 8, 32), (5000, 24, 96)])
+def test_products_in_parts(P, N, K):
+    """Few blocks and a long sum (dgrad over N, wgrad over P): part sums joined, twice the same bits, the output's other rows
+    left alone."""
+    log("parts", P, N, K)
+    rng = _rng("parts", P, N, K)
+    dc, x = _bf16(rng, P, N), _bf16(rng, P, K)
+    off = np.array([1, P // 2, P - 1], np.int32)
+    offd = torch.from_numpy(off).to(DEV)
+    if K % 128 == 0:
+        w = _bf16(rng, 2 * N, K, std=0.02)
+        W = q4.quantize(w.to(DEV), "nvfp4", layout="tiled")
+        wd = oracle.dequant(oracle.quantize("nvfp4", to_f32(w)))
+        out = torch.full((P, K), 7.0, dtype=BF16, device=DEV)
+        q4.q4_grouped_gemm_dgrad(dc.to(DEV), offd, W, N, dA=out)
+        ref = grad.dgrad(to_f32(dc), off, wd, N)
+        _close(out[1:P - 1], ref[1:P - 1], _dgrad_bound(to_f32(dc), off, wd, N, ref, True)[1:P - 1], "dA")
+        assert torch.all(out[0] == 7.0) and torch.all(out[P - 1] == 7.0)
+    A = q4.quantize(x.to(DEV), "mxint8")
+    a = to_f32(q4.q4_dequant(A, torch.empty(P, K, device=DEV)))
+    ref = grad.wgrad(to_f32(dc), a, None, off)
+    bound = _wgrad_bound(to_f32(dc), a, None, off)
+    got = q4.q4_grouped_gemm_wgrad(dc.to(DEV), A, None, offd)
+    _close(got, ref, bound, "dW")
+    assert torch.equal(got, q4.q4_grouped_gemm_wgrad(dc.to(DEV), A, None, offd))
+    acc = torch.full((2 * N, K), 2.0, device=DEV)
+    q4.q4_grouped_gemm_wgrad(dc.to(DEV), A, None, offd, dW=acc, accumulate=True)
+    _close(acc, 2.0 + ref, bound + 2.0 ** -23 * (2.0 + np.abs(ref)), "dW accumulated")
+    b = q4.q4_grouped_gemm_wgrad(dc.to(DEV), A, None, offd, dW=torch.empty(2 * N, K, dtype=BF16, device=DEV))
+    _close(b, ref, 1.01 * bound + 2.0 ** -8 * np.abs(ref), "dW bf16")
+
+
 def test_wgrad_of_no_rows_is_zero():
     dc = torch.empty(0, 16, dtype=BF16, device=DEV)
     for A in (torch.empty(0, 64, dtype=BF16, device=DEV), q4.empty_q4("mxint8", 0, 64, device=DEV)):

@@ -192,8 +192,8 @@ struct Kern {
 };
 
 template <bool WGRAD, int KIND, int LAYOUT, bool GATHER, int kWM, int kWK, int kMT>
-__global__ void __launch_bounds__(64 * kWM * kWK, 2)
-grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles) {
+__global__ void __launch_bounds__(64 * kWM * kWK, kMT > 4 ? 2 : 3)
+grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles, int splits) {
   using C = Kern<WGRAD, KIND, LAYOUT, GATHER, kWM, kWK, kMT>;
   constexpr int R = C::R, BM = C::BM;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
@@ -204,8 +204,9 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles) {
 
   // block of C: XCD-major, then groups of 4 row tiles
   const int b = blockIdx.x, per = gridDim.x >> 3;
-  const int lin = (b & 7) * per + (b >> 3);
-  if (lin >= tiles) return;
+  const int all = (b & 7) * per + (b >> 3);
+  if (all >= tiles * splits) return;
+  const int split = all / tiles, lin = all - split * tiles;
   const int P = (int)g.P, N = (int)g.N, K = (int)g.K;
   const int per_e = WGRAD ? mtiles * ktiles : tiles;
   int e = WGRAD ? lin / per_e : 0;
@@ -223,7 +224,13 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles) {
     hi = __builtin_amdgcn_readfirstlane(hi);
     m0 = lo;
   }
-  const int r_begin = WGRAD ? lo : 0, r_end = WGRAD ? hi : N;
+  // this workgroup's part of the sum: whole stages
+  int r_begin = WGRAD ? lo : 0, r_end = WGRAD ? hi : N;
+  if (kWM == 1 && splits > 1) {
+    const int part = ((r_end - r_begin + R - 1) / R + splits - 1) / splits * R;
+    r_begin = min(r_begin + split * part, r_end);
+    r_end = min(r_begin + part, r_end);
+  }
   const int stages = (r_end - r_begin + R - 1) / R;
   const int m_end = WGRAD ? N : hi;
 
@@ -248,7 +255,7 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles) {
   // the copies run through the stages in order: position and summed rows left
   // (0 or less past the last stage: the buffer is empty)
   const uint8_t* apos = reinterpret_cast<const uint8_t*>(
-      g.dc + (WGRAD ? (int64_t)r_begin * g.lddc + m0 : (int64_t)m0 * g.lddc));
+      g.dc + (WGRAD ? (int64_t)r_begin * g.lddc + m0 : (int64_t)m0 * g.lddc + r_begin));
   const int64_t astep = WGRAD ? (int64_t)R * g.lddc * 2 : R * 2;
   int aleft = r_end - r_begin;
   auto copy_a = [&](int buf) {
@@ -278,9 +285,9 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles) {
   const PieceAt<KIND> at = piece_at<KIND, LAYOUT>(br, bcols_at, K, (int)g.ldb);
   const int drow = KIND == kBf16Piece ? 2 * (int)g.ldb : WGRAD ? K : K / 2;     // bytes of a row
   const int srow = KIND == kBf16Piece ? 0 : K / PieceScale<KIND>::kCols * PieceScale<KIND>::kBytes;
-  const int64_t row0 = WGRAD ? r_begin : (int64_t)e * N;
+  const int64_t row0 = WGRAD ? r_begin : (int64_t)e * N + r_begin;
   const uint8_t *bpos = g.b + row0 * drow, *spos = g.b_scales + row0 * srow;
-  int bleft = WGRAD ? r_end - r_begin : LAYOUT == kLayoutTiled ? (N + 15) / 16 * 16 : N;
+  int bleft = WGRAD ? r_end - r_begin : (LAYOUT == kLayoutTiled ? (N + 15) / 16 * 16 : N) - r_begin;
   int bdst[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) bdst[i] = column_place(br, piece_chunk<KIND>(tid, i), C::kBlock, true);
@@ -489,7 +496,21 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles) {
   for (int t = 0; t < kMT; ++t) {
     const int m = m0 + 16 * (wm * kMT + t) + (i16 & 7);       // and m + 8
     const int64_t row = WGRAD ? (int64_t)e * N + m : m;
-    if (WGRAD && g.out_f32) {
+    if (kWM == 1 && splits > 1) {                              // a part of the sum, for join_kernel
+      float* const o = g.workspace + ((int64_t)split * (WGRAD ? (int64_t)g.E * N : P) + row) * K;
+#pragma unroll
+      for (int j = 0; j < C::kKT; j += 2) {
+        f32x4_t first, second;
+        exchange8(low, acc[t][j], acc[t][j + 1], first, second);
+        if constexpr (KIND == 2) {
+          first *= gs;
+          second *= gs;
+        }
+        const int k = kw + 16 * (low ? j : j + 1) + 4 * gq;
+        if (k < K && m < m_end) *reinterpret_cast<f32x4_t*>(o + k) = first;
+        if (k < K && m + 8 < m_end) *reinterpret_cast<f32x4_t*>(o + 8 * (int64_t)K + k) = second;
+      }
+    } else if (WGRAD && g.out_f32) {
       float* const o = static_cast<float*>(g.out) + row * g.ldo;
 #pragma unroll
       for (int j = 0; j < C::kKT; j += 2) {
@@ -523,8 +544,71 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles) {
   }
 }
 
+// out[row][k] (+)= the sum of the splits' parts, in order; four columns per
+// thread.  dgrad: only the rows inside the experts' ranges.
+__global__ void __launch_bounds__(256)
+join_kernel(GradArgs g, int64_t rows, int splits, int wgrad) {
+  const int64_t cpr = g.K / 4, c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (c >= rows * cpr) return;
+  const int64_t row = c / cpr, k = (c - row * cpr) * 4;
+  if (!wgrad && g.offsets && (row < g.offsets[0] || row >= g.offsets[g.E])) return;
+  const float* p = g.workspace + row * g.K + k;
+  f32x4_t v{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4_t*>(p + (int64_t)s * rows * g.K);
+  if (wgrad && g.out_f32) {
+    f32x4_t* o = reinterpret_cast<f32x4_t*>(static_cast<float*>(g.out) + row * g.ldo + k);
+    *o = g.accumulate ? *o + v : v;
+  } else {
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.out) + row * g.ldo + k) =
+        make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
+  }
+}
+
+// ---- which block and how many parts ------------------------------------------
+// By the sizes alone (the experts' own row counts are on the device; P / E is
+// their mean).  Measured on 2048 x 7168 experts and dense layers:
+//   256 rows  (8 waves, one workgroup per CU) moves a third less from L2 per
+//             product and converts B half as often as 128 rows (4 waves, two
+//             per CU), but overlaps less and rounds the experts' rows up
+//             further: dgrad 4 x 2048 rows 215 vs 246 us, 8 x 1024 rows 254 vs
+//             241; wgrad (8-bit) 8 x 1024 rows 345 vs 395, 32 x 256 631 vs 660,
+//             64 x 128 940 vs 914.  It needs a block for each of the 256 CUs.
+//   64 rows   wins where rows are few: dgrad 64 x 32 rows 205 vs 251 us, 64 x 8
+//             154 vs 222, 64 x 256 655 vs 609; wgrad 64 x 8 rows 652 vs 735.
+// Where the blocks would leave CUs idle the sum may be split over workgroups
+// that write fp32 parts, joined by a second kernel: into as many as cost least
+// by the measured time of a stage of 32 summed rows (0.45 us in a workgroup that
+// has its CU to itself), of the second launch (8 us with its host time) and of the parts (3.5 TB/s).
+// dgrad 16 x 8192 x 8192: 106 us in one part, 24 in 16; 256 x 8192 x 8192: 111
+// in one, 59 in 4; wgrad 8192 x 2048 x 2048 (8-bit): 182 in one, 100 in 4.
+constexpr int64_t kFill = 512;      // workgroups that fill the GPU: two per CU
+constexpr int64_t kStageNs = 450, kJoinNs = 8000, kJoinBytesPerNs = 3500;
+enum { kBlock64, kBlock128, kBlock256 };
+struct Plan {
+  int block, splits;
+};
+
+Plan plan(bool wgrad, int64_t P, int64_t E, int64_t N, int64_t K) {
+  const int64_t per = P / E, kt = (K + kBK - 1) / kBK;
+  auto tiles = [&](int64_t bm) { return wgrad ? E * ((N + bm - 1) / bm) * kt : ((P + bm - 1) / bm + E - 1) * kt; };
+  if (tiles(256) >= 256 && per >= (wgrad ? 256 : 2048)) return {kBlock256, 1};
+  const bool few = wgrad ? per <= 32 : per <= 128 || tiles(128) < 256;
+  const int64_t most = kFill / tiles(few ? 64 : 128), stages = ((wgrad ? per : N) + 31) / 32;
+  const int64_t part = (wgrad ? E * N : P) * K * 8 / kJoinBytesPerNs;   // writing and reading a part, ns
+  int64_t best = stages * kStageNs;
+  int splits = 1;
+  for (int s = 2; s <= most && s <= stages; ++s) {
+    const int64_t ns = (stages + s - 1) / s * kStageNs + kJoinNs + s * part;
+    if (ns < best) {
+      best = ns;
+      splits = s;
+    }
+  }
+  return {few ? kBlock64 : kBlock128, splits};
+}
+
 template <bool WGRAD, int KIND, int LAYOUT, bool GATHER, int kWM, int kWK, int kMT>
-hipError_t run(const GradArgs& g, hipStream_t stream) {
+hipError_t run(const GradArgs& g, int splits, hipStream_t stream) {
   using C = Kern<WGRAD, KIND, LAYOUT, GATHER, kWM, kWK, kMT>;
   const int64_t kt = (g.K + kBK - 1) / kBK;
   const int64_t mt = WGRAD ? (g.N + C::BM - 1) / C::BM : (g.P + C::BM - 1) / C::BM + g.E - 1;
@@ -532,34 +616,53 @@ hipError_t run(const GradArgs& g, hipStream_t stream) {
   const hipError_t attr = set_max_lds<&grad_kernel<WGRAD, KIND, LAYOUT, GATHER, kWM, kWK, kMT>>(C::kSmem);
   if (attr != hipSuccess) return attr;
   grad_kernel<WGRAD, KIND, LAYOUT, GATHER, kWM, kWK, kMT>
-      <<<(unsigned)((tiles + 7) / 8 * 8), C::kThreads, C::kSmem, stream>>>(g, (int)mt, (int)kt, (int)tiles);
+      <<<(unsigned)((tiles * splits + 7) / 8 * 8), C::kThreads, C::kSmem, stream>>>(g, (int)mt, (int)kt, (int)tiles,
+                                                                                   splits);
+  if (splits > 1) {
+    const int64_t rows = WGRAD ? g.E * g.N : g.P;
+    join_kernel<<<(unsigned)((rows * (g.K / 4) + 255) / 256), 256, 0, stream>>>(g, rows, splits, WGRAD);
+  }
   return hipGetLastError();
+}
+
+template <bool WGRAD, int KIND, int LAYOUT, bool GATHER>
+hipError_t run_plan(const GradArgs& g, hipStream_t stream) {
+  const Plan p = plan(WGRAD, g.P, g.E, g.N, g.K);
+  if (p.block == kBlock64) return run<WGRAD, KIND, LAYOUT, GATHER, 1, 4, 4>(g, p.splits, stream);
+  // (bf16 activations fill the registers of the 256-row block)
+  if (p.block == kBlock128 || KIND == kBf16Piece) return run<WGRAD, KIND, LAYOUT, GATHER, 1, 4, 8>(g, p.splits, stream);
+  if constexpr (KIND != kBf16Piece) return run<WGRAD, KIND, LAYOUT, GATHER, 2, 4, 8>(g, 1, stream);
 }
 
 template <int KIND, int LAYOUT>
 hipError_t run_dgrad(const GradArgs& g, hipStream_t stream) {
-  return run<false, KIND, LAYOUT, false, 1, 4, 8>(g, stream);
+  return run_plan<false, KIND, LAYOUT, false>(g, stream);
 }
 
 template <int KIND>
 hipError_t run_wgrad(const GradArgs& g, hipStream_t stream) {
-  return g.gather ? run<true, KIND, kLayoutRows, true, 1, 4, 8>(g, stream)
-                  : run<true, KIND, kLayoutRows, false, 1, 4, 8>(g, stream);
+  return g.gather ? run_plan<true, KIND, kLayoutRows, true>(g, stream)
+                  : run_plan<true, KIND, kLayoutRows, false>(g, stream);
 }
 
-constexpr int64_t kMaxTiles = ((int64_t)1 << 22);
+size_t parts_bytes(bool wgrad, int64_t P, int64_t E, int64_t N, int64_t K) {
+  const int splits = plan(wgrad, P, E, N, K).splits;
+  return splits > 1 ? (size_t)splits * (size_t)(wgrad ? E * N : P) * (size_t)K * 4 : 0;
+}
+
+constexpr int64_t kMaxTiles = (int64_t)1 << 22;   // of at most 512 threads each
 
 }  // namespace
 
-size_t dgrad_workspace(int64_t, int32_t, int64_t, int64_t) { return 0; }
-size_t wgrad_workspace(int64_t, int32_t, int64_t, int64_t) { return 0; }
+size_t dgrad_workspace(int64_t P, int32_t E, int64_t N, int64_t K) { return parts_bytes(false, P, E, N, K); }
+size_t wgrad_workspace(int64_t P, int32_t E, int64_t N, int64_t K) { return parts_bytes(true, P, E, N, K); }
 
-// (32-row tiles, the smallest of any variant)
+// (64-row tiles, the smallest)
 bool dgrad_fits(int64_t P, int32_t E, int64_t, int64_t K) {
-  return ((P + 31) / 32 + E) * ((K + kBK - 1) / kBK) <= kMaxTiles;
+  return ((P + 63) / 64 + E) * ((K + kBK - 1) / kBK) <= kMaxTiles;
 }
 bool wgrad_fits(int64_t, int32_t E, int64_t N, int64_t K) {
-  return E * ((N + 31) / 32) * ((K + kBK - 1) / kBK) <= kMaxTiles;
+  return E * ((N + 63) / 64) * ((K + kBK - 1) / kBK) <= kMaxTiles;
 }
 
 hipError_t launch_dgrad(int fmt, int layout, const GradArgs& g, hipStream_t stream) {
