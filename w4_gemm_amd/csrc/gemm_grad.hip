@@ -434,8 +434,10 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles, int splits) {
         __builtin_amdgcn_sched_barrier(0);
         // pieces of stages u + 1 and u + 2; groups that load, copy and convert
         constexpr int kNext = kSets == 2 ? 1 - J : 0, kLoad = kSets == 2 ? J : 0;
-        constexpr int kPer = kGroups == 2 ? 4 : 2, kConv = kSets == 2 && kGroups > 2 ? 1 : 0;
-        constexpr int kLoadAt = kSets == 2 ? 0 : 2, kCopyAt = kGroups == 2 ? 0 : kLoadAt + 1;
+        constexpr int kPer = kGroups == 2 || (kSets == 1 && kGroups == 4) ? 4 : 2;
+        constexpr int kConv = kSets == 2 && kGroups > 2 ? 1 : 0;
+        constexpr int kLoadAt = kSets == 2 ? 0 : 4 / kPer, kCopyAt = kGroups == 2 ? 0 : kLoadAt + 1;
+        static_assert(kCopyAt < kGroups - 1 && kConv + 4 / kPer <= kGroups - 1, "before the last group's wait");
         if (gi == kLoadAt) {
           load_b(raw[kLoad], idx[J], ok[kLoad]);
           if constexpr (GATHER) idx[J] = row_index(u + 4);

@@ -23,6 +23,13 @@
 namespace q4 {
 namespace {
 
+// The k rows of every token are more than the caches hold where it matters:
+// written past them.  16385 tokens, 7 of 8 choices kept, 7168 columns: 339 ->
+// 306 us, 1.88 GB at 6.1 TB/s.
+__device__ __forceinline__ void store_past(uint16_t* p, uint4 v) {
+  __builtin_nontemporal_store(__builtin_bit_cast(u32x4_t, v), reinterpret_cast<u32x4_t*>(p));
+}
+
 // ---- sort ------------------------------------------------------------------
 // Workgroups take consecutive chunks of the flattened choices, their 16 waves
 // consecutive parts of a chunk.  With more than one chunk a first kernel
@@ -186,7 +193,7 @@ moe_permute_kernel(const uint16_t* __restrict__ x, int64_t ldx, const int32_t* _
   const uint4 v = *reinterpret_cast<const uint4*>(x + t * ldx + n);
   for (int j = 0; j < k; ++j) {
     const int64_t p = inv[t * k + j];
-    if (p >= 0 && p < P) *reinterpret_cast<uint4*>(xs + p * ldxs + n) = v;
+    if (p >= 0 && p < P) store_past(xs + p * ldxs + n, v);
   }
 }
 
@@ -197,7 +204,7 @@ __device__ __forceinline__ void add8(float (&a)[8], const uint4& v) {
   a[6] += bf16_lo(v.w); a[7] += bf16_hi(v.w);
 }
 
-// Four rows' loads in flight at a time, added in choice order.
+// Eight rows' loads in flight at a time, added in choice order.
 __global__ void __launch_bounds__(kRowThreads)
 moe_permute_backward_kernel(const uint16_t* __restrict__ dxs, int64_t lds_, const int32_t* __restrict__ inv, int k,
                             int64_t K, int64_t P, uint16_t* __restrict__ dx, int64_t ldx, uint32_t slices) {
@@ -205,15 +212,15 @@ moe_permute_backward_kernel(const uint16_t* __restrict__ dxs, int64_t lds_, cons
   const int64_t n = (int64_t)(blockIdx.x % slices) * kRowCols + threadIdx.x * 8;
   if (n >= K) return;
   float a[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  for (int j0 = 0; j0 < k; j0 += 4) {
-    uint4 v[4];
+  for (int j0 = 0; j0 < k; j0 += 8) {
+    uint4 v[8];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < 8; ++q) {
       const int64_t p = j0 + q < k ? inv[t * k + j0 + q] : -1;
       v[q] = p >= 0 && p < P ? *reinterpret_cast<const uint4*>(dxs + p * lds_ + n) : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) add8(a, v[q]);
+    for (int q = 0; q < 8; ++q) add8(a, v[q]);
   }
   *reinterpret_cast<uint4*>(dx + t * ldx + n) =
       make_uint4(pk_bf16(a[0], a[1]), pk_bf16(a[2], a[3]), pk_bf16(a[4], a[5]), pk_bf16(a[6], a[7]));
@@ -254,7 +261,7 @@ moe_combine_backward_kernel(const uint16_t* __restrict__ dout, int64_t ldo, cons
             s = __builtin_fmaf(b, bf16_hi(yw[q]), s);
           }
         }
-        *reinterpret_cast<uint4*>(o + n) = make_uint4(r[0], r[1], r[2], r[3]);
+        store_past(o + n, make_uint4(r[0], r[1], r[2], r[3]));
       }
     }
     if constexpr (GATES) {
@@ -266,11 +273,11 @@ moe_combine_backward_kernel(const uint16_t* __restrict__ dout, int64_t ldo, cons
 }
 
 // ---- the gates' gradient -----------------------------------------------------
-// One wave per token, the E <= 1024 logits in registers.  A token whose logits
+// One wave per token, the E <= 64 * PER logits in registers (PER 1, 4 or 16).  A token whose logits
 // are all -inf has no softmax; its gradient is written as 0.
-constexpr int kLogitsPerLane = 16;
 constexpr int kTopkWaves = 4;
 
+template <int PER>
 __global__ void __launch_bounds__(64 * kTopkWaves)
 moe_topk_backward_kernel(const float* __restrict__ logits, int64_t ld, int64_t T, int E, int k,
                          const int32_t* __restrict__ ids, const float* __restrict__ dw, float* __restrict__ dl,
@@ -278,10 +285,10 @@ moe_topk_backward_kernel(const float* __restrict__ logits, int64_t ld, int64_t T
   const int lane = threadIdx.x & 63;
   const int64_t t = (int64_t)blockIdx.x * kTopkWaves + (threadIdx.x >> 6);
   if (t >= T) return;
-  float v[kLogitsPerLane], d[kLogitsPerLane];
+  float v[PER], d[PER];
   float m = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kLogitsPerLane; ++i) {
+  for (int i = 0; i < PER; ++i) {
     const int e = lane + 64 * i;
     v[i] = e < E ? logits[t * ld + e] : -INFINITY;
     d[i] = 0.0f;
@@ -291,29 +298,32 @@ moe_topk_backward_kernel(const float* __restrict__ logits, int64_t ld, int64_t T
   for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
   float s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kLogitsPerLane; ++i) {
+  for (int i = 0; i < PER; ++i) {
     v[i] = lane + 64 * i < E ? expf(v[i] - m) : 0.0f;
     s += v[i];
   }
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
+  // (k <= 32: lane j holds choice j)
+  const int id = lane < k ? ids[t * k + lane] : -1;
+  const float dwj = lane < k ? dw[t * k + lane] : 0.0f;
   for (int j = 0; j < k; ++j) {
-    const int e = ids[t * k + j];
-    const float g = dw[t * k + j];
+    const int e = __shfl(id, j);
+    const float g = __shfl(dwj, j);
 #pragma unroll
-    for (int i = 0; i < kLogitsPerLane; ++i)
+    for (int i = 0; i < PER; ++i)
       if (e == lane + 64 * i && e < E) d[i] += g;
   }
   float c = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kLogitsPerLane; ++i) {
+  for (int i = 0; i < PER; ++i) {
     v[i] = v[i] / s;
     if (lane + 64 * i < E) c = __builtin_fmaf(v[i], d[i], c);
   }
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) c += __shfl_xor(c, off);
 #pragma unroll
-  for (int i = 0; i < kLogitsPerLane; ++i) {
+  for (int i = 0; i < PER; ++i) {
     const int e = lane + 64 * i;
     if (e < E) dl[t * lddl + e] = m == -INFINITY ? 0.0f : v[i] * (d[i] - c);
   }
@@ -372,7 +382,8 @@ hipError_t launch_moe_topk_backward(const float* logits, int64_t ld, int64_t T, 
                                     const int32_t* ids, const float* dw, float* dl, int64_t lddl,
                                     hipStream_t stream) {
   const unsigned grid = (unsigned)((T + kTopkWaves - 1) / kTopkWaves);
-  moe_topk_backward_kernel<<<grid, 64 * kTopkWaves, 0, stream>>>(logits, ld, T, E, k, ids, dw, dl, lddl);
+  auto kernel = E <= 64 ? moe_topk_backward_kernel<1> : E <= 256 ? moe_topk_backward_kernel<4> : moe_topk_backward_kernel<16>;
+  kernel<<<grid, 64 * kTopkWaves, 0, stream>>>(logits, ld, T, E, k, ids, dw, dl, lddl);
   return hipGetLastError();
 }
 

@@ -33,6 +33,12 @@ __device__ __forceinline__ float sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * g));
 }
 
+// Rows that the next kernel reads from far behind: written past the caches
+// (gradient of 32768 x 2 x 2048: 95 -> 82 us, 540 MB at 6.6 TB/s).
+__device__ __forceinline__ void store_past(uint16_t* p, u32x4_t v) {
+  __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(p));
+}
+
 // 8 values per thread; rows of whole blocks, so four neighbouring lanes are
 // in the loop together and hold one block.
 template <int FMT>
@@ -95,7 +101,7 @@ swiglu_save_kernel(const uint16_t* __restrict__ gu, int64_t ld_gu, int64_t P, in
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       o[j] = pk_bf16(g[2 * j] * sigmoid(g[2 * j]) * u[2 * j], g[2 * j + 1] * sigmoid(g[2 * j + 1]) * u[2 * j + 1]);
-    *reinterpret_cast<uint4*>(h + p * ldh + n) = make_uint4(o[0], o[1], o[2], o[3]);
+    store_past(h + p * ldh + n, u32x4_t{o[0], o[1], o[2], o[3]});
     uint8_t* row = codes + p * 2 * I;
     *reinterpret_cast<uint2*>(row + n) = mx8_encode8<FMT>(gv, gb);
     *reinterpret_cast<uint2*>(row + I + n) = mx8_encode8<FMT>(uv, ub);
@@ -136,13 +142,10 @@ swiglu_backward_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restr
       if constexpr (WITH_H) hv[j] = act * u[j];
     }
     uint16_t* row = dgu + p * lddgu;
-    *reinterpret_cast<uint4*>(row + n) =
-        make_uint4(pk_bf16(dg[0], dg[1]), pk_bf16(dg[2], dg[3]), pk_bf16(dg[4], dg[5]), pk_bf16(dg[6], dg[7]));
-    *reinterpret_cast<uint4*>(row + I + n) =
-        make_uint4(pk_bf16(du[0], du[1]), pk_bf16(du[2], du[3]), pk_bf16(du[4], du[5]), pk_bf16(du[6], du[7]));
+    store_past(row + n, u32x4_t{pk_bf16(dg[0], dg[1]), pk_bf16(dg[2], dg[3]), pk_bf16(dg[4], dg[5]), pk_bf16(dg[6], dg[7])});
+    store_past(row + I + n, u32x4_t{pk_bf16(du[0], du[1]), pk_bf16(du[2], du[3]), pk_bf16(du[4], du[5]), pk_bf16(du[6], du[7])});
     if constexpr (WITH_H)
-      *reinterpret_cast<uint4*>(h + p * ldh + n) =
-          make_uint4(pk_bf16(hv[0], hv[1]), pk_bf16(hv[2], hv[3]), pk_bf16(hv[4], hv[5]), pk_bf16(hv[6], hv[7]));
+      store_past(h + p * ldh + n, u32x4_t{pk_bf16(hv[0], hv[1]), pk_bf16(hv[2], hv[3]), pk_bf16(hv[4], hv[5]), pk_bf16(hv[6], hv[7])});
   }
 }
 
