@@ -56,30 +56,28 @@ class _There:
         return self.outer.__exit__(*exc)
 
 
-def _tensors(args):
-    for name, t in args:
-        if isinstance(t, Q4Tensor):
-            yield name + ".codes", t.codes
-            yield name + ".scales", t.scales
-            if t.global_scale is not None:
-                yield name + ".global_scale", t.global_scale
-        elif t is not None:
-            yield name, t
-
-
 def _place(stream, *args):
     """Checks that every (name, tensor) is on the GPU, all on one; `with` it the
     call is on that device and the stream it runs on, as (device, stream) ready
     for torch and for the library."""
     where = None
-    for name, t in _tensors(args):
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a GPU tensor (got device {t.device})")
-        i = t.get_device()
-        if where is None:
-            where = i
-        elif i != where:
-            raise ValueError(f"{name} must be on cuda:{where} like the other tensors (got cuda:{i})")
+    for name, t in args:
+        if t is None:
+            continue
+        if isinstance(t, Q4Tensor):
+            parts = ((".codes", t.codes), (".scales", t.scales), (".global_scale", t.global_scale))
+        else:
+            parts = (("", t),)
+        for part, x in parts:
+            if x is None:
+                continue
+            if not x.is_cuda:
+                raise ValueError(f"{name}{part} must be a GPU tensor (got device {x.device})")
+            i = x.get_device()
+            if where is None:
+                where = i
+            elif i != where:
+                raise ValueError(f"{name}{part} must be on cuda:{where} like the other tensors (got cuda:{i})")
     if stream is None:
         if where == torch.cuda.current_device():
             return _Here(where, _raw_stream(where))
@@ -133,8 +131,8 @@ def q4_moe_topk(logits: torch.Tensor, k: int, stream=None) -> Tuple[torch.Tensor
     _matrix(logits, "logits", F32, 0, 0)
     T, E = logits.shape
     with _place(stream, ("logits", logits)) as (dev, s):
-        ids = torch.empty((T, k), dtype=I32, device=dev)
-        weights = torch.empty((T, k), dtype=F32, device=dev)
+        ids = torch.empty(T, k, dtype=I32, device=dev)
+        weights = torch.empty(T, k, dtype=F32, device=dev)
         _check(lib().q4_moe_topk(_ptr(logits), max(logits.stride(0), E), T, E, k, _ptr(ids), _ptr(weights), s),
                "q4_moe_topk")
     return ids, weights
@@ -154,7 +152,7 @@ def q4_moe_topk_backward(logits: torch.Tensor, ids: torch.Tensor, dweights: torc
         _matrix(dlogits, "dlogits", F32, T, E)
     with _place(stream, ("logits", logits), ("ids", ids), ("dweights", dweights), ("dlogits", dlogits)) as (dev, s):
         if dlogits is None:
-            dlogits = torch.empty((T, E), dtype=F32, device=dev)
+            dlogits = torch.empty(T, E, dtype=F32, device=dev)
         _check(lib().q4_moe_topk_backward(_ptr(logits), max(logits.stride(0), E), T, E, k, _ptr(ids), _ptr(dweights),
                                           _ptr(dlogits), max(dlogits.stride(0), E), s), "q4_moe_topk_backward")
     return dlogits
@@ -180,7 +178,7 @@ def q4_moe_sort(ids: torch.Tensor, experts: int, offsets: Optional[torch.Tensor]
         if gather is None:
             gather = torch.empty(T * k, dtype=I32, device=dev)
         if inv is None:
-            inv = torch.empty((T, k), dtype=I32, device=dev)
+            inv = torch.empty(T, k, dtype=I32, device=dev)
         _check(lib().q4_moe_sort(_ptr(ids), T, k, experts, _ptr(offsets), _ptr(gather), _ptr(inv), _ptr(ws), need, s),
                "q4_moe_sort")
     return offsets, gather, inv
@@ -199,7 +197,7 @@ def q4_moe_permute(x: torch.Tensor, inv: torch.Tensor, xs: Optional[torch.Tensor
         _matrix(xs, "xs", BF16, 0, K, exact_cols=True)
     with _place(stream, ("x", x), ("inv", inv), ("xs", xs)) as (dev, s):
         if xs is None:
-            xs = torch.empty((T * k, K), dtype=BF16, device=dev)
+            xs = torch.empty(T * k, K, dtype=BF16, device=dev)
         _check(lib().q4_moe_permute(_ptr(x), _ld(x), _ptr(inv), T, k, K, xs.shape[0], _ptr(xs), _ld(xs), s),
                "q4_moe_permute")
     return xs
@@ -215,7 +213,7 @@ def q4_moe_permute_backward(dxs: torch.Tensor, inv: torch.Tensor, dx: Optional[t
         _matrix(dx, "dx", BF16, T, K, exact_cols=True)
     with _place(stream, ("dxs", dxs), ("inv", inv), ("dx", dx)) as (dev, s):
         if dx is None:
-            dx = torch.empty((T, K), dtype=BF16, device=dev)
+            dx = torch.empty(T, K, dtype=BF16, device=dev)
         _check(lib().q4_moe_permute_backward(_ptr(dxs), _ld(dxs), _ptr(inv), T, k, K, dxs.shape[0], _ptr(dx), _ld(dx),
                                              s), "q4_moe_permute_backward")
     return dx
@@ -254,9 +252,9 @@ def q4_moe_combine_backward(dout: torch.Tensor, y: Optional[torch.Tensor], inv: 
     with _place(stream, ("dout", dout), ("y", y), ("inv", inv), ("weights", weights), ("dy", dy),
                 ("dweights", dweights)) as (dev, s):
         if dy is None:
-            dy = torch.empty((P, N), dtype=BF16, device=dev)
+            dy = torch.empty(P, N, dtype=BF16, device=dev)
         if gates and dweights is None:
-            dweights = torch.empty((T, k), dtype=F32, device=dev)
+            dweights = torch.empty(T, k, dtype=F32, device=dev)
         _check(lib().q4_moe_combine_backward(_ptr(dout), _ld(dout), _ptr(y) if gates else None,
                                              _ld(y) if gates else 0, _ptr(inv), _ptr(weights), T, k, N, P, _ptr(dy),
                                              _ld(dy), _ptr(dweights), s), "q4_moe_combine_backward")
@@ -282,7 +280,7 @@ def q4_swiglu_save(gu: torch.Tensor, inter: int, saved: Q4Tensor, h: Optional[to
         _matrix(h, "h", BF16, P, inter)
     with _place(stream, ("gu", gu), ("saved", saved), ("h", h)) as (dev, s):
         if h is None:
-            h = torch.empty((P, inter), dtype=BF16, device=dev)
+            h = torch.empty(P, inter, dtype=BF16, device=dev)
         d = saved.c()
         _check(lib().q4_swiglu_save(_ptr(gu), _ld(gu), P, inter, _ptr(h), _ld(h), ctypes.byref(d), s),
                "q4_swiglu_save")
@@ -309,7 +307,7 @@ def q4_swiglu_backward(gu: Union[torch.Tensor, Q4Tensor], dh: torch.Tensor, dgu:
         _matrix(h, "h", BF16, P, inter)
     with _place(stream, ("gu", gu), ("dh", dh), ("dgu", dgu), ("h", h)) as (dev, s):
         if dgu is None:
-            dgu = torch.empty((P, 2 * inter), dtype=BF16, device=dev)
+            dgu = torch.empty(P, 2 * inter, dtype=BF16, device=dev)
         if P and inter:
             d = gu.c() if q else None
             _check(lib().q4_swiglu_backward(None if q else _ptr(gu), 0 if q else _ld(gu),
@@ -328,7 +326,7 @@ def q4_gemm_dgrad(dC: torch.Tensor, W: Q4Tensor, dA: Optional[torch.Tensor] = No
         _matrix(dA, "dA", BF16, M, W.cols)
     with _place(stream, ("W", W), ("dC", dC), ("dA", dA)) as (dev, s):
         if dA is None:
-            dA = torch.empty((M, W.cols), dtype=BF16, device=dev)
+            dA = torch.empty(M, W.cols, dtype=BF16, device=dev)
         ws, need = _workspace("q4_dgrad_workspace", dev, M, 1, W.rows, W.cols)
         wd = W.c()
         _check(lib().q4_gemm_dgrad(M, _ptr(dC), _ld(dC), ctypes.byref(wd), _ptr(dA), _ld(dA), _ptr(ws), need, s),
@@ -353,7 +351,7 @@ def q4_grouped_gemm_dgrad(dC: torch.Tensor, offsets: torch.Tensor, W: Q4Tensor, 
         _matrix(dA, "dA", BF16, P, W.cols)
     with _place(stream, ("W", W), ("dC", dC), ("offsets", offsets), ("dA", dA)) as (dev, s):
         if dA is None:
-            dA = torch.empty((P, W.cols), dtype=BF16, device=dev)
+            dA = torch.empty(P, W.cols, dtype=BF16, device=dev)
         ws, need = _workspace("q4_dgrad_workspace", dev, P, E, N, W.cols)
         wd = W.c()
         _check(lib().q4_grouped_gemm_dgrad(_ptr(dC), _ld(dC), _ptr(offsets), E, P, ctypes.byref(wd), N, _ptr(dA),
@@ -400,7 +398,7 @@ def q4_gemm_wgrad(dC: torch.Tensor, A: Union[torch.Tensor, Q4Tensor], dW: Option
         raise ValueError(f"A must have {M} rows like dC (got {T})")
     with _place(stream, ("dC", dC), ("A", A), ("dW", dW)) as (dev, s):
         if dW is None:
-            dW = torch.empty((N, K), dtype=F32, device=dev)
+            dW = torch.empty(N, K, dtype=F32, device=dev)
         ws, need = _workspace("q4_wgrad_workspace", dev, M, 1, N, K)
         if N and K:
             if not M:
@@ -431,7 +429,7 @@ def q4_grouped_gemm_wgrad(dC: torch.Tensor, A: Union[torch.Tensor, Q4Tensor], ga
         raise ValueError(f"A must have at least {P} rows like dC (got {T})")
     with _place(stream, ("dC", dC), ("A", A), ("gather", gather), ("offsets", offsets), ("dW", dW)) as (dev, s):
         if dW is None:
-            dW = torch.empty((E * N, K), dtype=F32, device=dev)
+            dW = torch.empty(E * N, K, dtype=F32, device=dev)
         ws, need = _workspace("q4_wgrad_workspace", dev, P, E, N, K)
         if E and N and K:
             if not P or not T:
@@ -469,11 +467,11 @@ def moe_layer_save(x: torch.Tensor, logits: torch.Tensor, k: int, W_gu: Q4Tensor
         ids, weights = q4_moe_topk(logits, k)
         r = Routing(ids, weights, *q4_moe_sort(ids, E))
         P = T * k
-        gu = torch.empty((P, 2 * inter), dtype=BF16, device=dev)
+        gu = torch.empty(P, 2 * inter, dtype=BF16, device=dev)
         q4_grouped_gemm(x, r.gather, r.offsets, W_gu, 2 * inter, gu)
         gu_q = empty_q4(fmt, P, 2 * inter, device=dev)
         h = q4_swiglu_save(gu, inter, gu_q)
-        y = torch.empty((P, K), dtype=BF16, device=dev)
+        y = torch.empty(P, K, dtype=BF16, device=dev)
         q4_grouped_gemm(h, None, r.offsets, W_down, K, y)
         x_q = q4_quantize(x, empty_q4(fmt, T, K, device=dev)) if weights_grad else None
         return q4_moe_combine(y, r), MoESaved(r, logits, x_q, gu_q, y, inter)
@@ -491,7 +489,7 @@ def moe_layer_backward(saved: MoESaved, dout: torch.Tensor, W_gu: Q4Tensor, W_do
         dy, dw = q4_moe_combine_backward(dout, saved.y, r.inv, r.weights)
         dlogits = q4_moe_topk_backward(saved.logits, r.ids, dw)
         dh = q4_grouped_gemm_dgrad(dy, r.offsets, W_down, K)
-        h = torch.empty((dy.shape[0], inter), dtype=BF16, device=dev) if saved.x is not None else None
+        h = torch.empty(dy.shape[0], inter, dtype=BF16, device=dev) if saved.x is not None else None
         dgu = q4_swiglu_backward(saved.gu, dh, h=h)
         dxs = q4_grouped_gemm_dgrad(dgu, r.offsets, W_gu, 2 * inter)
         dx = q4_moe_permute_backward(dxs, r.inv)
