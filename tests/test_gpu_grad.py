@@ -516,6 +516,15 @@ def test_products_pass_nan_and_inf_on_where_they_belong():
     rows[[32, 40]] = False
     assert torch.equal(got[rows], clean[rows]) and not torch.isfinite(got[32].float()).all()
     assert torch.isnan(got[40].float()).all()
+    # nothing of an earlier call's values is left where a sum or a block ends
+    for t in (dc, bad):
+        q4.q4_grouped_gemm_dgrad(torch.full_like(dc, float("nan")), off, W, N)
+        again = q4.q4_grouped_gemm_dgrad(t, off, W, N)
+        assert torch.equal(again[rows], clean[rows])
+    xq = q4.quantize(_bf16(rng, P, K).to(DEV), "mxint8")
+    first = q4.q4_grouped_gemm_wgrad(dc, xq, None, off)
+    q4.q4_grouped_gemm_wgrad(torch.full_like(dc, float("nan")), xq, None, off)
+    assert torch.equal(q4.q4_grouped_gemm_wgrad(dc, xq, None, off), first)
     x = _bf16(rng, P, K)
     x[34, 3] = float("inf")                     # expert 2
     for A, wide in ((x.to(DEV), 1), (q4.quantize(x.to(DEV), "mxint8"), 32), (q4.quantize(x.to(DEV), "mxfp8"), 32)):
@@ -572,6 +581,22 @@ def test_moe_layer_step(fmt_w, fmt_a):
     dx2, dl2, n1, n2 = q4.moe_layer_backward(q4.moe_layer_save(xd, ld, k, Wgu, Wd, inter, fmt=fmt_a, weights_grad=False)[1],
                                              dout.to(DEV), Wgu, Wd)
     assert n1 is None and n2 is None and torch.equal(dx2, dx) and torch.equal(dl2, dl)
+
+
+def test_moe_layer_step_without_tokens_and_with_one():
+    _, _, x, lg, Wgu, Wd, dout = _layer("mxfp4", "mxint8", seed=3)
+    for T in (0, 1):
+        out, saved = q4.moe_layer_save(x[:T].to(DEV), lg[:T].to(DEV), 2, Wgu, Wd, 256)
+        dx, dl, a, b = q4.moe_layer_backward(saved, dout[:T].to(DEV), Wgu, Wd)
+        assert out.shape == dx.shape == (T, 512) and dl.shape == (T, 6)
+        assert a.shape == (6 * 512, 512) and b.shape == (6 * 512, 256)
+        used = torch.zeros(6, dtype=torch.bool)
+        used[saved.r.ids.cpu().long().flatten()] = True
+        for g in (a, b):
+            nz = g.reshape(6, -1).abs().sum(1).cpu() > 0
+            assert torch.equal(nz, used)
+        for t in (out, dx, dl, a, b):
+            assert torch.isfinite(t.float()).all()
 
 
 def test_moe_layer_step_in_a_graph():

@@ -130,6 +130,8 @@ def test_products_refuse():
     for bad in (dict(dc=ODD), dict(off=ODD + 1), dict(da=ODD), dict(ld=36)):
         assert g(**bad) == ALIGN, bad
     assert g(W=_d(q4.FP8_ROW)) == FMT
+    far = 1 << 22
+    assert g(ld=far) == SHAPE and g(W=_d(q4.MXFP4, cols=far), lda=far) == SHAPE and g(P=1 << 29) == SHAPE
     w = lambda **k: L.q4_grouped_gemm_wgrad(*[{**dict(dc=A16, ld=32, a=None, lda=0, q=None, T=64, gather=A16, off=A16, E=2, P=8,  # noqa: E731,E501
                                                       N=32, K=256, dw=A16, dt=1, ldw=256, acc=0, ws=A16, n=big, s=None), **k}[x]
                                               for x in ("dc", "ld", "a", "lda", "q", "T", "gather", "off", "E", "P", "N", "K", "dw",
@@ -140,6 +142,9 @@ def test_products_refuse():
     assert w(q=q, dt=2) == FMT and w(q=q, dt=0, acc=1) == FMT
     for bad in (dict(q=q, T=63), dict(q=q, K=128), dict(q=q, N=12), dict(q=q, ldw=248), dict(q=q, gather=None, P=65, ld=32),
                 dict(a=A16, lda=256, K=252), dict(a=A16, lda=248)):
+        assert w(**bad) == SHAPE, bad
+    for bad in (dict(q=q, ld=far), dict(a=A16, lda=far), dict(a=A16, lda=far, K=far, ldw=far), dict(q=q, P=(1 << 30) + 8),
+                dict(q=q, N=1 << 31), dict(q=q, N=1 << 28)):
         assert w(**bad) == SHAPE, bad
     for bad in (dict(q=q, dc=None), dict(q=q, off=None), dict(q=q, dw=None)):
         assert w(**bad) == NULL, bad

@@ -673,7 +673,7 @@ q4_status dgrad(const void* dC, int64_t lddc, const int32_t* offsets, int32_t E,
   if (need && !aligned(workspace, 16)) return Q4_ERR_ALIGN;
   q4::GradArgs g{};
   g.dc = static_cast<const uint16_t*>(dC);
-  g.lddc = lddc;
+  g.lddc = P > 1 ? lddc : N;  // (a single row's stride is never used)
   g.offsets = offsets;
   g.E = E;
   g.P = P;
@@ -724,7 +724,7 @@ q4_status wgrad(const void* dC, int64_t lddc, const void* A_bf16, int64_t lda, c
   if (need && !aligned(workspace, 16)) return Q4_ERR_ALIGN;
   q4::GradArgs g{};
   g.dc = static_cast<const uint16_t*>(dC);
-  g.lddc = lddc;
+  g.lddc = P > 1 ? lddc : N;  // (a single row's stride is never used)
   g.offsets = offsets;
   g.gather = gather;
   g.E = E;
@@ -734,7 +734,7 @@ q4_status wgrad(const void* dC, int64_t lddc, const void* A_bf16, int64_t lda, c
   g.T = T;
   g.b = static_cast<const uint8_t*>(A_q ? A_q->codes : A_bf16);
   g.b_scales = A_q ? static_cast<const uint8_t*>(A_q->scales) : nullptr;
-  g.ldb = lda;
+  g.ldb = T > 1 ? lda : K;
   g.out = dW;
   g.ldo = lddw;
   g.out_f32 = dw_dtype;

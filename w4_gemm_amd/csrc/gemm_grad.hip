@@ -653,18 +653,19 @@ size_t parts_bytes(bool wgrad, int64_t P, int64_t E, int64_t N, int64_t K) {
 }
 
 constexpr int64_t kMaxTiles = (int64_t)1 << 22;   // of at most 512 threads each
+constexpr int64_t kMaxSum = (int64_t)1 << 30;
 
 }  // namespace
 
 size_t dgrad_workspace(int64_t P, int32_t E, int64_t N, int64_t K) { return parts_bytes(false, P, E, N, K); }
 size_t wgrad_workspace(int64_t P, int32_t E, int64_t N, int64_t K) { return parts_bytes(true, P, E, N, K); }
 
-// (64-row tiles, the smallest)
-bool dgrad_fits(int64_t P, int32_t E, int64_t, int64_t K) {
-  return ((P + 63) / 64 + E) * ((K + kBK - 1) / kBK) <= kMaxTiles;
+// (64-row tiles, the smallest; the summed index plus a stage stays an int)
+bool dgrad_fits(int64_t P, int32_t E, int64_t N, int64_t K) {
+  return N <= kMaxSum && ((P + 63) / 64 + E) * ((K + kBK - 1) / kBK) <= kMaxTiles;
 }
-bool wgrad_fits(int64_t, int32_t E, int64_t N, int64_t K) {
-  return E * ((N + 63) / 64) * ((K + kBK - 1) / kBK) <= kMaxTiles;
+bool wgrad_fits(int64_t P, int32_t E, int64_t N, int64_t K) {
+  return P <= kMaxSum && N <= kMaxSum && E * ((N + 63) / 64) * ((K + kBK - 1) / kBK) <= kMaxTiles;
 }
 
 hipError_t launch_dgrad(int fmt, int layout, const GradArgs& g, hipStream_t stream) {
