@@ -106,9 +106,15 @@ __device__ __forceinline__ bool find_tile(const int32_t* offsets, int E, int P, 
 // pair of groups lie together (8 rows, 512 bytes) and one of their fours has
 // the halves of its 64 bytes swapped: 8 x 32 bytes on 256 bytes of banks; which
 // of them alternates with h, so that a wave that writes one chunk of rows 0..15
-// does not meet itself either.  Steps and (but for `turn`) pairs of tiles are
-// constant offsets; an odd tile and the second half are address ^ 32.  turn: the rows of block b are XORed with b % 4, so that
-// threads that write neighbouring blocks of one row meet no bank twice.
+// does not meet itself either.  Steps and pairs of tiles are constant offsets;
+// an odd tile and the second half are address ^ 32.
+//
+// of_b: B's tiles are not 16 consecutive columns.  So that the epilogue's stores
+// need few exchanges, tile j of a wave's 64 columns takes two chunks 32 columns
+// apart, j / 2 + 2 (j % 2) of either block, and the chunks of an odd block trade
+// places with their neighbours: again 256 bytes of banks.  The rows of block b
+// are XORed with b % 4, so that threads that write neighbouring blocks of one
+// row meet no bank twice.
 __device__ __forceinline__ int row_place(int r) {        // r in 0..31 -> 0..31
   return (r & 16) | ((r & 4) << 1) | ((r & 8) >> 1) | (r & 3);
 }
@@ -116,9 +122,9 @@ __device__ __forceinline__ int place_row(int p) {        // its inverse
   return (p & 16) | ((p & 4) << 1) | ((p & 8) >> 1) | (p & 3);
 }
 __device__ __forceinline__ int place_swap(int p) { return ((p >> 1) ^ (p >> 2)) & 2; }   // on the chunk's number
-__device__ __forceinline__ int column_place(int r, int c, int block_bytes, bool turn) {
-  const int p = row_place(r & 31) ^ (turn ? (c >> 2) & 3 : 0);
-  return (c >> 2) * block_bytes + ((r & ~31) + p) * 64 + (((c & 3) ^ place_swap(p)) << 4);
+__device__ __forceinline__ int column_place(int r, int c, int block_bytes, bool of_b) {
+  const int block = c >> 2, p = row_place(r & 31) ^ (of_b ? block & 3 : 0);
+  return block * block_bytes + ((r & ~31) + p) * 64 + (((c & 3) ^ place_swap(p) ^ (of_b ? block & 1 : 0)) << 4);
 }
 
 // Chunk permutation of dgrad's A, whose rows of R summed values are read by
@@ -143,31 +149,22 @@ __device__ __forceinline__ bf16x8_t read_columns(const trptr_t __restrict__ p0, 
   return __builtin_bit_cast(bf16x8_t, v);
 }
 
-// Lanes with l % 16 < 8 (low) hold the rows 0..7 of two pieces a, b, the others
-// rows 8..15.  first: rows 0..7, of a in the low lanes and of b in the others;
-// second: rows 8..15 likewise.
-template <class V>
-__device__ __forceinline__ void exchange8(bool low, V a, V b, V& first, V& second) {
-  const u32x4_t x = __builtin_bit_cast(u32x4_t, a), y = __builtin_bit_cast(u32x4_t, b);
-  u32x4_t f, s;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t other = __builtin_amdgcn_update_dpp(0, low ? y[i] : x[i], 0x128, 0xF, 0xF, false);  // row_ror:8
-    f[i] = low ? x[i] : other;
-    s[i] = low ? other : y[i];
-  }
-  first = __builtin_bit_cast(V, f);
-  second = __builtin_bit_cast(V, s);
+// Exchanges between lanes and registers: a lane bit trades places with the bit
+// that tells a from b.  Bit 0 or 1 of the lane (within its quad), `set` in this
+// lane; bit 4 (v_permlane16_swap exchanges the odd groups of 16 lanes of one
+// register with the even ones of the other).
+template <int BIT>
+__device__ __forceinline__ void swap_quad(bool set, uint32_t& a, uint32_t& b) {
+  constexpr int kPerm = BIT == 0 ? 0xB1 : 0x4E;        // quad_perm: lane ^ 1, lane ^ 2
+  const uint32_t from_b = __builtin_amdgcn_update_dpp(0, b, kPerm, 0xF, 0xF, true);
+  const uint32_t from_a = __builtin_amdgcn_update_dpp(0, a, kPerm, 0xF, 0xF, true);
+  a = set ? from_b : a;
+  b = set ? b : from_a;
 }
-
-// Two bf16 tiles, lane group g = l / 16 with columns 4g .. 4g + 3 of each (two
-// words) -> eight columns: group 0 columns 0..7 of the first tile, 1 of the
-// second, 2 and 3 their columns 8..15.  v_permlane16_swap exchanges the odd
-// groups of one register with the even ones of the other.
-__device__ __forceinline__ u32x4_t exchange16(uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1) {
-  const auto lo = __builtin_amdgcn_permlane16_swap(a0, b0, false, false);
-  const auto hi = __builtin_amdgcn_permlane16_swap(a1, b1, false, false);
-  return u32x4_t{lo[0], hi[0], lo[1], hi[1]};
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
 }
 
 // fp32 weight gradients are far larger than the caches and read by a later
@@ -322,11 +319,11 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles, int splits) {
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lptr_t)smem;
   const uint32_t col0 = lds0 + column_place(8 * gq + (i16 >> 2), (i16 & 3) >> 1, 0, false) + (i16 & 1) * 8;
   uint32_t acols[2], bcols[C::kKT];
+  static_assert(C::kKT == 4, "a wave's columns are two blocks");
 #pragma unroll
-  for (int j = 0; j < C::kKT; ++j) {
-    const int block = (wk * C::kKT + j) >> 1;
-    bcols[j] = (col0 ^ ((j & 1) << 5) ^ ((block & 3) << 6)) + block * C::kBlock;
-  }
+  for (int j = 0; j < C::kKT; ++j)
+    bcols[j] = lds0 + (i16 & 1) * 8 +
+               column_place(8 * gq + (i16 >> 2), 4 * (2 * wk + ((i16 & 3) >> 1)) + (j >> 1) + 2 * (j & 1), C::kBlock, true);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if constexpr (WGRAD) {
@@ -488,59 +485,78 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles, int splits) {
     wait_vmcnt_lgkm0<0>();  // no copy into LDS may still be running at exit
   }
 
-  // register q of lane l holds column 4 (l / 16) + q, row l % 16 of a 16 x 16
-  // tile.  Lanes exchange pieces so that a store instruction covers 128
-  // consecutive bytes of 8 rows, not 64 or 32 of 16: whole cache lines.
+  // Register q of tile j in lane 16 g + 4 a + b holds row 4 a + b and, of the
+  // wave's 64 columns, 32 (g / 2) + 16 (j % 2) + 8 (j / 2) + 4 (g % 2) + q.
+  // Stores go out at four lanes (one quad) per cycle if these lie in one 64-byte
+  // piece, else at a quarter of that (a CU: 151 against 35 GB/s), so lanes trade
+  // registers until quads do: fp32, 4 rows of 256 bytes per instruction, column
+  // 16 g + 4 b + q; bf16, 8 rows of 128 bytes.
   const float gs = KIND == 2 ? *g.gs : 1.0f;
-  const bool low = i16 < 8;
-  const int kw = k0 + 16 * wk * C::kKT;
+  const bool odd = lane & 1, upper = lane & 2;
+  const int kw = k0 + 64 * wk;
+  const bool f32 = (kWM == 1 && splits > 1) || (WGRAD && g.out_f32);
 #pragma unroll
   for (int t = 0; t < kMT; ++t) {
-    const int m = m0 + 16 * (wm * kMT + t) + (i16 & 7);       // and m + 8
-    const int64_t row = WGRAD ? (int64_t)e * N + m : m;
-    if (kWM == 1 && splits > 1) {                              // a part of the sum, for join_kernel
-      float* const o = g.workspace + ((int64_t)split * (WGRAD ? (int64_t)g.E * N : P) + row) * K;
+    const int mt0 = m0 + 16 * (wm * kMT + t) + (lane & 12);
+    if constexpr (KIND == 2)
 #pragma unroll
-      for (int j = 0; j < C::kKT; j += 2) {
-        f32x4_t first, second;
-        exchange8(low, acc[t][j], acc[t][j + 1], first, second);
-        if constexpr (KIND == 2) {
-          first *= gs;
-          second *= gs;
-        }
-        const int k = kw + 16 * (low ? j : j + 1) + 4 * gq;
-        if (k < K && m < m_end) *reinterpret_cast<f32x4_t*>(o + k) = first;
-        if (k < K && m + 8 < m_end) *reinterpret_cast<f32x4_t*>(o + 8 * (int64_t)K + k) = second;
+      for (int j = 0; j < 4; ++j) acc[t][j] *= gs;
+    if (f32) {
+      u32x4_t v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = __builtin_bit_cast(u32x4_t, acc[t][j]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t x[4] = {v[0][q], v[1][q], v[2][q], v[3][q]};
+        swap16(x[0], x[1]);
+        swap16(x[2], x[3]);
+        swap_quad<0>(odd, x[0], x[1]);
+        swap_quad<0>(odd, x[2], x[3]);
+        swap_quad<1>(upper, x[0], x[2]);
+        swap_quad<1>(upper, x[1], x[3]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j][q] = x[j];
       }
-    } else if (WGRAD && g.out_f32) {
-      float* const o = static_cast<float*>(g.out) + row * g.ldo;
+      const int k = kw + 16 * gq + 4 * (lane & 3);
 #pragma unroll
-      for (int j = 0; j < C::kKT; j += 2) {
-        f32x4_t first, second;                                 // of rows m, m + 8
-        exchange8(low, acc[t][j], acc[t][j + 1], first, second);
-        const int k = kw + 16 * (low ? j : j + 1) + 4 * gq;
-        if (k < K && m < m_end) store_f32(o + k, first, g.accumulate);
-        if (k < K && m + 8 < m_end) store_f32(o + 8 * g.ldo + k, second, g.accumulate);
+      for (int j = 0; j < 4; ++j) {                            // rows 4 a + j
+        const f32x4_t o4 = __builtin_bit_cast(f32x4_t, v[j]);
+        const int64_t row = WGRAD ? (int64_t)e * N + mt0 + j : mt0 + j;
+        if (k >= K || mt0 + j >= m_end) continue;
+        if (kWM == 1 && splits > 1)                            // a part of the sum, for join_kernel
+          *reinterpret_cast<f32x4_t*>(g.workspace + ((int64_t)split * (WGRAD ? (int64_t)g.E * N : P) + row) * K + k) = o4;
+        else
+          store_f32(static_cast<float*>(g.out) + row * g.ldo + k, o4, g.accumulate);
       }
     } else {
-      uint16_t* const o = static_cast<uint16_t*>(g.out) + row * g.ldo;
+      u32x4_t v[2];
 #pragma unroll
-      for (int j = 0; j < C::kKT; j += 4) {
-        u32x4_t v[2];                                          // tiles j, j + 1 and j + 2, j + 3
+      for (int h = 0; h < 2; ++h) {
+        uint32_t x[4];                                         // words h of the four tiles
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          f32x4_t a = acc[t][j + 2 * h], c = acc[t][j + 2 * h + 1];
-          if constexpr (KIND == 2) {
-            a *= gs;
-            c *= gs;
-          }
-          v[h] = exchange16(pk_bf16(a[0], a[1]), pk_bf16(a[2], a[3]), pk_bf16(c[0], c[1]), pk_bf16(c[2], c[3]));
+        for (int j = 0; j < 2; ++j) {
+          x[2 * j] = pk_bf16(acc[t][2 * j][2 * h], acc[t][2 * j][2 * h + 1]);
+          x[2 * j + 1] = pk_bf16(acc[t][2 * j + 1][2 * h], acc[t][2 * j + 1][2 * h + 1]);
+          swap16(x[2 * j], x[2 * j + 1]);
         }
-        u32x4_t first, second;
-        exchange8(low, v[0], v[1], first, second);
-        const int k = kw + 16 * j + (low ? 0 : 32) + 16 * (gq & 1) + 8 * (gq >> 1);
-        if (k < K && m < m_end) *reinterpret_cast<u32x4_t*>(o + k) = first;
-        if (k < K && m + 8 < m_end) *reinterpret_cast<u32x4_t*>(o + 8 * g.ldo + k) = second;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          swap_quad<0>(odd, x[j], x[j + 2]);
+          swap16(x[j], x[j + 2]);
+          swap_quad<1>(upper, x[j], x[j + 2]);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          v[0][2 * j + h] = x[j];
+          v[1][2 * j + h] = x[j + 2];
+        }
+      }
+      const int k = kw + 32 * (gq >> 1) + 8 * (lane & 3);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {                            // rows 4 a + 2 j + g % 2
+        const int m = mt0 + 2 * j + (gq & 1);
+        if (k < K && m < m_end)
+          *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(g.out) + (WGRAD ? (int64_t)e * N + m : m) * g.ldo + k) = v[j];
       }
     }
   }
