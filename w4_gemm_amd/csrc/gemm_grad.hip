@@ -23,7 +23,21 @@
 //   * A workgroup of kWM x kWK waves makes a block of C of 16 kMT kWM rows by
 //     256 columns and takes R = 8 kWM kWK summed rows per stage (one piece of B
 //     per thread).  A is copied two stages ahead (three buffers), B is loaded
-//     into registers two stages ahead and converted one ahead (two buffers).
+//     into registers up to two stages ahead and converted one ahead (two
+//     buffers).
+//   * The outputs go out as whole cache lines (see the epilogue).
+//
+// What bounds it.  Dense: the matrix pipe is busy 58% of the time (8192^3,
+// dgrad 495 us = 1110 TF/s, wgrad 950 us = 1160 TF/s); a loop of nothing but
+// the stage's matrix, LDS and conversion instructions reaches about 1430 TF/s
+// under the card's power limit.  Grouped wgrad (64 x 2048 x 7168, 512 rows an
+// expert, 1.47 ms): 3.8 GB of fp32 gradients, whose stores alone take 0.68 ms and
+// whose products alone 0.91 ms; they add up nearly in full, since a CU's loads
+// queue behind its stores.  (Not mended by delaying every other workgroup, by
+// a persistent workgroup that loads the next block's first stages before it
+// stores -- wgrad 4% faster, dgrad 5% slower for its registers --, nor by two
+// 128-row workgroups per CU.)  Few rows: the time of a stage, 0.45 - 0.8 us of
+// load latency over two stages in flight.
 #include "q4_launch.h"
 #include "q4_lds.h"
 #include "q4_piece.h"
@@ -168,7 +182,8 @@ __device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
 }
 
 // fp32 weight gradients are far larger than the caches and read by a later
-// kernel: written past them (64 x 2048 x 7168: 1778 -> 1730 us).
+// kernel: written past them (64 x 2048 x 7168 with 512 rows each: 1840 us through
+// them, 1510 past them).
 __device__ __forceinline__ void store_f32(float* p, f32x4_t v, int accumulate) {
   f32x4_t* const o = reinterpret_cast<f32x4_t*>(p);
   if (accumulate) v += *o;
@@ -374,6 +389,8 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles, int splits) {
   };
 
   if (stages > 0) {
+    // pieces of B in registers: of two stages, or (R = 64, whose registers are
+    // full) of one that is loaded again as soon as it is converted
     constexpr int kSets = C::kSteps == 1 ? 2 : 1;
     Piece<KIND> raw[kSets];
     bool ok[kSets];
@@ -595,12 +612,14 @@ join_kernel(GradArgs g, int64_t rows, int splits, int wgrad) {
 //             154 vs 222, 64 x 256 655 vs 609; wgrad 64 x 8 rows 652 vs 735.
 // Where the blocks would leave CUs idle the sum may be split over workgroups
 // that write fp32 parts, joined by a second kernel: into as many as cost least
-// by the measured time of a stage of 32 summed rows (0.45 us in a workgroup that
-// has its CU to itself), of the second launch (8 us with its host time) and of the parts (3.5 TB/s).
+// by the measured time of a stage of 32 summed rows in a workgroup that has its
+// CU to itself (dgrad 0.45 us, wgrad 0.8), of the second launch (8 us with its
+// host time) and of the parts (3.5 TB/s).
 // dgrad 16 x 8192 x 8192: 106 us in one part, 24 in 16; 256 x 8192 x 8192: 111
-// in one, 59 in 4; wgrad 8192 x 2048 x 2048 (8-bit): 182 in one, 100 in 4.
+// in one, 59 in 4; wgrad 8192 x 2048 x 2048 (8-bit): 182 in one, 100 in 4,
+// 1000 x 640 x 512: 29 in one, 17 in 4.
 constexpr int64_t kFill = 512;      // workgroups that fill the GPU: two per CU
-constexpr int64_t kStageNs = 450, kJoinNs = 8000, kJoinBytesPerNs = 3500;
+constexpr int64_t kDgradStageNs = 450, kWgradStageNs = 800, kJoinNs = 8000, kJoinBytesPerNs = 3500;
 enum { kBlock64, kBlock128, kBlock256 };
 struct Plan {
   int block, splits;
@@ -613,10 +632,11 @@ Plan plan(bool wgrad, int64_t P, int64_t E, int64_t N, int64_t K) {
   const bool few = wgrad ? per <= 32 : per <= 128 || tiles(128) < 256;
   const int64_t most = kFill / tiles(few ? 64 : 128), stages = ((wgrad ? per : N) + 31) / 32;
   const int64_t part = (wgrad ? E * N : P) * K * 8 / kJoinBytesPerNs;   // writing and reading a part, ns
-  int64_t best = stages * kStageNs;
+  const int64_t stage_ns = wgrad ? kWgradStageNs : kDgradStageNs;
+  int64_t best = stages * stage_ns;
   int splits = 1;
   for (int s = 2; s <= most && s <= stages; ++s) {
-    const int64_t ns = (stages + s - 1) / s * kStageNs + kJoinNs + s * part;
+    const int64_t ns = (stages + s - 1) / s * stage_ns + kJoinNs + s * part;
     if (ns < best) {
       best = ns;
       splits = s;
