@@ -36,7 +36,8 @@ __device__ __forceinline__ void store_past(uint16_t* p, uint4 v) {
 // writes each chunk's counts per expert to the workspace and every workgroup
 // of the second sums them over the chunks before its own (and over all, for
 // the offsets): at most 256 chunks, so that this reads at most 256 E words per
-// workgroup from L2.
+// workgroup from L2.  Bound by latency: 8 choices 3.9 us, 131080 choices of 64
+// experts 2.7 + 7.8 us.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int64_t kSortMaxChunks = 256;
@@ -180,7 +181,8 @@ moe_sort_place_kernel(const int32_t* __restrict__ ids, int64_t P, int k, int E, 
 // ---- permute and its gradient ------------------------------------------------
 // 8 columns per thread, a workgroup per (token, 1024 columns): each token's row
 // is read once and written to its k rows (reading through gather would read it
-// k times).
+// k times).  Bound by HBM (store_past above; the gradient, 8192 tokens of 8
+// rows, 203 us, 1.06 GB at 5.2 TB/s).
 constexpr int kRowThreads = 128;
 constexpr int kRowCols = kRowThreads * 8;
 
@@ -229,7 +231,8 @@ moe_permute_backward_kernel(const uint16_t* __restrict__ dxs, int64_t lds_, cons
 // ---- the combine's gradient --------------------------------------------------
 // A workgroup per token, a wave per choice (waves take every blockDim/64-th):
 // the wave walks the row, so dw's sum stays inside it, and dout[t] is read from
-// the cache by the other waves.
+// the cache by the other waves.  Bound by HBM: 8192 tokens of 8 choices, 7168
+// columns, 390 us, 2.0 GB at 5.1 TB/s (a plain copy reaches 4.8).
 template <bool GATES>
 __global__ void __launch_bounds__(512)
 moe_combine_backward_kernel(const uint16_t* __restrict__ dout, int64_t ldo, const uint16_t* __restrict__ y, int64_t ldy,
@@ -273,8 +276,9 @@ moe_combine_backward_kernel(const uint16_t* __restrict__ dout, int64_t ldo, cons
 }
 
 // ---- the gates' gradient -----------------------------------------------------
-// One wave per token, the E <= 64 * PER logits in registers (PER 1, 4 or 16).  A token whose logits
-// are all -inf has no softmax; its gradient is written as 0.
+// One wave per token, the E <= 64 * PER logits in registers (PER 1, 4 or 16).
+// A token whose logits are all -inf has no softmax; its gradient is written as
+// 0.  8192 tokens of 64 experts: 6 us.
 constexpr int kTopkWaves = 4;
 
 template <int PER>
