@@ -154,11 +154,16 @@ def _on_gpu(*args):
     for name, t in args:
         if t is None:
             continue
-        ts = ((f"{name}.codes", t.codes), (f"{name}.scales", t.scales),
-              (f"{name}.global_scale", t.global_scale)) if isinstance(t, Q4Tensor) else ((name, t),)
-        for n, x in ts:
-            if x is not None and x.device.type != "cuda":
-                raise ValueError(f"{n} must be a GPU tensor (got device {x.device})")
+        for part, x in _parts(t):
+            if x is not None and not x.is_cuda:
+                raise ValueError(f"{name}{part} must be a GPU tensor (got device {x.device})")
+
+
+def _parts(t):
+    """(suffix of its name, tensor) of each tensor of an argument."""
+    if isinstance(t, Q4Tensor):
+        return (".codes", t.codes), (".scales", t.scales), (".global_scale", t.global_scale)
+    return ("", t),
 
 
 def _matrix(t: torch.Tensor, name: str, dtype, rows: int, cols: int, exact_cols: bool = False):
@@ -167,6 +172,13 @@ def _matrix(t: torch.Tensor, name: str, dtype, rows: int, cols: int, exact_cols:
     call, so a wrong tensor never reaches a kernel as a pointer."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a torch tensor")
+    if t.dtype is dtype:
+        shape = t.shape
+        if len(shape) == 2:       # the usual case, with few looks at the tensor
+            r, c = shape
+            step, unit = t.stride()
+            if r >= rows and (c == cols if exact_cols else c >= cols) and unit == 1 and (step >= c or r <= 1):
+                return
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
     if t.dim() != 2:
@@ -191,9 +203,9 @@ def _q4(q: "Q4Tensor", name: str):
     for its format, layout and shape."""
     if not isinstance(q, Q4Tensor):
         raise ValueError(f"{name} must be a Q4Tensor")
-    cb, sb = q4_sizes(q.fmt, q.rows, q.cols, q.layout)
+    cb, sb = _sizes(q.fmt, q.layout, q.rows, q.cols)
     for part, t, need in (("codes", q.codes, cb), ("scales", q.scales, sb)):
-        if not t.is_contiguous() or t.numel() * t.element_size() < need:
+        if not t.is_contiguous() or t.nbytes < need:
             raise ValueError(f"{name}.{part} must be contiguous and hold {need} bytes")
     if q.fmt == NVFP4:
         if q.global_scale is None:
@@ -277,8 +289,8 @@ def empty_q4(fmt, rows: int, cols: int, device="cuda", layout=LAYOUT_ROWS) -> Q4
                         None, lay)
     g = GROUP[f]
     if f in (MXFP8, MXINT8):
-        return Q4Tensor(f, rows, cols, torch.empty((rows, cols), dtype=torch.uint8, device=device),
-                        torch.empty((rows, cols // g), dtype=torch.uint8, device=device), None, lay)
+        return Q4Tensor(f, rows, cols, torch.empty(rows, cols, dtype=torch.uint8, device=device),
+                        torch.empty(rows, cols // g, dtype=torch.uint8, device=device), None, lay)
     sdt = torch.int16 if f == INT4_G128 else torch.int32 if f == INT4_ZP else torch.uint8
     if lay == LAYOUT_ROWS:
         codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=device)
@@ -307,7 +319,8 @@ def q4_quantize(src: torch.Tensor, dst: Q4Tensor, nv_global_in: Optional[torch.T
 def quantize(src: torch.Tensor, fmt, nv_global_in: Optional[torch.Tensor] = None,
              stream=None, layout=LAYOUT_ROWS) -> Q4Tensor:
     """Allocate a Q4Tensor on src's device and quantize src into it."""
-    dst = empty_q4(fmt, src.shape[0], src.shape[1], device=src.device, layout=layout)
+    dst = empty_q4(fmt, src.shape[0], src.shape[1], device=src.get_device() if src.is_cuda else src.device,
+                   layout=layout)
     return q4_quantize(src, dst, nv_global_in, stream)
 
 

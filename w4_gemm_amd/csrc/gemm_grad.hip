@@ -27,9 +27,9 @@
 //     buffers).
 //   * The outputs go out as whole cache lines (see the epilogue).
 //
-// What bounds it.  Dense: the matrix pipe is busy 58% of the time (8192^3,
-// dgrad 495 us = 1110 TF/s, wgrad 950 us = 1160 TF/s); a loop of nothing but
-// the stage's matrix, LDS and conversion instructions reaches about 1430 TF/s
+// What bounds it.  Dense: the matrix pipe is busy 58% of the time (back to back,
+// dgrad 4096 x 8192 x 8192 495 us = 1110 TF/s, wgrad 8192^3 950 us = 1160); a loop of
+// nothing but the stage's matrix, LDS and conversion instructions reaches about 1430
 // under the card's power limit.  Grouped wgrad (64 x 2048 x 7168, 512 rows an
 // expert, 1.47 ms): 3.8 GB of fp32 gradients, whose stores alone take 0.68 ms and
 // whose products alone 0.91 ms; they add up nearly in full, since a CU's loads

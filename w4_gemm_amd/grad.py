@@ -18,7 +18,7 @@ from typing import Optional, Tuple, Union
 
 import torch
 
-from . import (MXFP8, MXINT8, Q4Tensor, _check, _matrix, _q4, _raw_stream, _vector, empty_q4, lib,
+from . import (MXFP8, MXINT8, Q4Tensor, _check, _matrix, _parts, _q4, _raw_stream, _vector, empty_q4, lib,
                q4_grouped_gemm, q4_moe_combine, q4_quantize, Routing)
 
 BF16, F32, I32 = torch.bfloat16, torch.float32, torch.int32
@@ -60,24 +60,21 @@ def _place(stream, *args):
     """Checks that every (name, tensor) is on the GPU, all on one; `with` it the
     call is on that device and the stream it runs on, as (device, stream) ready
     for torch and for the library."""
-    where = None
+    where = -1
     for name, t in args:
         if t is None:
             continue
-        if isinstance(t, Q4Tensor):
-            parts = ((".codes", t.codes), (".scales", t.scales), (".global_scale", t.global_scale))
-        else:
-            parts = (("", t),)
-        for part, x in parts:
-            if x is None:
-                continue
-            if not x.is_cuda:
-                raise ValueError(f"{name}{part} must be a GPU tensor (got device {x.device})")
-            i = x.get_device()
-            if where is None:
-                where = i
-            elif i != where:
-                raise ValueError(f"{name}{part} must be on cuda:{where} like the other tensors (got cuda:{i})")
+        i = t.get_device() if isinstance(t, torch.Tensor) else t.codes.get_device()
+        if where < 0:
+            where = i
+        if i < 0 or i != where or isinstance(t, Q4Tensor):
+            for part, x in _parts(t):
+                if x is None:
+                    continue
+                if not x.is_cuda:
+                    raise ValueError(f"{name}{part} must be a GPU tensor (got device {x.device})")
+                if x.get_device() != where:
+                    raise ValueError(f"{name}{part} must be on cuda:{where} like the other tensors (got cuda:{x.get_device()})")
     if stream is None:
         if where == torch.cuda.current_device():
             return _Here(where, _raw_stream(where))
