@@ -42,6 +42,8 @@
 #include "q4_lds.h"
 #include "q4_piece.h"
 
+#include <algorithm>
+#include <cstdint>
 #include <type_traits>
 
 namespace q4 {
@@ -610,16 +612,18 @@ join_kernel(GradArgs g, int64_t rows, int splits, int wgrad) {
 //             64 x 128 940 vs 914.  It needs a block for each of the 256 CUs.
 //   64 rows   wins where rows are few: dgrad 64 x 32 rows 205 vs 251 us, 64 x 8
 //             154 vs 222, 64 x 256 655 vs 609; wgrad 64 x 8 rows 652 vs 735.
-// Where the blocks would leave CUs idle the sum may be split over workgroups
-// that write fp32 parts, joined by a second kernel: into as many as cost least
-// by the measured time of a stage of 32 summed rows in a workgroup that has its
-// CU to itself (dgrad 0.45 us, wgrad 0.8), of the second launch (8 us with its
-// host time) and of the parts (3.5 TB/s).
-// dgrad 16 x 8192 x 8192: 106 us in one part, 24 in 16; 256 x 8192 x 8192: 111
-// in one, 59 in 4; wgrad 8192 x 2048 x 2048 (8-bit): 182 in one, 100 in 4,
-// 1000 x 640 x 512: 29 in one, 17 in 4.
+// Where the blocks would leave CUs idle, 64 rows also put more CUs to work (wgrad
+// 512 x 2048 x 2048, 8 bits: 15 vs 19 us), and the sum may be split over
+// workgroups that write fp32 parts, joined by a second kernel: the block and as
+// many parts as cost least by the measured time of a stage of 32 summed rows in
+// a workgroup that has its CU to itself (dgrad 0.45 us, wgrad 0.6 in 64 rows and
+// 0.8 in 128), of the second launch (8 us with its host time) and of the parts
+// (3.5 TB/s).  dgrad 16 x 8192 x 8192: 106 us in one part, 24 in 16; 256 x 8192
+// x 8192: 111 in one, 59 in 4; wgrad 8192 x 2048 x 2048 (8-bit): 182 in one,
+// 97 in 4 of 128 rows, 120 in 2 of 64; 1000 x 640 x 512: 29 in one, 15 in 4.
 constexpr int64_t kFill = 512;      // workgroups that fill the GPU: two per CU
-constexpr int64_t kDgradStageNs = 450, kWgradStageNs = 800, kJoinNs = 8000, kJoinBytesPerNs = 3500;
+constexpr int64_t kDgradStageNs = 450, kWgradStage64Ns = 600, kWgradStage128Ns = 800;
+constexpr int64_t kJoinNs = 8000, kJoinBytesPerNs = 3500;
 enum { kBlock64, kBlock128, kBlock256 };
 struct Plan {
   int block, splits;
@@ -629,20 +633,24 @@ Plan plan(bool wgrad, int64_t P, int64_t E, int64_t N, int64_t K) {
   const int64_t per = P / E, kt = (K + kBK - 1) / kBK;
   auto tiles = [&](int64_t bm) { return wgrad ? E * ((N + bm - 1) / bm) * kt : ((P + bm - 1) / bm + E - 1) * kt; };
   if (tiles(256) >= 256 && per >= (wgrad ? 256 : 2048)) return {kBlock256, 1};
-  const bool few = wgrad ? per <= 32 : per <= 128 || tiles(128) < 256;
-  const int64_t most = kFill / tiles(few ? 64 : 128), stages = ((wgrad ? per : N) + 31) / 32;
+  const int64_t stages = ((wgrad ? per : N) + 31) / 32;
   const int64_t part = (wgrad ? E * N : P) * K * 8 / kJoinBytesPerNs;   // writing and reading a part, ns
-  const int64_t stage_ns = wgrad ? kWgradStageNs : kDgradStageNs;
-  int64_t best = stages * stage_ns;
-  int splits = 1;
-  for (int s = 2; s <= most && s <= stages; ++s) {
-    const int64_t ns = (stages + s - 1) / s * stage_ns + kJoinNs + s * part;
-    if (ns < best) {
-      best = ns;
-      splits = s;
+  Plan best{};
+  int64_t least = INT64_MAX;
+  auto consider = [&](int block, int64_t bm, int64_t stage_ns) {
+    const int64_t most = std::min(kFill / tiles(bm), stages);
+    for (int s = 1; s == 1 || s <= most; ++s) {
+      const int64_t ns = (stages + s - 1) / s * stage_ns + (s > 1 ? kJoinNs + s * part : 0);
+      if (ns < least) {
+        least = ns;
+        best = {block, s};
+      }
     }
-  }
-  return {few ? kBlock64 : kBlock128, splits};
+  };
+  const bool few = per <= (wgrad ? 32 : 128), idle = tiles(128) < 256;
+  if (few || idle) consider(kBlock64, 64, wgrad ? kWgradStage64Ns : kDgradStageNs);
+  if (!few && (wgrad || !idle)) consider(kBlock128, 128, wgrad ? kWgradStage128Ns : kDgradStageNs);
+  return best;
 }
 
 template <bool WGRAD, int KIND, int LAYOUT, bool GATHER, int kWM, int kWK, int kMT>
