@@ -249,20 +249,20 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles, int splits) {
   const int m_end = WGRAD ? N : hi;
 
   // ---- A: this lane's part of each copy, as a byte offset from the stage's
-  // first row or column; a lane with nothing to copy takes an offset past the
-  // buffer's end and gets zeros
-  int aoff[C::kCPW];
+  // first row or column.  wgrad: 16 rows of a block of 32 columns, in the order
+  // of column_place; a wave's copies are 64 columns apart, and what they hold
+  // of columns from N on is not used (the buffer ends with column N of the last
+  // row).  dgrad: a lane with nothing to copy takes an offset past the buffer's
+  // end and gets zeros.
+  constexpr int AC = R / 8, RPC = 64 / AC;
+  int aoff[WGRAD ? 1 : C::kCPW];
+  if constexpr (WGRAD) {
+    const int at = wave * 16 + (lane >> 2), p = at % R, c = at / R * 4 + ((lane & 3) ^ place_swap(p));
+    aoff[0] = (((p & ~31) + place_row(p & 31)) * (int)g.lddc + 8 * c) * 2;
+  } else {
 #pragma unroll
-  for (int q = 0; q < C::kCPW; ++q) {
-    const int ci = wave + C::kWaves * q;              // copy instruction: 1 KB
-    if constexpr (WGRAD) {
-      // 16 rows of a block of 32 columns, in the order of column_place
-      const int at = ci * 16 + (lane >> 2), p = at % R, c = at / R * 4 + ((lane & 3) ^ place_swap(p));
-      const int r = (p & ~31) + place_row(p & 31);
-      aoff[q] = m0 + 8 * c < N ? (r * (int)g.lddc + 8 * c) * 2 : kPast;
-    } else {
-      constexpr int AC = R / 8, RPC = 64 / AC;
-      const int m = ci * RPC + lane / AC, c = (lane % AC) ^ swizzle_rows<R>(m);
+    for (int q = 0; q < C::kCPW; ++q) {
+      const int m = (wave + C::kWaves * q) * RPC + lane / AC, c = (lane % AC) ^ swizzle_rows<R>(m);
       aoff[q] = (min(m, hi - 1 - m0) * (int)g.lddc + 8 * c) * 2;
     }
   }
@@ -273,17 +273,21 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles, int splits) {
   const int64_t astep = WGRAD ? (int64_t)R * g.lddc * 2 : R * 2;
   int aleft = r_end - r_begin;
   auto copy_a = [&](int buf) {
-    const rsrc_t rsrc = rows_buffer(apos, WGRAD ? aleft : aleft > 0 ? R : 0, R, WGRAD ? (int)g.lddc * 2 : kPast / R);
+    const rsrc_t rsrc = WGRAD ? rows_buffer(apos, aleft, R, (int)g.lddc * 2, ((int)g.lddc - (N - m0)) * 2)
+                              : rows_buffer(apos, aleft > 0 ? R : 0, R, kPast / R);
     uint8_t* dst = abase + buf * C::kABytes;
 #pragma unroll
     for (int q = 0; q < C::kCPW; ++q) {
       const int ci = wave + C::kWaves * q;
       if (C::kCopies % C::kWaves != 0 && ci >= C::kCopies) continue;
-      int off = aoff[q];
-      if constexpr (!WGRAD) {
-        constexpr int AC = R / 8, RPC = 64 / AC;
+      int off;
+      if constexpr (WGRAD) {
+        off = aoff[0];
+        asm volatile("" : "+v"(off));                   // (one register, not one per copy)
+        off += 128 * q;
+      } else {
         const int m = ci * RPC + lane / AC, c = (lane % AC) ^ swizzle_rows<R>(m);
-        if (8 * c >= aleft) off = kPast;
+        off = 8 * c >= aleft ? kPast : aoff[q];
       }
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lptr_t)(dst + ci * 1024), 16, off, 0, 0, 0);
     }

@@ -25,6 +25,8 @@
 #include "q4_mma.h"
 #include "q4_mx8.h"
 
+#include <type_traits>
+
 namespace q4 {
 
 constexpr int kBf16Piece = 7;   // beside the q4_format values 0..2, 4 (weights) and 5, 6 (saved activations)
@@ -38,7 +40,8 @@ struct Piece {
   static constexpr int kScales = KIND == kBf16Piece ? 0 : piece_is_mx8(KIND) ? 2 : 1;
   static constexpr int kLoads = kWords + kScales;                                      // load instructions
   u32x4_t q[kWords];
-  uint32_t s[kScales ? kScales : 1];
+  // (bytes as loaded: widened any earlier, the widening waits for the load)
+  std::conditional_t<KIND == 1 || piece_is_mx8(KIND), uint8_t, uint32_t> s[kScales ? kScales : 1];
 };
 
 // Where thread `tid` of a workgroup has its piece: row of the stage, and the
@@ -139,7 +142,7 @@ __device__ __forceinline__ void piece_clear(Piece<KIND>& p, bool clear) {
 #pragma unroll
   for (int i = 0; i < Piece<KIND>::kWords; ++i) p.q[i] = clear ? u32x4_t{0u, 0u, 0u, 0u} : p.q[i];
 #pragma unroll
-  for (int i = 0; i < Piece<KIND>::kScales; ++i) p.s[i] = clear ? 0u : p.s[i];
+  for (int i = 0; i < Piece<KIND>::kScales; ++i) p.s[i] = clear ? 0 : p.s[i];
 }
 
 // Eight of the piece's values as bf16: the i-th in the order of piece_chunk.
