@@ -28,16 +28,16 @@
 //   * The outputs go out as whole cache lines (see the epilogue).
 //
 // What bounds it.  Dense: the matrix pipe is busy 58% of the time (back to back,
-// dgrad 4096 x 8192 x 8192 495 us = 1110 TF/s, wgrad 8192^3 950 us = 1160); a loop of
-// nothing but the stage's matrix, LDS and conversion instructions reaches about 1430
-// under the card's power limit.  Grouped wgrad (64 x 2048 x 7168, 512 rows an
-// expert, 1.47 ms): 3.8 GB of fp32 gradients, whose stores alone take 0.68 ms and
-// whose products alone 0.91 ms; they add up nearly in full, since a CU's loads
-// queue behind its stores.  (Not mended by delaying every other workgroup, by
-// a persistent workgroup that loads the next block's first stages before it
-// stores -- wgrad 4% faster, dgrad 5% slower for its registers --, nor by two
-// 128-row workgroups per CU.)  Few rows: the time of a stage, 0.45 - 0.8 us of
-// load latency over two stages in flight.
+// dgrad 4096 x 8192 x 8192 495 us = 1110 TF/s, wgrad 8192^3 950 us = 1160); a
+// loop of nothing but the stage's matrix, LDS and conversion instructions
+// reaches about 1430 under the card's power limit.  Grouped wgrad (64 x 2048 x
+// 7168, 32768 ragged rows, 1.34 ms): 3.8 GB of fp32 gradients, whose stores take
+// 0.68 ms alone; the products take 0.95 ms alone, and the two add up by more
+// than half, since a CU's loads queue behind its stores.  (Not mended by
+// delaying every other workgroup, by a persistent workgroup that loads the next
+// block's first stages before it stores -- wgrad 4% faster, dgrad 5% slower for
+// its registers --, nor by two 128-row workgroups per CU.)  Few rows: the time
+// of a stage, 0.4 - 0.8 us of load latency over two stages in flight.
 #include "q4_launch.h"
 #include "q4_lds.h"
 #include "q4_piece.h"
@@ -611,9 +611,11 @@ join_kernel(GradArgs g, int64_t rows, int splits, int wgrad) {
 //   256 rows  (8 waves, one workgroup per CU) moves a third less from L2 per
 //             product and converts B half as often as 128 rows (4 waves, two
 //             per CU), but overlaps less and rounds the experts' rows up
-//             further: dgrad 4 x 2048 rows 215 vs 246 us, 8 x 1024 rows 254 vs
-//             241; wgrad (8-bit) 8 x 1024 rows 345 vs 395, 32 x 256 631 vs 660,
-//             64 x 128 940 vs 914.  It needs a block for each of the 256 CUs.
+//             further: dgrad 4 x 2048 rows 215 vs 246 us, 8 x 1024 rows 257 vs
+//             249, 16 x 512 300 vs 250; wgrad (8-bit, ragged) 8 x 1024 rows 293
+//             vs 305, 64 x 256 1017 vs 1055; dense 8192 x 8192 with 1024 rows
+//             168 vs 177, 512 116 vs 110, 256 88 vs 77.  It needs a block for
+//             each of the 256 CUs.
 //   64 rows   wins where rows are few: dgrad 64 x 32 rows 205 vs 251 us, 64 x 8
 //             154 vs 222, 64 x 256 655 vs 609; wgrad 64 x 8 rows 652 vs 735.
 // Where the blocks would leave CUs idle, 64 rows also put more CUs to work (wgrad
@@ -624,7 +626,7 @@ join_kernel(GradArgs g, int64_t rows, int splits, int wgrad) {
 // 0.8 in 128), of the second launch (8 us with its host time) and of the parts
 // (3.5 TB/s).  dgrad 16 x 8192 x 8192: 106 us in one part, 24 in 16; 256 x 8192
 // x 8192: 111 in one, 59 in 4; wgrad 8192 x 2048 x 2048 (8-bit): 182 in one,
-// 97 in 4 of 128 rows, 120 in 2 of 64; 1000 x 640 x 512: 29 in one, 15 in 4.
+// 84 in 4 of 128 rows, 108 in 2 of 64; 1000 x 640 x 512: 29 in one, 14 in 4.
 constexpr int64_t kFill = 512;      // workgroups that fill the GPU: two per CU
 constexpr int64_t kDgradStageNs = 450, kWgradStage64Ns = 600, kWgradStage128Ns = 800;
 constexpr int64_t kJoinNs = 8000, kJoinBytesPerNs = 3500;
@@ -636,7 +638,7 @@ struct Plan {
 Plan plan(bool wgrad, int64_t P, int64_t E, int64_t N, int64_t K) {
   const int64_t per = P / E, kt = (K + kBK - 1) / kBK;
   auto tiles = [&](int64_t bm) { return wgrad ? E * ((N + bm - 1) / bm) * kt : ((P + bm - 1) / bm + E - 1) * kt; };
-  if (tiles(256) >= 256 && per >= (wgrad ? 256 : 2048)) return {kBlock256, 1};
+  if (tiles(256) >= 256 && per >= (!wgrad ? 2048 : E > 1 ? 256 : 1024)) return {kBlock256, 1};
   const int64_t stages = ((wgrad ? per : N) + 31) / 32;
   const int64_t part = (wgrad ? E * N : P) * K * 8 / kJoinBytesPerNs;   // writing and reading a part, ns
   Plan best{};
