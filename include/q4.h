@@ -391,9 +391,9 @@ q4_status q4_moe_combine(const void* y_bf16, int64_t ldy, const int32_t* inv, co
  * call gives (host arithmetic only; 0 for many sizes, then NULL may be passed),
  * without contents to keep; two calls that may run at once (two streams, two
  * captured graphs) need one each.  The per-token calls need T < 2^23 and
- * T * ceil(columns/1024) < 2^25; the products K and the leading dimensions of
- * dC and A up to 2^21, summed and output rows up to 2^30, and at most 2^22
- * blocks of 64 x 256 outputs (else Q4_ERR_SHAPE).
+ * T * ceil(columns/1024) < 2^25; the products N, K and the leading dimensions
+ * of dC and A up to 2^21, summed rows up to 2^30, and at most 2^22 blocks of
+ * 64 x 256 outputs (else Q4_ERR_SHAPE).
  */
 
 /*

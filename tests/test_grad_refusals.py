@@ -144,7 +144,8 @@ def test_products_refuse():
                 dict(a=A16, lda=256, K=252), dict(a=A16, lda=248)):
         assert w(**bad) == SHAPE, bad
     for bad in (dict(q=q, ld=far), dict(a=A16, lda=far), dict(a=A16, lda=far, K=far, ldw=far), dict(q=q, P=(1 << 30) + 8),
-                dict(q=q, N=1 << 31), dict(q=q, N=1 << 28)):
+                dict(q=q, N=1 << 31), dict(q=q, N=1 << 28),
+                dict(q=q, P=1, N=far, ld=far)):
         assert w(**bad) == SHAPE, bad
     for bad in (dict(q=q, dc=None), dict(q=q, off=None), dict(q=q, dw=None)):
         assert w(**bad) == NULL, bad

@@ -665,7 +665,7 @@ q4_status dgrad(const void* dC, int64_t lddc, const int32_t* offsets, int32_t E,
   if (!aligned(offsets, 4)) return Q4_ERR_ALIGN;
   st = check_bf16(dC, P, N, lddc);
   if (st != Q4_OK) return st;
-  if ((P > 1 && lddc > kMaxGradLd) || K > kMaxGradLd) return Q4_ERR_SHAPE;
+  if ((P > 1 && lddc > kMaxGradLd) || N > kMaxGradLd || K > kMaxGradLd) return Q4_ERR_SHAPE;
   st = check_bf16(dA, P, K, ldda);
   if (st != Q4_OK) return st;
   if (need && !workspace) return Q4_ERR_NULL;
@@ -710,7 +710,7 @@ q4_status wgrad(const void* dC, int64_t lddc, const void* A_bf16, int64_t lda, c
   if (!aligned(gather, 4) || !aligned(offsets, 4)) return Q4_ERR_ALIGN;
   st = check_bf16(dC, P, N, lddc);
   if (st != Q4_OK) return st;
-  if ((P > 1 && lddc > kMaxGradLd) || K > kMaxGradLd) return Q4_ERR_SHAPE;
+  if ((P > 1 && lddc > kMaxGradLd) || N > kMaxGradLd || K > kMaxGradLd) return Q4_ERR_SHAPE;
   if (!A_q) {
     st = check_bf16(A_bf16, T, K, lda);
     if (st != Q4_OK) return st;

@@ -722,12 +722,12 @@ constexpr int64_t kMaxSum = (int64_t)1 << 30;
 size_t dgrad_workspace(int64_t P, int32_t E, int64_t N, int64_t K) { return parts_bytes(false, P, E, N, K); }
 size_t wgrad_workspace(int64_t P, int32_t E, int64_t N, int64_t K) { return parts_bytes(true, P, E, N, K); }
 
-// (64-row tiles, the smallest; the summed index plus a stage stays an int)
+// (64-row tiles, the smallest; a summed row plus a stage stays an int)
 bool dgrad_fits(int64_t P, int32_t E, int64_t N, int64_t K) {
-  return N <= kMaxSum && ((P + 63) / 64 + E) * ((K + kBK - 1) / kBK) <= kMaxTiles;
+  return ((P + 63) / 64 + E) * ((K + kBK - 1) / kBK) <= kMaxTiles;
 }
 bool wgrad_fits(int64_t P, int32_t E, int64_t N, int64_t K) {
-  return P <= kMaxSum && N <= kMaxSum && E * ((N + 63) / 64) * ((K + kBK - 1) / kBK) <= kMaxTiles;
+  return P <= kMaxSum && E * ((N + 63) / 64) * ((K + kBK - 1) / kBK) <= kMaxTiles;
 }
 
 hipError_t launch_dgrad(int fmt, int layout, const GradArgs& g, hipStream_t stream) {
