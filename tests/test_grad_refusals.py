@@ -114,8 +114,10 @@ def test_products_refuse():
     n = ctypes.c_size_t()
     for f in (L.q4_dgrad_workspace, L.q4_wgrad_workspace):
         assert f(4, 1, 64, 256, None) == NULL
-        for a in ((-1, 1, 64, 256), (4, -1, 64, 256), (4, 65536, 64, 256), (4, 1, -1, 256), (4, 1, 64, 1 << 31)):
+        for a in ((-1, 1, 64, 256), (4, -1, 64, 256), (4, 65536, 64, 256), (4, 1, -1, 256), (4, 1, 64, 1 << 31),
+                  (4, 1, (1 << 21) + 8, 256), (1, 65535, (1 << 31) - 8, (1 << 31) - 128)):
             assert f(*a, ctypes.byref(n)) == SHAPE
+        assert f((1 << 31) - 1, 65535, 1 << 21, 1 << 21, ctypes.byref(n)) == OK and n.value == 0
     big = 1 << 40
     W = _d(q4.MXFP4)
     g = lambda **k: L.q4_grouped_gemm_dgrad(*[{**dict(dc=A16, ld=32, off=A16, E=2, P=8, W=W, N=32, da=A16, lda=256, ws=A16,  # noqa: E731,E501

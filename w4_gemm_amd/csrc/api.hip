@@ -602,7 +602,7 @@ q4_status q4_swiglu_backward(const void* gu_bf16, int64_t ld_gu, const q4_tensor
 
 q4_status q4_dgrad_workspace(int64_t P, int32_t E, int64_t N, int64_t K, size_t* bytes) {
   if (!bytes) return Q4_ERR_NULL;
-  if (P < 0 || E < 0 || E > 65535 || N < 0 || K < 0 || P >= kMaxDim || N >= kMaxDim || K >= kMaxDim)
+  if (P < 0 || E < 0 || E > 65535 || N < 0 || K < 0 || P >= kMaxDim || N > kMaxGradLd || K > kMaxGradLd)
     return Q4_ERR_SHAPE;
   *bytes = P && E && K ? q4::dgrad_workspace(P, E, N, K) : 0;
   return Q4_OK;
@@ -610,7 +610,7 @@ q4_status q4_dgrad_workspace(int64_t P, int32_t E, int64_t N, int64_t K, size_t*
 
 q4_status q4_wgrad_workspace(int64_t P, int32_t E, int64_t N, int64_t K, size_t* bytes) {
   if (!bytes) return Q4_ERR_NULL;
-  if (P < 0 || E < 0 || E > 65535 || N < 0 || K < 0 || P >= kMaxDim || N >= kMaxDim || K >= kMaxDim)
+  if (P < 0 || E < 0 || E > 65535 || N < 0 || K < 0 || P >= kMaxDim || N > kMaxGradLd || K > kMaxGradLd)
     return Q4_ERR_SHAPE;
   *bytes = E && N && K ? q4::wgrad_workspace(P, E, N, K) : 0;
   return Q4_OK;
@@ -665,7 +665,7 @@ q4_status dgrad(const void* dC, int64_t lddc, const int32_t* offsets, int32_t E,
   if (!aligned(offsets, 4)) return Q4_ERR_ALIGN;
   st = check_bf16(dC, P, N, lddc);
   if (st != Q4_OK) return st;
-  if ((P > 1 && lddc > kMaxGradLd) || N > kMaxGradLd || K > kMaxGradLd) return Q4_ERR_SHAPE;
+  if (P > 1 && lddc > kMaxGradLd) return Q4_ERR_SHAPE;
   st = check_bf16(dA, P, K, ldda);
   if (st != Q4_OK) return st;
   if (need && !workspace) return Q4_ERR_NULL;
@@ -710,7 +710,7 @@ q4_status wgrad(const void* dC, int64_t lddc, const void* A_bf16, int64_t lda, c
   if (!aligned(gather, 4) || !aligned(offsets, 4)) return Q4_ERR_ALIGN;
   st = check_bf16(dC, P, N, lddc);
   if (st != Q4_OK) return st;
-  if ((P > 1 && lddc > kMaxGradLd) || N > kMaxGradLd || K > kMaxGradLd) return Q4_ERR_SHAPE;
+  if (P > 1 && lddc > kMaxGradLd) return Q4_ERR_SHAPE;
   if (!A_q) {
     st = check_bf16(A_bf16, T, K, lda);
     if (st != Q4_OK) return st;
