@@ -650,6 +650,46 @@ def test_calls_on_another_stream():
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("kind", ("mxint8", "mxfp8"))
+def test_wgrad_dense_of_many_rows(kind):
+    """A dense layer in the largest block, without gather; every size odd for it."""
+    log("wgrad many rows", kind)
+    rng = _rng("wgradm")
+    M, N, K = 1061, 4104, 4128
+    dc = _bf16(rng, M, N)
+    A = q4.quantize(_bf16(rng, M, K).to(DEV), kind)
+    a = to_f32(q4.q4_dequant(A, torch.empty(M, K, device=DEV)))
+    off = np.array([0, M], np.int32)
+    bound = _wgrad_bound(to_f32(dc), a, None, off)
+    ref = grad.wgrad(to_f32(dc), a, None, off)
+    _close(q4.q4_gemm_wgrad(_strided(dc), A), ref, bound, "dW")
+
+
+@pytest.mark.parametrize("gathered", (True, False))
+def test_products_of_many_experts(gathered):
+    """More blocks than the XCDs' first turns hold, experts of very different sizes, empty ones among them."""
+    log("many experts", gathered)
+    rng = _rng("many", gathered)
+    E, P, N, K, T = 331, 1777, 72, 384, 1800
+    off = _segments(rng, E, P, "empty_first")
+    off[100:130] = off[100]
+    w, dc, x = _bf16(rng, E * N, K, std=0.02), _bf16(rng, P, N), _bf16(rng, T, K)
+    W = q4.quantize(w.to(DEV), "mxfp4")
+    wd = oracle.dequant(oracle.quantize("mxfp4", to_f32(w)))
+    offd = torch.from_numpy(off).to(DEV)
+    ref = grad.dgrad(to_f32(dc), off, wd, N)
+    _close(q4.q4_grouped_gemm_dgrad(dc.to(DEV), offd, W, N), ref,
+           _dgrad_bound(to_f32(dc), off, wd, N, ref, True), "dA")
+    gather = rng.integers(0, T, P).astype(np.int32) if gathered else None
+    gd = torch.from_numpy(gather).to(DEV) if gathered else None
+    for kind in ("bf16", "mxint8"):
+        A = x.to(DEV) if kind == "bf16" else q4.quantize(x.to(DEV), kind)
+        a = to_f32(x) if kind == "bf16" else to_f32(q4.q4_dequant(A, torch.empty(T, K, device=DEV)))
+        a_ref = a if gathered else a[:P]
+        _close(q4.q4_grouped_gemm_wgrad(dc.to(DEV), A, gd, offd), grad.wgrad(to_f32(dc), a_ref, gather, off),
+               _wgrad_bound(to_f32(dc), a_ref, gather, off), (kind, "dW"))
+
+
 def test_results_do_not_vary():
     rng = _rng("again")
     dc = _bf16(rng, 3000, 128).to(DEV)
