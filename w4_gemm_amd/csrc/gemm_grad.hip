@@ -56,9 +56,8 @@ typedef const __attribute__((address_space(3))) u32x4_t* u32x4_lds_t;
 constexpr int kBK = 256;              // columns of a block of C
 constexpr int kABufs = 3, kBBufs = 2;
 
-// Range of the buffers that A is copied from: an offset of kPast is past the
-// end, where a buffer load gives zeros; every other offset is checked here to
-// lie in the matrix.
+// A is copied through buffers, where an offset past the end loads zeros.  wgrad's
+// end with the matrix; dgrad's offsets lie in the matrix or are kPast.
 constexpr int kPast = 0x7FFFFFF0;
 constexpr int kRsrcFlags = 0x00020000;   // a raw buffer of 32-bit words
 
@@ -184,8 +183,8 @@ __device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
 }
 
 // fp32 weight gradients are far larger than the caches and read by a later
-// kernel: written past them (64 x 2048 x 7168 with 512 rows each: 1840 us through
-// them, 1510 past them).
+// kernel: written past them (64 x 2048 x 7168, 32768 ragged rows: 1500 us through
+// them, 1300 past them).
 __device__ __forceinline__ void store_f32(float* p, f32x4_t v, int accumulate) {
   f32x4_t* const o = reinterpret_cast<f32x4_t*>(p);
   if (accumulate) v += *o;
