@@ -204,39 +204,18 @@ struct Kern {
   static constexpr int kCPW = (kCopies + kWaves - 1) / kWaves;
 };
 
+// One block of C: of expert e's rows lo .. hi - 1, from row (dgrad) or n (wgrad)
+// m0 and column k0 on; part `split` of the sum.
 template <bool WGRAD, int KIND, int LAYOUT, bool GATHER, int kWM, int kWK, int kMT>
-__global__ void __launch_bounds__(64 * kWM * kWK, kMT > 4 ? 2 : 3)
-grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles, int splits, int turn) {
+__device__ __forceinline__ void make_block(const GradArgs& g, uint8_t* const smem, int e, int lo, int hi, int m0,
+                                           int k0, int split, int splits) {
   using C = Kern<WGRAD, KIND, LAYOUT, GATHER, kWM, kWK, kMT>;
-  constexpr int R = C::R, BM = C::BM;
-  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  constexpr int R = C::R;
   uint8_t* const bbase = smem;                        // (first: its offsets fit the instructions)
   uint8_t* const abase = smem + kBBufs * C::kBBytes;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / kWK, wk = wave % kWK;
-
-  // block of C: the XCDs take turns of `turn` blocks, in groups of 4 row tiles
-  const int xcd = blockIdx.x & 7, i = blockIdx.x >> 3;
-  const int all = (i / turn * 8 + xcd) * turn + i % turn;
-  if (all >= tiles * splits) return;
-  const int split = all / tiles, lin = all - split * tiles;
   const int P = (int)g.P, N = (int)g.N, K = (int)g.K;
-  const int per_e = WGRAD ? mtiles * ktiles : tiles;
-  int e = WGRAD ? lin / per_e : 0;
-  const int in_e = lin - e * per_e;
-  const int gsz = 4 * ktiles, first_m = (in_e / gsz) * 4, gm = min(mtiles - first_m, 4);
-  const int mt = first_m + (in_e % gsz) % gm, k0 = ((in_e % gsz) / gm) * kBK;
-  int lo, hi, m0;     // the expert's rows; first row (dgrad) / first n (wgrad) of the block
-  if constexpr (WGRAD) {
-    segment(g.offsets, e, P, lo, hi);
-    m0 = mt * BM;
-  } else {
-    if (!find_tile<BM>(g.offsets, g.E, P, mt, e, lo, hi)) return;
-    e = __builtin_amdgcn_readfirstlane(e);
-    lo = __builtin_amdgcn_readfirstlane(lo);
-    hi = __builtin_amdgcn_readfirstlane(hi);
-    m0 = lo;
-  }
   // this workgroup's part of the sum: whole stages
   int r_begin = WGRAD ? lo : 0, r_end = WGRAD ? hi : N;
   if (kWM == 1 && splits > 1) {
@@ -582,6 +561,41 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles, int splits, int turn)
       }
     }
   }
+}
+
+template <bool WGRAD, int KIND, int LAYOUT, bool GATHER, int kWM, int kWK, int kMT>
+__global__ void __launch_bounds__(64 * kWM * kWK, kMT > 4 ? 2 : 3)
+grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles, int splits, int turn) {
+  constexpr int BM = 16 * kMT * kWM;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  // block of C: the XCDs take turns of `turn` blocks, in groups of 4 row tiles
+  const int xcd = blockIdx.x & 7, i = blockIdx.x >> 3;
+  const int all = (i / turn * 8 + xcd) * turn + i % turn;
+  if (all >= tiles * splits) return;
+  const int split = all / tiles, lin = all - split * tiles;
+  const int P = (int)g.P;
+  const int per_e = WGRAD ? mtiles * ktiles : tiles;
+  int e = WGRAD ? lin / per_e : 0;
+  const int in_e = lin - e * per_e;
+  const int gsz = 4 * ktiles, first_m = (in_e / gsz) * 4, gm = min(mtiles - first_m, 4);
+  const int mt = first_m + (in_e % gsz) % gm, k0 = ((in_e % gsz) / gm) * kBK;
+  int lo, hi, m0;     // the expert's rows; first row (dgrad) / first n (wgrad) of the block
+  if constexpr (WGRAD) {
+    segment(g.offsets, e, P, lo, hi);
+    m0 = mt * BM;
+  } else {
+    if (!find_tile<BM>(g.offsets, g.E, P, mt, e, lo, hi)) return;
+    e = __builtin_amdgcn_readfirstlane(e);
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    hi = __builtin_amdgcn_readfirstlane(hi);
+    m0 = lo;
+    // an expert's last rows: half a block does (64 x 2048 x 7168, 32768 ragged
+    // rows 951 -> 931 us, 16384 rows 572 -> 540)
+    if constexpr (kWM == 1 && kMT > 4)
+      if (hi - m0 <= BM / 2)
+        return make_block<WGRAD, KIND, LAYOUT, GATHER, kWM, kWK, kMT / 2>(g, smem, e, lo, hi, m0, k0, split, splits);
+  }
+  make_block<WGRAD, KIND, LAYOUT, GATHER, kWM, kWK, kMT>(g, smem, e, lo, hi, m0, k0, split, splits);
 }
 
 // out[row][k] (+)= the sum of the splits' parts, in order; four columns per
