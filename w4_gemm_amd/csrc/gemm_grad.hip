@@ -31,7 +31,7 @@
 // dgrad 4096 x 8192 x 8192 495 us = 1110 TF/s, wgrad 8192^3 950 us = 1160); a
 // loop of nothing but the stage's matrix, LDS and conversion instructions
 // reaches about 1430 under the card's power limit.  Grouped wgrad (64 x 2048 x
-// 7168, 32768 ragged rows, 1.34 ms): 3.8 GB of fp32 gradients, whose stores take
+// 7168, 32768 ragged rows, 1.30 - 1.34 ms): 3.8 GB of fp32 gradients, whose stores take
 // 0.68 ms alone; the products take 0.95 ms alone, and the two add up by more
 // than half, since a CU's loads queue behind its stores.  (Not mended by
 // delaying every other workgroup, by a persistent workgroup that loads the next
@@ -590,7 +590,8 @@ grad_kernel(GradArgs g, int mtiles, int ktiles, int tiles, int splits, int turn)
     hi = __builtin_amdgcn_readfirstlane(hi);
     m0 = lo;
     // an expert's last rows: half a block does (64 x 2048 x 7168, 32768 ragged
-    // rows 951 -> 931 us, 16384 rows 572 -> 540)
+    // rows 951 -> 931 us, 16384 rows 572 -> 540; of 64-row blocks it does not:
+    // 512 rows 141 -> 171)
     if constexpr (kWM == 1 && kMT > 4)
       if (hi - m0 <= BM / 2)
         return make_block<WGRAD, KIND, LAYOUT, GATHER, kWM, kWK, kMT / 2>(g, smem, e, lo, hi, m0, k0, split, splits);
