@@ -33,8 +33,14 @@ __device__ __forceinline__ uint32_t max_of_4(uint32_t a) {
   return max(a, (uint32_t)__shfl_xor((int)a, 2));
 }
 
+// 1 / (1 + e), e = exp(-g).  v_rcp_f32 returns 0 where the reciprocal is below
+// the smallest normal number (g < -87.3), which times a large u is not small: it
+// takes (1 + e) / 16, and the multiplication by 1/16 makes the denormal.  Powers
+// of two: no other value changes.  (From e = 2^128 on, g < -88.7, it is 0, as in
+// q4_swiglu.)
 __device__ __forceinline__ float sigmoid(float g) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * g));
+  const float e = __builtin_amdgcn_exp2f(-1.4426950408889634f * g);
+  return 0.0625f * __builtin_amdgcn_rcpf(__builtin_fmaf(e, 0.0625f, 0.0625f));
 }
 
 // Rows that the next kernel reads from far behind: written past the caches
