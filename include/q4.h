@@ -408,7 +408,8 @@ q4_status q4_moe_topk(const float* logits, int64_t ld, int64_t T, int32_t E, int
  * token t's logits and d[e] the sum of dweights[t][j] over the choices j with
  * topk_ids[t][j] == e (ids outside 0 .. E-1 take no part),
  *     dlogits[t][e] = p[e] * (d[e] - sum_e' p[e'] d[e']).
- * A token whose logits are all -inf gets 0.  logits [T][ld], dlogits
+ * A token whose logits are all -inf gets 0, one with a NaN among them NaN
+ * throughout.  logits [T][ld], dlogits
  * [T][lddl] fp32; topk_ids, dweights [T][k].  E <= 1024, 1 <= k <= 32.
  */
 q4_status q4_moe_topk_backward(const float* logits, int64_t ld, int64_t T, int32_t E, int32_t k,

@@ -1,5 +1,5 @@
-"""The backward calls at values where a shortcut would show: sigmoids below
-the smallest normal number."""
+"""The backward calls at values where a shortcut would show: logits that are
+not numbers, sigmoids below the smallest normal number."""
 import numpy as np
 import pytest
 import torch
@@ -11,6 +11,27 @@ from q4_helpers import log, to_f32
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 BF16 = torch.bfloat16
+
+
+@pytest.mark.parametrize("E", (5, 64, 100, 700))
+def test_gates_of_logits_that_are_not_numbers(E):
+    """A NaN among a token's logits (alone, or beside nothing but -inf) makes its whole gradient NaN, as the formula does;
+    only a token whose logits are all -inf gets zeros."""
+    log("gates, NaN", E)
+    rng = np.random.default_rng(E)
+    lg = rng.standard_normal((6, E)).astype(np.float32)
+    lg[0] = np.nan
+    lg[1], lg[1, E - 1] = -np.inf, np.nan
+    lg[2, 0] = np.nan
+    lg[3] = -np.inf
+    lg[4, 1:] = -np.inf
+    ids = np.stack([rng.permutation(E)[:3] for _ in range(6)]).astype(np.int32)
+    dw = rng.standard_normal((6, 3)).astype(np.float32)
+    out = q4.q4_moe_topk_backward(*(torch.from_numpy(a).to(DEV) for a in (lg, ids, dw))).cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        ref = grad.topk_backward(lg, ids, dw)
+    assert np.array_equal(np.isnan(out), np.isnan(ref))
+    assert np.isnan(out[:3]).all() and np.all(out[3] == 0) and np.isfinite(out[4:]).all()
 
 
 # every bf16 g whose sigmoid exp(g) is around the smallest normal fp32 number (2^-126: g = -87.34) and still has a

@@ -278,7 +278,9 @@ moe_combine_backward_kernel(const uint16_t* __restrict__ dout, int64_t ldo, cons
 // ---- the gates' gradient -----------------------------------------------------
 // One wave per token, the E <= 64 * PER logits in registers (PER 1, 4 or 16).
 // A token whose logits are all -inf has no softmax; its gradient is written as
-// 0.  8192 tokens of 64 experts: 6 us.
+// 0.  A NaN among them is carried by the sum of the exponentials into the whole
+// row (the maximum alone, which passes over NaN, cannot tell a row of NaN and
+// -inf from one of -inf).  8192 tokens of 64 experts: 6 us.
 constexpr int kTopkWaves = 4;
 
 template <int PER>
@@ -291,15 +293,18 @@ moe_topk_backward_kernel(const float* __restrict__ logits, int64_t ld, int64_t T
   if (t >= T) return;
   float v[PER], d[PER];
   float m = -INFINITY;
+  bool nan = false;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = lane + 64 * i;
     v[i] = e < E ? logits[t * ld + e] : -INFINITY;
     d[i] = 0.0f;
     m = fmaxf(m, v[i]);
+    nan |= v[i] != v[i];
   }
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+  const bool none = m == -INFINITY && __ballot(nan) == 0;
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
@@ -329,7 +334,7 @@ moe_topk_backward_kernel(const float* __restrict__ logits, int64_t ld, int64_t T
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = lane + 64 * i;
-    if (e < E) dl[t * lddl + e] = m == -INFINITY ? 0.0f : v[i] * (d[i] - c);
+    if (e < E) dl[t * lddl + e] = none ? 0.0f : v[i] * (d[i] - c);
   }
 }
 
