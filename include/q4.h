@@ -524,6 +524,17 @@ q4_status q4_grouped_gemm_wgrad(const void* dC_bf16, int64_t lddc, const void* A
                                 void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Which kernel the products take for these sizes (host arithmetic only; the
+ * sizes as in the matching *_workspace call): the rows of a block of outputs
+ * that a workgroup makes, 64, 128 or 256 by 256 columns, and the parts that
+ * its sum is split into; 0 and 0 where nothing is launched.  For tests and
+ * measurements that have to reach a certain block.  a_is_bf16: dW from A_bf16.
+ */
+q4_status q4_dgrad_plan(int64_t P, int32_t E, int64_t N, int64_t K, int32_t* block_rows, int32_t* parts);
+q4_status q4_wgrad_plan(int64_t P, int32_t E, int64_t N, int64_t K, int a_is_bf16, int32_t* block_rows,
+                        int32_t* parts);
+
+/*
  * Measurement helper, not a step of the method: reads `bytes` of device
  * memory at src with a plain streaming kernel (16-byte non-temporal loads,
  * each wave 8 KB in flight) and discards the data.  Decode GEMVs are bound

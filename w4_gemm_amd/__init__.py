@@ -72,7 +72,7 @@ def _lib_handle():
         L = ctypes.CDLL(LIB_PATH)
         i64, vp, i32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32
         P = ctypes.POINTER(_Q4TensorC)
-        sz, SZ = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+        sz, SZ, I32P = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(i32)
         sig = {
             "q4_version": ([], ctypes.c_int),
             "q4_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -103,6 +103,8 @@ def _lib_handle():
             "q4_swiglu_backward": ([vp, i64, P, vp, i64, i64, i64, vp, i64, vp, i64, vp], ctypes.c_int),
             "q4_dgrad_workspace": ([i64, i32, i64, i64, SZ], ctypes.c_int),
             "q4_wgrad_workspace": ([i64, i32, i64, i64, SZ], ctypes.c_int),
+            "q4_dgrad_plan": ([i64, i32, i64, i64, I32P, I32P], ctypes.c_int),
+            "q4_wgrad_plan": ([i64, i32, i64, i64, ctypes.c_int, I32P, I32P], ctypes.c_int),
             "q4_gemm_dgrad": ([i64, vp, i64, P, vp, i64, vp, sz, vp], ctypes.c_int),
             "q4_grouped_gemm_dgrad": ([vp, i64, vp, i32, i64, P, i64, vp, i64, vp, sz, vp], ctypes.c_int),
             "q4_gemm_wgrad": ([i64, vp, i64, vp, i64, P, i64, i64, vp, ctypes.c_int, i64, ctypes.c_int, vp, sz, vp],
@@ -607,12 +609,13 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, k: int, W_gu: Q4Tensor, W_d
 
 
 from .grad import (  # noqa: E402  (uses the helpers above)
-    MoESaved, moe_layer_backward, moe_layer_save, q4_gemm_dgrad, q4_gemm_wgrad, q4_grouped_gemm_dgrad,
+    MoESaved, moe_layer_backward, moe_layer_save, q4_dgrad_plan, q4_gemm_dgrad, q4_gemm_wgrad, q4_grouped_gemm_dgrad,
     q4_grouped_gemm_wgrad, q4_moe_combine_backward, q4_moe_permute, q4_moe_permute_backward, q4_moe_sort, q4_moe_topk,
-    q4_moe_topk_backward, q4_swiglu_backward, q4_swiglu_save)
+    q4_moe_topk_backward, q4_swiglu_backward, q4_swiglu_save, q4_wgrad_plan)
 
 __all__ += [
-    "MoESaved", "moe_layer_backward", "moe_layer_save", "q4_gemm_dgrad", "q4_gemm_wgrad", "q4_grouped_gemm_dgrad",
-    "q4_grouped_gemm_wgrad", "q4_moe_combine_backward", "q4_moe_permute", "q4_moe_permute_backward", "q4_moe_sort",
-    "q4_moe_topk", "q4_moe_topk_backward", "q4_swiglu_backward", "q4_swiglu_save",
+    "MoESaved", "moe_layer_backward", "moe_layer_save", "q4_dgrad_plan", "q4_gemm_dgrad", "q4_gemm_wgrad",
+    "q4_grouped_gemm_dgrad", "q4_grouped_gemm_wgrad", "q4_moe_combine_backward", "q4_moe_permute",
+    "q4_moe_permute_backward", "q4_moe_sort", "q4_moe_topk", "q4_moe_topk_backward", "q4_swiglu_backward",
+    "q4_swiglu_save", "q4_wgrad_plan",
 ]

@@ -104,7 +104,7 @@ hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
 extern "C" {
 
-int q4_version(void) { return 103; }
+int q4_version(void) { return 104; }
 
 const char* q4_status_string(int status) {
   switch (status) {
@@ -613,6 +613,29 @@ q4_status q4_wgrad_workspace(int64_t P, int32_t E, int64_t N, int64_t K, size_t*
   if (P < 0 || E < 0 || E > 65535 || N < 0 || K < 0 || P >= kMaxDim || N > kMaxGradLd || K > kMaxGradLd)
     return Q4_ERR_SHAPE;
   *bytes = E && N && K ? q4::wgrad_workspace(P, E, N, K) : 0;
+  return Q4_OK;
+}
+
+q4_status q4_dgrad_plan(int64_t P, int32_t E, int64_t N, int64_t K, int32_t* block_rows, int32_t* parts) {
+  if (!block_rows || !parts) return Q4_ERR_NULL;
+  size_t bytes = 0;
+  const q4_status st = q4_dgrad_workspace(P, E, N, K, &bytes);
+  if (st != Q4_OK) return st;
+  const q4::GradPlan p = P && E && K ? q4::grad_plan(false, false, P, E, N, K) : q4::GradPlan{0, 0};
+  *block_rows = p.rows;
+  *parts = p.parts;
+  return Q4_OK;
+}
+
+q4_status q4_wgrad_plan(int64_t P, int32_t E, int64_t N, int64_t K, int a_is_bf16, int32_t* block_rows,
+                        int32_t* parts) {
+  if (!block_rows || !parts) return Q4_ERR_NULL;
+  size_t bytes = 0;
+  const q4_status st = q4_wgrad_workspace(P, E, N, K, &bytes);
+  if (st != Q4_OK) return st;
+  const q4::GradPlan p = E && N && K ? q4::grad_plan(true, a_is_bf16 != 0, P, E, N, K) : q4::GradPlan{0, 0};
+  *block_rows = p.rows;
+  *parts = p.parts;
   return Q4_OK;
 }
 

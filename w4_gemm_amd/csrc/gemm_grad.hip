@@ -733,6 +733,10 @@ constexpr int64_t kMaxSum = (int64_t)1 << 30;
 
 }  // namespace
 
+GradPlan grad_plan(bool wgrad, bool a_bf16, int64_t P, int32_t E, int64_t N, int64_t K) {
+  const Plan p = plan(wgrad, P, E, N, K);
+  return {p.block == kBlock64 ? 64 : p.block == kBlock128 || a_bf16 ? 128 : 256, p.splits};
+}
 size_t dgrad_workspace(int64_t P, int32_t E, int64_t N, int64_t K) { return parts_bytes(false, P, E, N, K); }
 size_t wgrad_workspace(int64_t P, int32_t E, int64_t N, int64_t K) { return parts_bytes(true, P, E, N, K); }
 

@@ -217,6 +217,11 @@ struct GradArgs {
   int out_f32, accumulate;
   float* workspace;
 };
+// rows of a block of outputs and parts of the sum, as the launch chooses them
+struct GradPlan {
+  int32_t rows, parts;
+};
+GradPlan grad_plan(bool wgrad, bool a_bf16, int64_t P, int32_t E, int64_t N, int64_t K);
 size_t dgrad_workspace(int64_t P, int32_t E, int64_t N, int64_t K);
 size_t wgrad_workspace(int64_t P, int32_t E, int64_t N, int64_t K);
 // whether the launch stays within 2^32 threads

@@ -314,6 +314,22 @@ def q4_swiglu_backward(gu: Union[torch.Tensor, Q4Tensor], dh: torch.Tensor, dgu:
     return dgu
 
 
+def q4_dgrad_plan(P: int, E: int, N: int, K: int) -> Tuple[int, int]:
+    """(rows of a block of outputs, parts of the sum) that the gradient for the
+    activations takes for these sizes; (0, 0) where nothing is launched."""
+    rows, parts = ctypes.c_int32(), ctypes.c_int32()
+    _check(lib().q4_dgrad_plan(P, E, N, K, ctypes.byref(rows), ctypes.byref(parts)), "q4_dgrad_plan")
+    return rows.value, parts.value
+
+
+def q4_wgrad_plan(P: int, E: int, N: int, K: int, a_is_bf16: bool = False) -> Tuple[int, int]:
+    """The same of the gradient for the weights, from activations in 8 bits or
+    in bf16."""
+    rows, parts = ctypes.c_int32(), ctypes.c_int32()
+    _check(lib().q4_wgrad_plan(P, E, N, K, int(a_is_bf16), ctypes.byref(rows), ctypes.byref(parts)), "q4_wgrad_plan")
+    return rows.value, parts.value
+
+
 def q4_gemm_dgrad(dC: torch.Tensor, W: Q4Tensor, dA: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """dA = dC W' (bf16 [M, K]): the gradient of q4_gemm(A, W) for A."""
     _q4(W, "W")
