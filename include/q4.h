@@ -40,13 +40,20 @@
  *                 2^(b-127).  scale = the least 2^e >= 2^-111 with
  *                 max|x| <= top * 2^e; code = rne(x / scale) as a two's
  *                 complement byte (MXINT8, top = 127) or an E4M3 byte (MXFP8,
- *                 top = 448).  Integers err by up to 1/256 of (nearly) the
- *                 block's largest value everywhere; E4M3 by up to 2^-4 of each
- *                 value: integers suit ordinary blocks, E4M3 blocks in which
- *                 one outlier would leave the rest few codes.  A block with
+ *                 top = 448).  Integers err by at most scale / 2 everywhere:
+ *                 1/254 to 1/127 of the block's largest value, more where
+ *                 that is below 2^-104 (2^-111 is the least scale).  E4M3 errs
+ *                 by at most max(2^-4 |x|, 2^-10 scale) of each value x:
+ *                 integers suit ordinary blocks, E4M3 blocks in which one
+ *                 outlier would leave the rest few codes.  A block with
  *                 an infinity or a NaN has b = 255 and reads back as NaN
  *                 throughout; a code whose value would reach 2^128 is stored
- *                 one lower.  8.25 bits per value.
+ *                 one lower (so the largest bf16 number errs by 3/4 scale in
+ *                 integers).  8.25 bits per value.
+ *                 Not the interchange formats of these names: MXINT8's
+ *                 codes are whole scales, not 64ths of one, and both
+ *                 formats' rule for the scale (the least that does not clip)
+ *                 is this library's own.
  * Every rounding is to nearest, ties to the even code; E2M1 and E4M3 keep
  * the sign bit of the input; a block whose stored scale is 0 has magnitude
  * codes 0.
@@ -107,7 +114,8 @@
  *     argument returns its error code and launches nothing.  A failed launch
  *     returns Q4_ERR_HIP; q4_last_hip_error() gives the hipError_t of the
  *     calling thread's last failure.
- *   - Inputs must be finite.  Calls on distinct outputs may run
+ *   - Inputs must be finite, but where a format or call says what it makes
+ *     of infinities and NaN.  Calls on distinct outputs may run
  *     concurrently; outputs must not alias inputs.
  *   - The first launch of a kernel that uses more than 64 KB of LDS on a
  *     device raises that kernel's LDS limit there (hipFuncSetAttribute, once
