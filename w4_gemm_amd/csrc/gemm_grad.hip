@@ -130,11 +130,8 @@ __device__ __forceinline__ bool find_tile(const int32_t* offsets, int E, int P, 
 // places with their neighbours: again 256 bytes of banks.  The rows of block b
 // are XORed with b % 4, so that threads that write neighbouring blocks of one
 // row meet no bank twice.
-__device__ __forceinline__ int row_place(int r) {        // r in 0..31 -> 0..31
+__device__ __forceinline__ int row_place(int r) {        // r in 0..31 -> 0..31, its own inverse
   return (r & 16) | ((r & 4) << 1) | ((r & 8) >> 1) | (r & 3);
-}
-__device__ __forceinline__ int place_row(int p) {        // its inverse
-  return (p & 16) | ((p & 4) << 1) | ((p & 8) >> 1) | (p & 3);
 }
 __device__ __forceinline__ int place_swap(int p) { return ((p >> 1) ^ (p >> 2)) & 2; }   // on the chunk's number
 __device__ __forceinline__ int column_place(int r, int c, int block_bytes, bool of_b) {
@@ -201,7 +198,8 @@ struct Kern {
   static constexpr int kABytes = R * BM * 2, kBBytes = R * kBK * 2;
   static constexpr int kSmem = kABufs * kABytes + kBBufs * kBBytes;
   static constexpr int kCopies = kABytes / 1024;          // copy instructions per stage
-  static constexpr int kCPW = (kCopies + kWaves - 1) / kWaves;
+  static constexpr int kCPW = kCopies / kWaves;           // per wave: what its waits count
+  static_assert(kCopies % kWaves == 0, "every wave makes as many copies");
 };
 
 // One block of C: of expert e's rows lo .. hi - 1, from row (dgrad) or n (wgrad)
@@ -236,7 +234,7 @@ __device__ __forceinline__ void make_block(const GradArgs& g, uint8_t* const sme
   int aoff[WGRAD ? 1 : C::kCPW];
   if constexpr (WGRAD) {
     const int at = wave * 16 + (lane >> 2), p = at % R, c = at / R * 4 + ((lane & 3) ^ place_swap(p));
-    aoff[0] = (((p & ~31) + place_row(p & 31)) * (int)g.lddc + 8 * c) * 2;
+    aoff[0] = (((p & ~31) + row_place(p & 31)) * (int)g.lddc + 8 * c) * 2;
   } else {
 #pragma unroll
     for (int q = 0; q < C::kCPW; ++q) {
@@ -257,7 +255,6 @@ __device__ __forceinline__ void make_block(const GradArgs& g, uint8_t* const sme
 #pragma unroll
     for (int q = 0; q < C::kCPW; ++q) {
       const int ci = wave + C::kWaves * q;
-      if (C::kCopies % C::kWaves != 0 && ci >= C::kCopies) continue;
       int off;
       if constexpr (WGRAD) {
         off = aoff[0];
@@ -342,7 +339,7 @@ __device__ __forceinline__ void make_block(const GradArgs& g, uint8_t* const sme
   // ---- a stage is kGroups groups of kGT row tiles by all of the wave's
   // column tiles; the fragments of a group are read under the group before
   constexpr int kGT = C::kSteps == 1 && kMT > 4 ? 2 : 1, kG = kMT / kGT, kGroups = C::kSteps * kG;
-  static_assert(kGroups == 2 || kGroups >= 4, "the loads, copies and conversions of a stage come before its last group");
+  static_assert(kGroups >= 4, "the loads, copies and conversions of a stage come before its last group");
   bf16x8_t fa[2][kGT], fb[C::kKT];
   // (step s is 32 rows on, the second half of a fragment 8 places)
   // this lane's addresses in A's buffer of the stage being read (opaque, so
@@ -432,9 +429,8 @@ __device__ __forceinline__ void make_block(const GradArgs& g, uint8_t* const sme
         __builtin_amdgcn_sched_barrier(0);
         // pieces of stages u + 1 and u + 2; groups that load, copy and convert
         constexpr int kNext = kSets == 2 ? 1 - J : 0, kLoad = kSets == 2 ? J : 0;
-        constexpr int kPer = kGroups == 2 || (kSets == 1 && kGroups == 4) ? 4 : 2;
-        constexpr int kConv = kSets == 2 && kGroups > 2 ? 1 : 0;
-        constexpr int kLoadAt = kSets == 2 ? 0 : 4 / kPer, kCopyAt = kGroups == 2 ? 0 : kLoadAt + 1;
+        constexpr int kPer = 2, kConv = kSets == 2 ? 1 : 0;
+        constexpr int kLoadAt = kSets == 2 ? 0 : 4 / kPer, kCopyAt = kLoadAt + 1;
         static_assert(kCopyAt < kGroups - 1 && kConv + 4 / kPer <= kGroups - 1, "before the last group's wait");
         if (gi == kLoadAt) {
           load_b(raw[kLoad], idx[J], ok[kLoad]);
