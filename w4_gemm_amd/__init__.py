@@ -6,7 +6,8 @@ This module is the thin Python binding of libq4.so's C ABI (include/q4.h):
 the functions have the same names and only marshal arguments -- torch
 tensors supply device memory and the current HIP stream, every step of the
 computation runs in the library's kernels.  There is no CPU fallback: if the
-library cannot be loaded, every call raises.
+library cannot be loaded, every call raises.  No call records itself for
+torch's differentiation (w4_gemm_amd/grad.py has the gradients).
 """
 from __future__ import annotations
 

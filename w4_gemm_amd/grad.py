@@ -7,6 +7,12 @@ Without `stream` the work goes to that device's current stream; outputs and
 workspaces that a call allocates belong to the stream it runs on (a caller that
 passes another stream than the current one orders the two, as with torch's own
 operators).
+
+No call, here or in the package, records itself for torch's differentiation: its
+outputs never require gradients, also where its inputs do, so a graph that runs
+through one ends there without an error.  A model that torch differentiates
+calls a forward function in the `forward` of a torch.autograd.Function and its
+gradient in the `backward`.
 """
 from __future__ import annotations
 
