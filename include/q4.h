@@ -494,8 +494,8 @@ q4_status q4_swiglu_backward(const void* gu_bf16, int64_t ld_gu, const q4_tensor
  * over the rows p of expert e (q4_gemm_dgrad: one dense weight, all rows).
  * bf16 matrix cores, fp32 sums, bf16 output.  W: any weight format, either
  * layout, as the forward call takes it; INT4 weights (with or without a zero
- * point) are rounded to bf16 as in the forward products, MXFP4 and NVFP4 enter
- * exactly.  dC_bf16 [P][lddc], dA_bf16 [P][ldda]; N % 8 == 0 (16 for the
+ * point) are rounded to bf16 as in q4_gemm from bf16 and q4_grouped_gemm, MXFP4
+ * and NVFP4 enter exactly.  dC_bf16 [P][lddc], dA_bf16 [P][ldda]; N % 8 == 0 (16 for the
  * grouped call in the tiled layout), K % 128 == 0.  expert_offsets as in
  * q4_grouped_gemm; rows of dA outside every expert's range are left as they
  * were.  N == 0 writes zeros.

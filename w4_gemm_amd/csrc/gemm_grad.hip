@@ -27,11 +27,13 @@
 //     buffers).
 //   * The outputs go out as whole cache lines (see the epilogue).
 //
-// What bounds it.  Dense: the matrix pipe is busy 58% of the time (back to back,
-// dgrad 4096 x 8192 x 8192 495 us = 1110 TF/s, wgrad 8192^3 950 us = 1160); a
-// loop of nothing but the stage's matrix, LDS and conversion instructions
-// reaches about 1430 under the card's power limit.  Grouped wgrad (64 x 2048 x
-// 7168, 32768 ragged rows, 1.30 - 1.34 ms): 3.8 GB of fp32 gradients, whose stores take
+// What bounds it.  Dense: the matrix pipe is busy 60% of the time (back to back:
+// dgrad 4096 x 8192 x 8192, INT4, 450 us = 1220 TF/s, wgrad 8192^3 930 us = 1180,
+// after some 50 passes; the first ten after an idle moment take a fifth longer,
+// 540 and 1080); a loop of nothing but the stage's matrix, LDS and conversion
+// instructions reaches about 1430 under the card's power limit.  Grouped dgrad
+// (64 x 2048 x 7168, 32768 ragged rows, MXFP4): 950 us, 1010 at first.  Grouped
+// wgrad (the same, 1.30 - 1.35 ms): 3.8 GB of fp32 gradients, whose stores take
 // 0.68 ms alone; the products take 0.95 ms alone, and the two add up by more
 // than half, since a CU's loads queue behind its stores.  (Not mended by
 // delaying every other workgroup, by a persistent workgroup that loads the next

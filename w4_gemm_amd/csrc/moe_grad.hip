@@ -36,8 +36,8 @@ __device__ __forceinline__ void store_past(uint16_t* p, uint4 v) {
 // writes each chunk's counts per expert to the workspace and every workgroup
 // of the second sums them over the chunks before its own (and over all, for
 // the offsets): at most 256 chunks, so that this reads at most 256 E words per
-// workgroup from L2.  Bound by latency: 8 choices 3.9 us, 131080 choices of 64
-// experts 2.7 + 7.8 us.
+// workgroup from L2.  Bound by latency: 8 choices 4.0 us, 131080 choices of 64
+// experts 4.8 + 7.9 us.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int64_t kSortMaxChunks = 256;
@@ -232,7 +232,7 @@ moe_permute_backward_kernel(const uint16_t* __restrict__ dxs, int64_t lds_, cons
 // A workgroup per token, a wave per choice (waves take every blockDim/64-th):
 // the wave walks the row, so dw's sum stays inside it, and dout[t] is read from
 // the cache by the other waves.  Bound by HBM: 8192 tokens of 8 choices, 7168
-// columns, 390 us, 2.0 GB at 5.1 TB/s (a plain copy reaches 4.8).
+// columns, 394 us, 2.0 GB at 5.1 TB/s (a plain copy reaches 4.8).
 template <bool GATES>
 __global__ void __launch_bounds__(512)
 moe_combine_backward_kernel(const uint16_t* __restrict__ dout, int64_t ldo, const uint16_t* __restrict__ y, int64_t ldy,
@@ -280,7 +280,7 @@ moe_combine_backward_kernel(const uint16_t* __restrict__ dout, int64_t ldo, cons
 // A token whose logits are all -inf has no softmax; its gradient is written as
 // 0.  A NaN among them is carried by the sum of the exponentials into the whole
 // row (the maximum alone, which passes over NaN, cannot tell a row of NaN and
-// -inf from one of -inf).  8192 tokens of 64 experts: 6 us.
+// -inf from one of -inf).  8192 tokens of 64 experts: 7 us.
 constexpr int kTopkWaves = 4;
 
 template <int PER>

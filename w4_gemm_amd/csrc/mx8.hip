@@ -9,7 +9,9 @@
 // bf16 at the end.
 //
 // Bound by HBM, each value read and written once: quantize 8192 x 8192 (203 MB)
-// 35 us, 5.8 TB/s; SwiGLU that saves, 32768 x 2 x 2048 (540 MB) 92 us, 5.9.
+// 35 us, 5.8 TB/s, dequantize 31 us; SwiGLU of 32768 x 2 x 2048 (540 MB each way)
+// 94 us to save and 80 back, each repeated by itself, 84 + 99 one after the
+// other (of so few bytes the caches still hold a part for the next call).
 // A block's maximum takes two lane exchanges, so nothing is staged in LDS.
 #include "q4_device.h"
 #include "q4_launch.h"
@@ -44,7 +46,7 @@ __device__ __forceinline__ float sigmoid(float g) {
 }
 
 // Rows that the next kernel reads from far behind: written past the caches
-// (gradient of 32768 x 2 x 2048: 95 -> 82 us, 540 MB at 6.6 TB/s).
+// (gradient of 32768 x 2 x 2048, repeated: 95 -> 80 us).
 __device__ __forceinline__ void store_past(uint16_t* p, u32x4_t v) {
   __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(p));
 }

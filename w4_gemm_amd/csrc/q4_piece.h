@@ -10,15 +10,21 @@
 // lanes are consecutive, 32 where they are 64 bytes apart, 64 where each lane
 // is on a row of its own (measured).  So:
 //   4-bit weights  one load of 32 columns; lane l row l % 16, columns
-//                  32 (l / 16): in the tiled layout one contiguous kilobyte
+//                  32 (l / 16): in the tiled layout one contiguous kilobyte.
+//                  (Row-major it is the slow case, but there are few loads and
+//                  they run under the products: dA 4096 x 8192 x 8192 MXFP4
+//                  405 us, tiled 410; 16 rows 24.3 and 24.5.)
 //   8-bit          two loads of 16 columns, 16 b + 128 h for lane b of 8
 //   bf16           four loads of 8 columns, 8 b + 64 i for lane b of 8
 //
 // Every conversion is exact except INT4's (with or without a zero point): an
 // integer of 4 bits times an fp16 scale has up to 15 significant bits and is
-// rounded once to bf16, as the forward W4A16 products round it.  NVFP4's
-// tensor scale is left out (code times E4M3 has at most 6 significant bits);
-// the products apply it to their fp32 sums.
+// rounded once to bf16, as the forward W4A16 and grouped products round it.  An
+// output is then off by 2.4e-3 (2-norms) in place of the 1.7e-3 of its own
+// rounding to bf16, against 1e-1 by which INT4 itself is off; the weight's
+// second bf16 term would take every product twice.  NVFP4's tensor scale is
+// left out (code times E4M3 has at most 6 significant bits); the products apply
+// it to their fp32 sums.
 #pragma once
 
 #include "q4_layout.h"
