@@ -406,7 +406,7 @@ q4_status q4_moe_combine(const void* y_bf16, int64_t ldy, const int32_t* inv, co
 
 /*
  * The first half of q4_moe_route, for any number of tokens: the k largest
- * logits' ids and softmax gates.  T < 2^26.
+ * logits' ids and softmax gates.  T <= 2^26 - 4, here and in its gradient.
  */
 q4_status q4_moe_topk(const float* logits, int64_t ld, int64_t T, int32_t E, int32_t k,
                       int32_t* topk_ids, float* topk_weights, void* stream);

@@ -13,7 +13,7 @@ thread_local int g_last_hip_error = 0;
 
 constexpr int64_t kMaxDim = (int64_t)1 << 31;  // kernels index rows/cols in int
 constexpr int64_t kMaxGradLd = (int64_t)1 << 21;      // the gradient products address 256 rows in 2^30 bytes
-constexpr int64_t kMaxTopkTokens = (int64_t)1 << 26;  // a wave per token, within 2^32 threads
+constexpr int64_t kMaxTopkTokens = ((int64_t)1 << 26) - 4;  // a wave per token, four a workgroup: below 2^32 threads
 
 int block_of(int fmt) {
   switch (fmt) {
@@ -455,7 +455,7 @@ q4_status q4_read_probe(const void* src, int64_t bytes, uint32_t* sink, void* st
 
 q4_status q4_moe_topk(const float* logits, int64_t ld, int64_t T, int32_t E, int32_t k, int32_t* topk_ids,
                       float* topk_weights, void* stream) {
-  if (T < 0 || T >= kMaxTopkTokens || E < 1 || E > 1024 || k < 1 || k > 32 || k > E) return Q4_ERR_SHAPE;
+  if (T < 0 || T > kMaxTopkTokens || E < 1 || E > 1024 || k < 1 || k > 32 || k > E) return Q4_ERR_SHAPE;
   if (T == 0) return Q4_OK;
   if (!logits || !topk_ids || !topk_weights) return Q4_ERR_NULL;
   if (ld < E) return Q4_ERR_SHAPE;
@@ -466,7 +466,7 @@ q4_status q4_moe_topk(const float* logits, int64_t ld, int64_t T, int32_t E, int
 q4_status q4_moe_topk_backward(const float* logits, int64_t ld, int64_t T, int32_t E, int32_t k,
                                const int32_t* topk_ids, const float* dweights, float* dlogits, int64_t lddl,
                                void* stream) {
-  if (T < 0 || T >= kMaxTopkTokens || E < 1 || E > 1024 || k < 1 || k > 32) return Q4_ERR_SHAPE;
+  if (T < 0 || T > kMaxTopkTokens || E < 1 || E > 1024 || k < 1 || k > 32) return Q4_ERR_SHAPE;
   if (T == 0) return Q4_OK;
   if (!logits || !topk_ids || !dweights || !dlogits) return Q4_ERR_NULL;
   if (ld < E || lddl < E) return Q4_ERR_SHAPE;
