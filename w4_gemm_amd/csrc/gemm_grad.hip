@@ -703,10 +703,9 @@ hipError_t run(const GradArgs& g, int splits, hipStream_t stream) {
 
 template <bool WGRAD, int KIND, int LAYOUT, bool GATHER>
 hipError_t run_plan(const GradArgs& g, hipStream_t stream) {
-  const Plan p = plan(WGRAD, g.P, g.E, g.N, g.K);
-  if (p.block == kBlock64) return run<WGRAD, KIND, LAYOUT, GATHER, 1, 4, 4>(g, p.splits, stream);
-  // (bf16 activations fill the registers of the 256-row block)
-  if (p.block == kBlock128 || KIND == kBf16Piece) return run<WGRAD, KIND, LAYOUT, GATHER, 1, 4, 8>(g, p.splits, stream);
+  const GradPlan p = grad_plan(WGRAD, KIND == kBf16Piece, g.P, g.E, g.N, g.K);
+  if (p.rows == 64) return run<WGRAD, KIND, LAYOUT, GATHER, 1, 4, 4>(g, p.parts, stream);
+  if (p.rows == 128 || KIND == kBf16Piece) return run<WGRAD, KIND, LAYOUT, GATHER, 1, 4, 8>(g, p.parts, stream);
   if constexpr (KIND != kBf16Piece) return run<WGRAD, KIND, LAYOUT, GATHER, 2, 4, 8>(g, 1, stream);
 }
 
@@ -733,6 +732,7 @@ constexpr int64_t kMaxSum = (int64_t)1 << 30;
 
 GradPlan grad_plan(bool wgrad, bool a_bf16, int64_t P, int32_t E, int64_t N, int64_t K) {
   const Plan p = plan(wgrad, P, E, N, K);
+  // (bf16 activations fill the registers of the 256-row block)
   return {p.block == kBlock64 ? 64 : p.block == kBlock128 || a_bf16 ? 128 : 256, p.splits};
 }
 size_t dgrad_workspace(int64_t P, int32_t E, int64_t N, int64_t K) { return parts_bytes(false, P, E, N, K); }
