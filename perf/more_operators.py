@@ -144,9 +144,10 @@ def _normed(h, weight):
 
 
 def _rows8(v):
-    """(codes as whole numbers, scales) of rows of 32-bit values in 8-bit integers."""
-    s = torch.clamp_min(v.abs().amax(1), 1e-12) / 127
-    return torch.clamp(torch.round(v / s[:, None]), -127, 127), s
+    """(codes as whole numbers, scales) of rows of 32-bit values in 8-bit integers: each value times the 32-bit 127 / amax,
+    rounded to nearest, ties to even (a product of 24 bits by 24 has its place in 64)."""
+    most = torch.clamp_min(v.abs().amax(1), 1e-12)
+    return torch.round(v.double() * (127 / most).double()[:, None]).float(), most / 127
 
 
 def _pow2(e):
@@ -262,8 +263,8 @@ def work(case):
 # ------------------------------------------------------- in 64 bits, apart
 
 def _exact_rows8(v):
-    s = (v.abs().amax(1).clamp(min=1e-12) / 127).to(F32).to(F64)
-    return torch.clamp((v / s[:, None]).round(), -127, 127), s
+    most = v.abs().amax(1).clamp(min=1e-12)
+    return torch.clamp((v * (127 / most)[:, None]).round(), -127, 127), most / 127
 
 
 def _exact_norm(st):
