@@ -34,6 +34,14 @@
  *                 E4M3(clamp(x/scale, +-448)).  ("Quantization in
  *                 deployment", formats.py fp8() per row; "Quantization
  *                 chains", "One outlier sets the scale".)
+ *   Q4_INT8_ROW   both operands of W8A8: one two's complement byte per value
+ *                 and one fp32 scale per row (a token of the activations, an
+ *                 output channel of a weight), with a = max(amax_row, 1e-12):
+ *                 scale = a/127, code = rne(x * fp32(127/a)) of the exact
+ *                 product, so -127..127.  A row with an infinity or a NaN gets
+ *                 the scale NaN, and every product with it is NaN.
+ *                 ("Quantization in deployment", format cheat sheet, W8A8;
+ *                 "LLM quantization", the absmax method.)
  *   Q4_MXINT8, Q4_MXFP8  activations saved for the backward pass, not an
  *                 operand of a W4 product: one byte per value and one
  *                 power-of-two scale per 32 values, stored as the byte b of
@@ -98,6 +106,9 @@
  *              16..31 at 1024 + 16l.  Padding rows hold code 0.
  *   scales     fp32 [rows] in both layouts; global_scale is NULL.
  *
+ * Q4_INT8_ROW (row-major only, cols % 16 == 0): codes int8 [rows][cols],
+ *   scales fp32 [rows]; global_scale is NULL.
+ *
  * Q4_MXINT8 and Q4_MXFP8 (row-major only, cols % 32 == 0): codes uint8
  *   [rows][cols], scales uint8 [rows][cols/32]; global_scale is NULL.
  *
@@ -138,7 +149,8 @@ typedef enum q4_format {
     Q4_FP8_ROW = 3,
     Q4_INT4_ZP_G128 = 4,
     Q4_MXFP8 = 5,
-    Q4_MXINT8 = 6
+    Q4_MXINT8 = 6,
+    Q4_INT8_ROW = 8 /* (7 is no format) */
 } q4_format;
 
 typedef enum q4_layout {
@@ -212,7 +224,8 @@ q4_status q4_relayout(const q4_tensor* src, const q4_tensor* dst, void* stream);
  * and written to dst->global_scale.  nv_global_in must be NULL for the other
  * formats.  rows == 0 or cols == 0 is a no-op (for NVFP4 without
  * nv_global_in, gs is still written: max(0,1e-12)/2688).  Q4_FP8_ROW
- * quantizes each row with its own scale (the W4A8 activations).
+ * quantizes each row with its own scale (the W4A8 activations), Q4_INT8_ROW
+ * likewise (W8A8's activations and weights; rows < 2^22, else Q4_ERR_SHAPE).
  */
 q4_status q4_quantize(const void* src_bf16, int64_t ld, const q4_tensor* dst,
                       const float* nv_global_in, void* stream);
@@ -264,6 +277,11 @@ q4_status q4_gemv(const q4_tensor* W, const void* x_bf16, int64_t B, int64_t ldx
  *                       table, row W4A8; "Quantization in deployment", the
  *                       per-block promotion of block-scaled FP8 GEMMs);
  *                       C = s_a[m] * sum_g s_w[n][g] * sum_(k in g) a8*q.
+ *   A_q (Q4_INT8_ROW, rows M, cols K) with W Q4_INT8_ROW -> W8A8: sums of
+ *                       products of bytes, exact in 32-bit integers (K < 2^17,
+ *                       else Q4_ERR_SHAPE), one scale of the token and one of
+ *                       the channel on the sum:
+ *                       C = (s_a[m] * s_w[n]) * sum_k a8*w8.
  * Other format pairs, and a Q4_FP8_ROW W: Q4_ERR_FORMAT.
  * K = W->cols must be a multiple of 128.  M == 0 or N == 0 is a no-op.
  */

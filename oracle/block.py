@@ -1,0 +1,31 @@
+"""Plain definitions (numpy, fp64) of what stands around the products of a
+block: rows in 8-bit integers and their product.  Nothing is shared with the
+GPU path.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+
+def int8_rows(x: np.ndarray):
+    """(codes int8 [rows, cols], scales fp32 [rows]) of fp32 x.  The factor
+    127 / a and the scale a / 127 are fp32 quotients; a product of two fp32
+    values is exact in fp64, so rint rounds it once, ties to even."""
+    codes = np.zeros(x.shape, np.int8)
+    scales = np.zeros(x.shape[0], np.float32)
+    for r in range(x.shape[0]):
+        if not np.all(np.isfinite(x[r])):
+            scales[r] = np.nan
+            continue
+        a = max(np.float32(np.max(np.abs(x[r]), initial=0.0)), np.float32(1e-12))
+        f = np.float32(127.0) / a
+        codes[r] = np.rint(x[r].astype(np.float64) * np.float64(f)).astype(np.int8)
+        scales[r] = a / np.float32(127.0)
+    return codes, scales
+
+
+def int8_product(ac: np.ndarray, asc: np.ndarray, wc: np.ndarray, wsc: np.ndarray) -> np.ndarray:
+    """s_a[m] s_w[n] sum_k a[m, k] w[n, k] (fp64; the sum is a whole number
+    below 2^53, so exact)."""
+    s = ac.astype(np.float64) @ wc.astype(np.float64).T
+    return s * asc.astype(np.float64)[:, None] * wsc.astype(np.float64)[None, :]

@@ -25,15 +25,17 @@ __all__ = [
     "lib", "q4_version", "q4_sizes", "q4_quantize", "q4_dequant", "q4_relayout", "relayout", "q4_gemv", "q4_gemm", "q4_gemm_quantized",
     "q4_grouped_gemm", "q4_grouped_gemm_swiglu", "q4_moe_route", "q4_swiglu", "q4_moe_combine",
     "moe_layer", "interleave_gate_up", "q4_read_probe", "q4_mfma_probe", "PROBE_KINDS", "PROBE_MIX_SINK",
-    "empty_q4", "quantize", "LIB_PATH", "MXFP8", "MXINT8",
+    "empty_q4", "quantize", "LIB_PATH", "MXFP8", "MXINT8", "INT8_ROW",
 ]
 
 INT4_G128, MXFP4, NVFP4, FP8_ROW, INT4_ZP, MXFP8, MXINT8 = 0, 1, 2, 3, 4, 5, 6
+INT8_ROW = 8
 FORMAT_NAMES = {"int4": INT4_G128, "mxfp4": MXFP4, "nvfp4": NVFP4, "fp8_row": FP8_ROW, "int4_zp": INT4_ZP,
-                "mxfp8": MXFP8, "mxint8": MXINT8}
+                "mxfp8": MXFP8, "mxint8": MXINT8, "int8_row": INT8_ROW}
 LAYOUT_ROWS, LAYOUT_TILED = 0, 1
 LAYOUT_NAMES = {"rows": LAYOUT_ROWS, "tiled": LAYOUT_TILED}
-GROUP = {INT4_G128: 128, MXFP4: 32, NVFP4: 16, FP8_ROW: 16, INT4_ZP: 128, MXFP8: 32, MXINT8: 32}
+GROUP = {INT4_G128: 128, MXFP4: 32, NVFP4: 16, FP8_ROW: 16, INT4_ZP: 128, MXFP8: 32, MXINT8: 32,
+         INT8_ROW: 16}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libq4.so")
@@ -237,6 +239,8 @@ class Q4Tensor:
     global_scale  NVFP4: float32 [1] (dequant multiplier); else None
     FP8_ROW (W4A8 activations): codes uint8 [rows, cols] E4M3 (flat when
       tiled), scales float32 [rows].
+    INT8_ROW (both operands of W8A8, row-major only): codes int8 [rows, cols],
+      scales float32 [rows].
     MXFP8, MXINT8 (saved activations, row-major only): codes uint8
       [rows, cols], scales uint8 [rows, cols/32].
     """
@@ -290,6 +294,9 @@ def empty_q4(fmt, rows: int, cols: int, device="cuda", layout=LAYOUT_ROWS) -> Q4
                             device=device)
         return Q4Tensor(f, rows, cols, codes, torch.empty(rows, dtype=torch.float32, device=device),
                         None, lay)
+    if f == INT8_ROW:
+        return Q4Tensor(f, rows, cols, torch.empty(rows, cols, dtype=torch.int8, device=device),
+                        torch.empty(rows, dtype=torch.float32, device=device), None, lay)
     g = GROUP[f]
     if f in (MXFP8, MXINT8):
         return Q4Tensor(f, rows, cols, torch.empty(rows, cols, dtype=torch.uint8, device=device),
@@ -312,10 +319,9 @@ def q4_quantize(src: torch.Tensor, dst: Q4Tensor, nv_global_in: Optional[torch.T
     _q4(dst, "dst")
     if nv_global_in is not None:
         _vector(nv_global_in, "nv_global_in", torch.float32, 1)
-    _on_gpu(("src", src), ("dst", dst), ("nv_global_in", nv_global_in))
-    desc = dst.c()
-    _check(lib().q4_quantize(_ptr(src), src.stride(0), ctypes.byref(desc), _ptr(nv_global_in),
-                             _stream(stream)), "q4_quantize")
+    with _place(stream, ("src", src), ("dst", dst), ("nv_global_in", nv_global_in)) as (_, s):
+        desc = dst.c()
+        _check(lib().q4_quantize(_ptr(src), src.stride(0), ctypes.byref(desc), _ptr(nv_global_in), s), "q4_quantize")
     return dst
 
 
@@ -357,10 +363,9 @@ def q4_dequant(src: Q4Tensor, dst: torch.Tensor, stream=None) -> torch.Tensor:
         raise ValueError("dst must be bf16 or float32")
     _matrix(dst, "dst", dst.dtype, src.rows, src.cols)
     _q4(src, "src")
-    _on_gpu(("src", src), ("dst", dst))
-    desc = src.c()
-    _check(lib().q4_dequant(ctypes.byref(desc), _ptr(dst), dt, dst.stride(0), _stream(stream)),
-           "q4_dequant")
+    with _place(stream, ("src", src), ("dst", dst)) as (_, s):
+        desc = src.c()
+        _check(lib().q4_dequant(ctypes.byref(desc), _ptr(dst), dt, dst.stride(0), s), "q4_dequant")
     return dst
 
 
@@ -378,8 +383,8 @@ def q4_gemv(W: Q4Tensor, x: torch.Tensor, y: torch.Tensor, stream=None) -> torch
 
 def q4_gemm(A, W: Q4Tensor, C: torch.Tensor, stream=None) -> torch.Tensor:
     """C = A' W'^T.  A is a bf16 tensor [M, K] (W4A16), an MXFP4 or NVFP4
-    Q4Tensor (W4A4, with W in the same format) or an FP8_ROW Q4Tensor (W4A8,
-    with W INT4)."""
+    Q4Tensor (W4A4, with W in the same format), an FP8_ROW Q4Tensor (W4A8,
+    with W INT4) or an INT8_ROW Q4Tensor (W8A8, with W INT8_ROW)."""
     _q4(W, "W")
     if isinstance(A, Q4Tensor):
         _q4(A, "A")
@@ -390,16 +395,14 @@ def q4_gemm(A, W: Q4Tensor, C: torch.Tensor, stream=None) -> torch.Tensor:
         _matrix(A, "A", torch.bfloat16, 0, W.cols, exact_cols=True)
         M = A.shape[0]
     _matrix(C, "C", torch.bfloat16, M, W.rows)
-    _on_gpu(("W", W), ("A", A), ("C", C))
-    wd = W.c()
-    if isinstance(A, Q4Tensor):
-        ad = A.c()
-        st = lib().q4_gemm(A.rows, None, 0, ctypes.byref(ad), ctypes.byref(wd), _ptr(C),
-                           C.stride(0), _stream(stream))
-    else:
-        st = lib().q4_gemm(A.shape[0], _ptr(A), A.stride(0), None, ctypes.byref(wd), _ptr(C),
-                           C.stride(0), _stream(stream))
-    _check(st, "q4_gemm")
+    with _place(stream, ("W", W), ("A", A), ("C", C)) as (_, s):
+        wd = W.c()
+        if isinstance(A, Q4Tensor):
+            ad = A.c()
+            st = lib().q4_gemm(A.rows, None, 0, ctypes.byref(ad), ctypes.byref(wd), _ptr(C), C.stride(0), s)
+        else:
+            st = lib().q4_gemm(A.shape[0], _ptr(A), A.stride(0), None, ctypes.byref(wd), _ptr(C), C.stride(0), s)
+        _check(st, "q4_gemm")
     return C
 
 
@@ -610,7 +613,7 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, k: int, W_gu: Q4Tensor, W_d
 
 
 from .grad import (  # noqa: E402  (uses the helpers above)
-    MoESaved, moe_layer_backward, moe_layer_save, q4_dgrad_plan, q4_gemm_dgrad, q4_gemm_wgrad, q4_grouped_gemm_dgrad,
+    _place, MoESaved, moe_layer_backward, moe_layer_save, q4_dgrad_plan, q4_gemm_dgrad, q4_gemm_wgrad, q4_grouped_gemm_dgrad,
     q4_grouped_gemm_wgrad, q4_moe_combine_backward, q4_moe_permute, q4_moe_permute_backward, q4_moe_sort, q4_moe_topk,
     q4_moe_topk_backward, q4_swiglu_backward, q4_swiglu_save, q4_wgrad_plan)
 

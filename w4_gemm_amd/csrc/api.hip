@@ -13,6 +13,8 @@ thread_local int g_last_hip_error = 0;
 
 constexpr int64_t kMaxDim = (int64_t)1 << 31;  // kernels index rows/cols in int
 constexpr int64_t kMaxGradLd = (int64_t)1 << 21;      // the gradient products address 256 rows in 2^30 bytes
+constexpr int64_t kMaxRows = ((int64_t)1 << 22) - 1;    // up to 1024 threads per row: below 2^32 threads
+constexpr int64_t kMaxIntK = (int64_t)1 << 17;        // 2^14 K < 2^31: sums of products of two bytes stay exact
 constexpr int64_t kMaxTopkTokens = ((int64_t)1 << 26) - 4;  // a wave per token, four a workgroup: below 2^32 threads
 
 int block_of(int fmt) {
@@ -20,7 +22,8 @@ int block_of(int fmt) {
     case Q4_INT4_G128: return 128;
     case Q4_MXFP4: return 32;
     case Q4_NVFP4: return 16;
-    case Q4_FP8_ROW: return 16;  // row-major rows are stored in 16-byte pieces
+    case Q4_FP8_ROW:
+    case Q4_INT8_ROW: return 16;  // row-major rows are stored in 16-byte pieces
     case Q4_INT4_ZP_G128: return 128;
     case Q4_MXFP8:
     case Q4_MXINT8: return 32;
@@ -30,7 +33,10 @@ int block_of(int fmt) {
 
 // The saved-activation formats: row-major only, no operand of a W4 product.
 bool is_mx8(int fmt) { return fmt == Q4_MXFP8 || fmt == Q4_MXINT8; }
-bool is_weight(int fmt) { return fmt != Q4_FP8_ROW && !is_mx8(fmt); }
+// One byte per value, one fp32 scale per row.
+bool is_row8(int fmt) { return fmt == Q4_FP8_ROW || fmt == Q4_INT8_ROW; }
+bool rows_only(int fmt) { return is_mx8(fmt) || fmt == Q4_INT8_ROW; }
+bool is_weight(int fmt) { return !is_row8(fmt) && !is_mx8(fmt); }  // in 4 bits
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -47,7 +53,7 @@ q4_status check_tensor(const q4_tensor* t) {
   if (!t) return Q4_ERR_NULL;
   const int g = block_of(t->fmt);
   if (!g || (t->layout != Q4_LAYOUT_ROWS && t->layout != Q4_LAYOUT_TILED)) return Q4_ERR_FORMAT;
-  if (is_mx8(t->fmt) && t->layout != Q4_LAYOUT_ROWS) return Q4_ERR_FORMAT;
+  if (rows_only(t->fmt) && t->layout != Q4_LAYOUT_ROWS) return Q4_ERR_FORMAT;
   if (t->rows < 0 || t->cols < 0 || t->rows >= kMaxDim || t->cols >= kMaxDim) return Q4_ERR_SHAPE;
   if (t->cols % (t->layout == Q4_LAYOUT_TILED ? 512 : g)) return Q4_ERR_SHAPE;
   if (t->fmt == Q4_NVFP4) {
@@ -104,7 +110,7 @@ hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
 extern "C" {
 
-int q4_version(void) { return 104; }
+int q4_version(void) { return 105; }
 
 const char* q4_status_string(int status) {
   switch (status) {
@@ -124,13 +130,13 @@ q4_status q4_sizes(int fmt, int layout, int64_t rows, int64_t cols, size_t* code
                    size_t* scales_bytes) {
   const int g = block_of(fmt);
   if (!g || (layout != Q4_LAYOUT_ROWS && layout != Q4_LAYOUT_TILED)) return Q4_ERR_FORMAT;
-  if (is_mx8(fmt) && layout != Q4_LAYOUT_ROWS) return Q4_ERR_FORMAT;
+  if (rows_only(fmt) && layout != Q4_LAYOUT_ROWS) return Q4_ERR_FORMAT;
   if (rows < 0 || cols < 0 || rows >= kMaxDim || cols >= kMaxDim) return Q4_ERR_SHAPE;
   if (cols % (layout == Q4_LAYOUT_TILED ? 512 : g)) return Q4_ERR_SHAPE;
   // the tiled layout stores whole 16-row tiles; per stored row both layouts
   // hold cols/2 code bytes and cols/g scales (fp16 for INT4)
   const size_t srows = layout == Q4_LAYOUT_TILED ? (size_t)((rows + 15) / 16) * 16 : (size_t)rows;
-  if (fmt == Q4_FP8_ROW) {  // one byte per value, one fp32 scale per row
+  if (is_row8(fmt)) {  // one byte per value, one fp32 scale per row
     if (codes_bytes) *codes_bytes = srows * (size_t)cols;
     if (scales_bytes) *scales_bytes = (size_t)rows * 4;
     return Q4_OK;
@@ -159,6 +165,12 @@ q4_status q4_quantize(const void* src_bf16, int64_t ld, const q4_tensor* dst,
     return hip_status(q4::launch_fp8_rows_quantize(dst->layout, static_cast<const uint16_t*>(src_bf16), ld,
                                                    dst->rows, dst->cols, static_cast<uint8_t*>(dst->codes),
                                                    static_cast<float*>(dst->scales), as_stream(stream)));
+  if (dst->fmt == Q4_INT8_ROW) {
+    if (dst->rows > kMaxRows) return Q4_ERR_SHAPE;
+    return hip_status(q4::launch_int8_rows_quantize(static_cast<const uint16_t*>(src_bf16), ld, dst->rows, dst->cols,
+                                                    static_cast<uint8_t*>(dst->codes),
+                                                    static_cast<float*>(dst->scales), as_stream(stream)));
+  }
   if (is_mx8(dst->fmt))
     return hip_status(q4::launch_mx8_quantize(dst->fmt, static_cast<const uint16_t*>(src_bf16), ld, dst->rows,
                                               dst->cols, static_cast<uint8_t*>(dst->codes),
@@ -181,6 +193,10 @@ q4_status q4_dequant(const q4_tensor* src, void* dst, int dst_dtype, int64_t ld,
     return hip_status(q4::launch_fp8_rows_dequant(src->layout, static_cast<const uint8_t*>(src->codes),
                                                   static_cast<const float*>(src->scales), src->rows,
                                                   src->cols, dst, dst_dtype, ld, as_stream(stream)));
+  if (src->fmt == Q4_INT8_ROW)
+    return hip_status(q4::launch_int8_rows_dequant(static_cast<const uint8_t*>(src->codes),
+                                                   static_cast<const float*>(src->scales), src->rows, src->cols, dst,
+                                                   dst_dtype, ld, as_stream(stream)));
   if (is_mx8(src->fmt))
     return hip_status(q4::launch_mx8_dequant(src->fmt, static_cast<const uint8_t*>(src->codes),
                                              static_cast<const uint8_t*>(src->scales), src->rows, src->cols, dst,
@@ -239,7 +255,8 @@ q4_status q4_gemm(int64_t M, const void* A_bf16, int64_t lda, const q4_tensor* A
                   const q4_tensor* W, void* C_bf16, int64_t ldc, void* stream) {
   q4_status st = check_tensor(W);
   if (st != Q4_OK) return st;
-  if (!is_weight(W->fmt)) return Q4_ERR_FORMAT;
+  const bool w8 = W->fmt == Q4_INT8_ROW;
+  if (!is_weight(W->fmt) && !(w8 && A_q)) return Q4_ERR_FORMAT;
   if (M < 0 || M >= kMaxDim || M > (int64_t)65535 * 64) return Q4_ERR_SHAPE;
   if ((A_bf16 == nullptr) == (A_q == nullptr)) return A_bf16 ? Q4_ERR_FORMAT : Q4_ERR_NULL;
   const int64_t N = W->rows, K = W->cols;
@@ -249,8 +266,10 @@ q4_status q4_gemm(int64_t M, const void* A_bf16, int64_t lda, const q4_tensor* A
     if (st != Q4_OK) return st;
     const bool w4a4 = A_q->fmt == W->fmt && (W->fmt == Q4_MXFP4 || W->fmt == Q4_NVFP4);
     const bool w4a8 = A_q->fmt == Q4_FP8_ROW && W->fmt == Q4_INT4_G128;
-    if (!w4a4 && !w4a8) return Q4_ERR_FORMAT;
+    const bool w8a8 = A_q->fmt == Q4_INT8_ROW && w8;
+    if (!w4a4 && !w4a8 && !w8a8) return Q4_ERR_FORMAT;
     if (A_q->rows != M || A_q->cols != K) return Q4_ERR_SHAPE;
+    if (w8a8 && K >= kMaxIntK) return Q4_ERR_SHAPE;
   }
   if (M == 0 || N == 0) return Q4_OK;
   if (K == 0) return Q4_ERR_SHAPE;
@@ -260,6 +279,11 @@ q4_status q4_gemm(int64_t M, const void* A_bf16, int64_t lda, const q4_tensor* A
   }
   st = check_out_bf16(C_bf16, M, N, ldc);
   if (st != Q4_OK) return st;
+  if (w8)
+    return hip_status(q4::launch_gemm_w8a8(
+        static_cast<const uint8_t*>(A_q->codes), static_cast<const float*>(A_q->scales), M,
+        static_cast<const uint8_t*>(W->codes), static_cast<const float*>(W->scales), N, K,
+        static_cast<uint16_t*>(C_bf16), ldc, as_stream(stream)));
   if (A_q && A_q->fmt == Q4_FP8_ROW)
     return hip_status(q4::launch_gemm_w4a8(
         A_q->layout, W->layout, static_cast<const uint8_t*>(A_q->codes), static_cast<const float*>(A_q->scales),

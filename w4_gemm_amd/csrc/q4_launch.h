@@ -124,6 +124,17 @@ hipError_t launch_gemm_w4a8(int a_layout, int w_layout, const uint8_t* a_codes, 
                             int64_t M, const uint8_t* w_codes, const uint16_t* w_scales, int64_t N,
                             int64_t K, uint16_t* C, int64_t ldc, hipStream_t stream);
 
+// Rows in 8-bit integers with one fp32 scale each (Q4_INT8_ROW, row-major,
+// cols % 16 == 0), and back.
+hipError_t launch_int8_rows_quantize(const uint16_t* src, int64_t ld, int64_t rows, int64_t cols, uint8_t* codes,
+                                     float* scales, hipStream_t stream);
+hipError_t launch_int8_rows_dequant(const uint8_t* codes, const float* scales, int64_t rows, int64_t cols, void* dst,
+                                    int dst_dtype, int64_t ld, hipStream_t stream);
+
+// W8A8 GEMM C [M][ldc] = A8' . W8'^T, both Q4_INT8_ROW, 0 < K < 2^17, K % 128 == 0.
+hipError_t launch_gemm_w8a8(const uint8_t* a, const float* sa, int64_t M, const uint8_t* w, const float* sw, int64_t N,
+                            int64_t K, uint16_t* C, int64_t ldc, hipStream_t stream);
+
 // MoE routing: top-k experts per token (ids, softmax gates) from fp32
 // logits [T][ld], then the expert-major dispatch (offsets [E+1], gather
 // [T*k], inv [T][k]) in one workgroup whose LDS holds per-expert token
