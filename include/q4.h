@@ -314,6 +314,51 @@ q4_status q4_gemm_quantized(int64_t M, const void* A_bf16, int64_t lda, const q4
                             void* stream);
 
 /*
+ * Root-mean-square norm in front of the products, with the residual's addition
+ * and the quantization of their activations in the same pass ("Quantization in
+ * deployment", Exercises, "The cost of block FP8": activation scales computed
+ * at the end of the previous kernel):
+ *     h = bf16(x + residual)           (without a residual h = x, not written)
+ *     y = h * weight / sqrt(mean_k(h^2) + eps)        (fp32, from h as stored)
+ * y_bf16 receives y rounded to bf16, y_q (Q4_FP8_ROW in either layout, or
+ * Q4_INT8_ROW) its 8-bit codes and row scales, from the fp32 values and not by
+ * way of bf16: scale = max(amax_row(|y|), 1e-12) / top (448, 127), code = the
+ * nearest to y / scale, ties to even, y and the quotient within a few fp32
+ * roundings.  One or both of y_bf16 and y_q are given.
+ *   x_bf16 [rows][ldx], residual_bf16 [rows][ldr] or NULL, weight [cols] bf16
+ *   (w_dtype 0) or fp32 (1), 16-byte aligned, eps finite and >= 0, h_bf16
+ *   [rows][ldh] with a residual (else NULL; Q4_ERR_FORMAT for one without the
+ *   other), y_bf16 [rows][ldy].  cols % 8 == 0 (y_q: % 16, tiled % 512),
+ *   cols <= 32768, rows < 2^22.  h may be x or the residual itself (same
+ *   pointer and leading dimension).  Other overlaps are not allowed.
+ * A row with an infinity or a NaN, or whose sum of squares reaches 2^128, gives
+ * NaN throughout (in 8 bits: the scale NaN, codes without meaning), and so does a
+ * row of zeros with eps = 0.  Other rows are not touched by it.
+ */
+q4_status q4_rmsnorm(const void* x_bf16, int64_t ldx, const void* residual_bf16, int64_t ldr, const void* weight,
+                     int w_dtype, float eps, int64_t rows, int64_t cols, void* h_bf16, int64_t ldh, void* y_bf16,
+                     int64_t ldy, const q4_tensor* y_q, void* stream);
+
+/*
+ * Its gradient, from h as the forward call wrote it (or x without a residual);
+ * an 8-bit output's is that of y (straight through).  With
+ * r = 1 / sqrt(mean_k(h^2) + eps), n = h * r, g = dy * weight:
+ *     dx         = bf16(dh + r * (g - n * mean_k(g * n)))
+ *     dweight[k] (+)= sum over rows of dy * n                          (fp32)
+ * dx is the gradient of x and of the residual alike; dh_bf16 [rows][lddh] is
+ * the one that reaches h on its own path (NULL: none).  dweight fp32 [cols],
+ * written whole, added to with accumulate != 0; NULL: not wanted.  dx may be dh
+ * or dy itself (same pointer and leading dimension).  Limits as above.  Results
+ * do not vary from run to run.  workspace: as for the gradient products below,
+ * of the size the query gives (not read without dweight).
+ */
+q4_status q4_rmsnorm_backward_workspace(int64_t rows, int64_t cols, size_t* bytes);
+q4_status q4_rmsnorm_backward(const void* dy_bf16, int64_t lddy, const void* h_bf16, int64_t ldh, const void* weight,
+                              int w_dtype, float eps, const void* dh_bf16, int64_t lddh, int64_t rows, int64_t cols,
+                              void* dx_bf16, int64_t lddx, float* dweight, int accumulate, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
  * Grouped per-expert GEMM for MoE ("Low-bit inference for very large MoE",
  * "A few details": one low-bit weight matrix per expert, rows grouped by
  * routing).  W holds E experts stacked expert-major: W->rows == E*N, expert

@@ -29,3 +29,27 @@ def int8_product(ac: np.ndarray, asc: np.ndarray, wc: np.ndarray, wsc: np.ndarra
     below 2^53, so exact)."""
     s = ac.astype(np.float64) @ wc.astype(np.float64).T
     return s * asc.astype(np.float64)[:, None] * wsc.astype(np.float64)[None, :]
+
+
+def rmsnorm(x: np.ndarray, weight: np.ndarray, eps: float) -> np.ndarray:
+    """x / sqrt(mean(x^2) + eps) * weight of each row (fp64)."""
+    out = np.zeros(x.shape)
+    for r in range(x.shape[0]):
+        v = x[r].astype(np.float64)
+        with np.errstate(all="ignore"):
+            out[r] = v / np.sqrt(np.sum(v * v) / v.size + eps) * weight.astype(np.float64)
+    return out
+
+
+def rmsnorm_backward(dy: np.ndarray, x: np.ndarray, weight: np.ndarray, eps: float):
+    """(dx, dweight) of sum(dy * rmsnorm(x, weight)) from the quotient rule,
+    element by element of the definition (fp64)."""
+    w = weight.astype(np.float64)
+    dx, dw = np.zeros(x.shape), np.zeros(w.shape)
+    for r in range(x.shape[0]):
+        v, d = x[r].astype(np.float64), dy[r].astype(np.float64)
+        root = np.sqrt(np.sum(v * v) / v.size + eps)
+        # y_j = w_j v_j / root, d root / d v_k = v_k / (n root)
+        dx[r] = d * w / root - np.sum(d * w * v) / root ** 2 * v / (v.size * root)
+        dw += d * v / root
+    return dx, dw

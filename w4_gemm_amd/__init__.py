@@ -114,6 +114,11 @@ def _lib_handle():
                               ctypes.c_int),
             "q4_grouped_gemm_wgrad": ([vp, i64, vp, i64, P, i64, vp, vp, i32, i64, i64, i64, vp, ctypes.c_int, i64,
                                        ctypes.c_int, vp, sz, vp], ctypes.c_int),
+            "q4_rmsnorm": ([vp, i64, vp, i64, vp, ctypes.c_int, ctypes.c_float, i64, i64, vp, i64, vp, i64, P, vp],
+                           ctypes.c_int),
+            "q4_rmsnorm_backward_workspace": ([i64, i64, SZ], ctypes.c_int),
+            "q4_rmsnorm_backward": ([vp, i64, vp, i64, vp, ctypes.c_int, ctypes.c_float, vp, i64, i64, i64, vp, i64,
+                                     vp, ctypes.c_int, vp, sz, vp], ctypes.c_int),
             "q4_read_probe": ([vp, i64, vp, vp], ctypes.c_int),
             "q4_mfma_probe": ([ctypes.c_int32, i64, ctypes.c_uint32, vp, ctypes.POINTER(ctypes.c_double), vp],
                               ctypes.c_int),
@@ -623,3 +628,7 @@ __all__ += [
     "q4_moe_permute_backward", "q4_moe_sort", "q4_moe_topk", "q4_moe_topk_backward", "q4_swiglu_backward",
     "q4_swiglu_save", "q4_wgrad_plan",
 ]
+
+from .block import q4_rmsnorm, q4_rmsnorm_backward  # noqa: E402
+
+__all__ += ["q4_rmsnorm", "q4_rmsnorm_backward"]

@@ -14,6 +14,7 @@ thread_local int g_last_hip_error = 0;
 constexpr int64_t kMaxDim = (int64_t)1 << 31;  // kernels index rows/cols in int
 constexpr int64_t kMaxGradLd = (int64_t)1 << 21;      // the gradient products address 256 rows in 2^30 bytes
 constexpr int64_t kMaxRows = ((int64_t)1 << 22) - 1;    // up to 1024 threads per row: below 2^32 threads
+constexpr int64_t kMaxNormCols = 32768;               // a row in the registers of 16 waves
 constexpr int64_t kMaxIntK = (int64_t)1 << 17;        // 2^14 K < 2^31: sums of products of two bytes stay exact
 constexpr int64_t kMaxTopkTokens = ((int64_t)1 << 26) - 4;  // a wave per token, four a workgroup: below 2^32 threads
 
@@ -95,6 +96,16 @@ q4_status check_tokens(int64_t T, int32_t k, int64_t cols) {
   if (T < 0 || cols < 0 || T >= ((int64_t)1 << 23) || cols >= kMaxDim || k < 1 || k > 32) return Q4_ERR_SHAPE;
   if (T * ((cols + 1023) / 1024) >= ((int64_t)1 << 25)) return Q4_ERR_SHAPE;
   return cols % 8 ? Q4_ERR_SHAPE : Q4_OK;
+}
+
+// The arguments q4_rmsnorm and its gradient share.
+q4_status check_norm(const void* weight, int w_dtype, float eps, int64_t rows, int64_t cols) {
+  if (w_dtype != 0 && w_dtype != 1) return Q4_ERR_FORMAT;
+  if (rows < 0 || cols < 0 || rows > kMaxRows || cols > kMaxNormCols || cols % 8) return Q4_ERR_SHAPE;
+  if (!(eps >= 0.0f && eps <= 3.402823466e+38f)) return Q4_ERR_SHAPE;
+  if (cols == 0) return Q4_OK;
+  if (!weight) return Q4_ERR_NULL;
+  return aligned(weight, 16) ? Q4_OK : Q4_ERR_ALIGN;
 }
 
 // The arguments q4_gemm_dgrad and q4_grouped_gemm_dgrad share.
@@ -349,6 +360,91 @@ q4_status q4_gemm_quantized(int64_t M, const void* A_bf16, int64_t lda, const q4
                                                      W->scales, W->global_scale, N, K,
                                                      static_cast<const uint16_t*>(A_bf16), lda, M, qo,
                                                      as_stream(stream)));
+}
+
+q4_status q4_rmsnorm(const void* x_bf16, int64_t ldx, const void* residual_bf16, int64_t ldr, const void* weight,
+                     int w_dtype, float eps, int64_t rows, int64_t cols, void* h_bf16, int64_t ldh, void* y_bf16,
+                     int64_t ldy, const q4_tensor* y_q, void* stream) {
+  q4_status st = check_norm(weight, w_dtype, eps, rows, cols);
+  if (st != Q4_OK) return st;
+  if (!y_bf16 && !y_q) return Q4_ERR_NULL;
+  if ((residual_bf16 == nullptr) != (h_bf16 == nullptr)) return Q4_ERR_FORMAT;
+  if (y_q) {
+    st = check_tensor(y_q);
+    if (st != Q4_OK) return st;
+    if (!is_row8(y_q->fmt)) return Q4_ERR_FORMAT;
+    if (y_q->rows != rows || y_q->cols != cols) return Q4_ERR_SHAPE;
+  }
+  if (rows == 0 || cols == 0) return Q4_OK;
+  st = check_bf16(x_bf16, rows, cols, ldx);
+  if (st == Q4_OK && residual_bf16) st = check_bf16(residual_bf16, rows, cols, ldr);
+  if (st == Q4_OK && h_bf16) st = check_bf16(h_bf16, rows, cols, ldh);
+  if (st == Q4_OK && y_bf16) st = check_bf16(y_bf16, rows, cols, ldy);
+  if (st != Q4_OK) return st;
+  q4::NormArgs a{};
+  a.x = static_cast<const uint16_t*>(x_bf16);
+  a.ldx = ldx;
+  a.residual = static_cast<const uint16_t*>(residual_bf16);
+  a.ldr = ldr;
+  a.w = weight;
+  a.w_f32 = w_dtype;
+  a.eps = eps;
+  a.rows = rows;
+  a.tiled = y_q && y_q->layout == Q4_LAYOUT_TILED;
+  a.srows = a.tiled ? (rows + 15) / 16 * 16 : rows;
+  a.cols = (int)cols;
+  a.h = static_cast<uint16_t*>(h_bf16);
+  a.ldh = ldh;
+  a.y = static_cast<uint16_t*>(y_bf16);
+  a.ldy = ldy;
+  if (y_q) {
+    a.codes = static_cast<uint8_t*>(y_q->codes);
+    a.scales = static_cast<float*>(y_q->scales);
+  }
+  return hip_status(q4::launch_rmsnorm(y_q ? y_q->fmt : -1, a, as_stream(stream)));
+}
+
+q4_status q4_rmsnorm_backward_workspace(int64_t rows, int64_t cols, size_t* bytes) {
+  if (!bytes) return Q4_ERR_NULL;
+  if (rows < 0 || cols < 0 || rows > kMaxRows || cols > kMaxNormCols || cols % 8) return Q4_ERR_SHAPE;
+  *bytes = rows && cols ? q4::rmsnorm_backward_workspace(rows, cols) : 0;
+  return Q4_OK;
+}
+
+q4_status q4_rmsnorm_backward(const void* dy_bf16, int64_t lddy, const void* h_bf16, int64_t ldh, const void* weight,
+                              int w_dtype, float eps, const void* dh_bf16, int64_t lddh, int64_t rows, int64_t cols,
+                              void* dx_bf16, int64_t lddx, float* dweight, int accumulate, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  q4_status st = check_norm(weight, w_dtype, eps, rows, cols);
+  if (st != Q4_OK) return st;
+  if (cols == 0 || (rows == 0 && (!dweight || accumulate))) return Q4_OK;
+  if (!aligned(dweight, 4)) return Q4_ERR_ALIGN;
+  st = check_bf16(dy_bf16, rows, cols, lddy);
+  if (st == Q4_OK) st = check_bf16(h_bf16, rows, cols, ldh);
+  if (st == Q4_OK && dh_bf16) st = check_bf16(dh_bf16, rows, cols, lddh);
+  if (st == Q4_OK) st = check_bf16(dx_bf16, rows, cols, lddx);
+  if (st != Q4_OK) return st;
+  if (dweight && rows > 0) {
+    if (!workspace) return Q4_ERR_NULL;
+    if (workspace_bytes < q4::rmsnorm_backward_workspace(rows, cols)) return Q4_ERR_SHAPE;
+    if (!aligned(workspace, 16)) return Q4_ERR_ALIGN;
+  }
+  q4::NormGradArgs a{};
+  a.dy = static_cast<const uint16_t*>(dy_bf16);
+  a.lddy = lddy;
+  a.h = static_cast<const uint16_t*>(h_bf16);
+  a.ldh = ldh;
+  a.dh = static_cast<const uint16_t*>(dh_bf16);
+  a.lddh = lddh;
+  a.w = weight;
+  a.w_f32 = w_dtype;
+  a.eps = eps;
+  a.rows = rows;
+  a.cols = (int)cols;
+  a.dx = static_cast<uint16_t*>(dx_bf16);
+  a.lddx = lddx;
+  a.partial = dweight ? static_cast<float*>(workspace) : nullptr;
+  return hip_status(q4::launch_rmsnorm_backward(a, dweight, accumulate, as_stream(stream)));
 }
 
 q4_status q4_grouped_gemm(const void* A_bf16, int64_t lda, int64_t T, const int32_t* gather,

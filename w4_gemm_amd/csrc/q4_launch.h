@@ -135,6 +135,44 @@ hipError_t launch_int8_rows_dequant(const uint8_t* codes, const float* scales, i
 hipError_t launch_gemm_w8a8(const uint8_t* a, const float* sa, int64_t M, const uint8_t* w, const float* sw, int64_t N,
                             int64_t K, uint16_t* C, int64_t ldc, hipStream_t stream);
 
+// RMS norm (rmsnorm.hip): 0 < cols <= 32768, rows > 0.  fmt 3 or 8: the 8-bit
+// output's format; -1: y alone.  srows: rows of storage (tiled codes).
+struct NormArgs {
+  const uint16_t* x;         // [rows][ldx]
+  int64_t ldx;
+  const uint16_t* residual;  // [rows][ldr], or NULL: no sum, h is not written
+  int64_t ldr;
+  const void* w;             // [cols], fp32 or bf16
+  int w_f32;
+  float eps;
+  int64_t rows, srows;
+  int cols;
+  uint16_t* h;               // [rows][ldh]
+  int64_t ldh;
+  uint16_t* y;               // [rows][ldy] or NULL
+  int64_t ldy;
+  uint8_t* codes;
+  float* scales;
+  int tiled;
+};
+hipError_t launch_rmsnorm(int fmt, const NormArgs& a, hipStream_t stream);
+
+// Its gradient; partial NULL: the weight's is not wanted.
+struct NormGradArgs {
+  const uint16_t *dy, *h, *dh;   // [rows][ld*]; dh NULL: nothing to add
+  int64_t lddy, ldh, lddh;
+  const void* w;
+  int w_f32;
+  float eps;
+  int64_t rows;
+  int cols;
+  uint16_t* dx;
+  int64_t lddx;
+  float* partial;                // workspace
+};
+size_t rmsnorm_backward_workspace(int64_t rows, int64_t cols);
+hipError_t launch_rmsnorm_backward(const NormGradArgs& a, float* dweight, int accumulate, hipStream_t stream);
+
 // MoE routing: top-k experts per token (ids, softmax gates) from fp32
 // logits [T][ld], then the expert-major dispatch (offsets [E+1], gather
 // [T*k], inv [T][k]) in one workgroup whose LDS holds per-expert token

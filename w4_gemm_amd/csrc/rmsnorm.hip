@@ -1,0 +1,351 @@
+// rmsnorm.hip -- root-mean-square norm with the residual's addition in front
+// and the quantization of the 8-bit products behind it, and its gradient.
+//
+//   h = bf16(x + residual)                (the residual stream; h = x without)
+//   y = (h * w) * r,   r = 1 / sqrt(mean(h^2) + eps)
+//
+// in fp32 from h as it is stored, so that the gradient, which has h alone, is
+// that of what the forward pass computed.  y goes out in bf16, or in 8 bits with
+// one scale per row (Q4_FP8_ROW, Q4_INT8_ROW) straight from the fp32 values, or
+// both.  r is one factor of the whole row and fp32 multiplication is monotone,
+// so the row's largest |y| is r times the largest |h w|: one reduction gives the
+// sum of squares and the scale together, and a code is that of
+// (h w) * (r * top / a), a the largest |y|.
+//
+// A row is held in registers by 1, 4 or 16 waves (lane i of them has the chunks
+// of eight values i, i + 64 WAVES, ...) and read once.
+#include "q4_launch.h"
+#include "q4_layout.h"
+#include "q4_mma.h"
+#include "q4_row8.h"
+
+namespace q4 {
+namespace {
+
+// Eight weights: fp32, or bf16 widened.
+template <bool WF32>
+__device__ __forceinline__ void load_weight8(const void* w, int k0, float (&o)[8]) {
+  if constexpr (WF32) {
+    const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(w) + k0);
+    const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(w) + k0 + 4);
+    o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
+    o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+  } else {
+    unpack_bf16x8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + k0), o);
+  }
+}
+
+__device__ __forceinline__ uint4 pack_bf16x8(const float (&v)[8]) {
+  return make_uint4(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]), pk_bf16(v[6], v[7]));
+}
+
+// 1 / sqrt(mean + eps); NaN where the sum of squares is no number below 2^128,
+// so that a row whose squares overflow is not taken for zeros.
+__device__ __forceinline__ float row_rstd(float ss, int cols, float eps) {
+  return ss <= 3.402823466e+38f ? 1.0f / __builtin_sqrtf(ss / (float)cols + eps) : u2f(0x7FC00000u);
+}
+
+// KIND: kRowInt8, kRowE4m3, or -1 for no output in 8 bits.
+template <int WAVES, int CH, int KIND, bool WF32>
+__global__ void __launch_bounds__(64 * (WAVES < 4 ? 4 : WAVES))
+rmsnorm_kernel(const NormArgs p) {
+  constexpr int kRows = WAVES < 4 ? 4 / WAVES : 1;
+  const int tid = threadIdx.x % (64 * WAVES), in = threadIdx.x / (64 * WAVES);
+  const int64_t r = (int64_t)blockIdx.x * kRows + in;
+  const int cols = p.cols;
+  if (r >= p.rows) {  // (a wave of its own, or the whole workgroup: nobody waits for it)
+    if (KIND == kRowE4m3 && p.tiled && r < p.srows)   // padding row of the last tile: zero codes
+      for (int k0 = tid * 8; k0 < cols; k0 += 512 * WAVES) {
+        *reinterpret_cast<uint32_t*>(p.codes + fp8_tiled_dword(r, k0, cols, 0)) = 0u;
+        *reinterpret_cast<uint32_t*>(p.codes + fp8_tiled_dword(r, k0, cols, 1)) = 0u;
+      }
+    return;
+  }
+  const uint16_t* x = p.x + r * p.ldx;
+  uint4 v[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int k0 = (tid + 64 * WAVES * i) * 8;
+    v[i] = *reinterpret_cast<const uint4*>(x + (k0 < cols ? k0 : 0));
+  }
+  if (p.residual) {
+    const uint16_t* res = p.residual + r * p.ldr;
+    uint4 u[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int k0 = (tid + 64 * WAVES * i) * 8;
+      u[i] = *reinterpret_cast<const uint4*>(res + (k0 < cols ? k0 : 0));
+    }
+    uint16_t* h = p.h + r * p.ldh;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int k0 = (tid + 64 * WAVES * i) * 8;
+      float a[8], b[8];
+      unpack_bf16x8(v[i], a);
+      unpack_bf16x8(u[i], b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a[j] += b[j];
+      v[i] = pack_bf16x8(a);
+      if (k0 < cols) *reinterpret_cast<uint4*>(h + k0) = v[i];
+    }
+  }
+  float hw[CH][8];
+  float ss = 0.0f;
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int k0 = (tid + 64 * WAVES * i) * 8;
+    if (k0 < cols) {
+      float a[8], w[8];
+      unpack_bf16x8(v[i], a);
+      load_weight8<WF32>(p.w, k0, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        ss = __builtin_fmaf(a[j], a[j], ss);
+        hw[i][j] = a[j] * w[j];
+      }
+      if (KIND >= 0) most = max_bits8(hw[i], most);
+    }
+  }
+  ss = wave_sum(ss);
+  if (KIND >= 0) most = wave_max(most);
+  if constexpr (WAVES > 1) {
+    __shared__ float sum[WAVES];
+    __shared__ uint32_t top[WAVES];
+    if ((tid & 63) == 0) {
+      sum[tid >> 6] = ss;
+      top[tid >> 6] = most;
+    }
+    __syncthreads();
+    ss = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      ss += sum[w];
+      most = top[w] > most ? top[w] : most;
+    }
+  }
+  const float rstd = row_rstd(ss, cols, p.eps);
+  float f = 0.0f;
+  if constexpr (KIND >= 0) {
+    const float a = u2f(most) * rstd;              // the largest |y|
+    const bool fine = a <= 3.402823466e+38f;
+    const float least = fmaxf(a, 1e-12f);
+    f = fine ? rstd * kRowTop<KIND> / least : 0.0f;
+    if (tid == 0) p.scales[r] = fine ? least / kRowTop<KIND> : u2f(0x7FC00000u);
+  }
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int k0 = (tid + 64 * WAVES * i) * 8;
+    if (k0 >= cols) continue;
+    if constexpr (KIND == kRowInt8) {
+      *reinterpret_cast<uint2*>(p.codes + r * cols + k0) = int8_pack8(hw[i], f);
+    } else if constexpr (KIND == kRowE4m3) {
+      const uint2 q = e4m3_pack8(hw[i], f);
+      if (p.tiled) {   // even elements in one word, odd ones in the next
+        *reinterpret_cast<uint32_t*>(p.codes + fp8_tiled_dword(r, k0, cols, 0)) = __builtin_amdgcn_perm(q.y, q.x, 0x06040200u);
+        *reinterpret_cast<uint32_t*>(p.codes + fp8_tiled_dword(r, k0, cols, 1)) = __builtin_amdgcn_perm(q.y, q.x, 0x07050301u);
+      } else {
+        *reinterpret_cast<uint2*>(p.codes + r * cols + k0) = q;
+      }
+    }
+    if (KIND < 0 || p.y) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) hw[i][j] *= rstd;
+      *reinterpret_cast<uint4*>(p.y + r * p.ldy + k0) = pack_bf16x8(hw[i]);
+    }
+  }
+}
+
+// ---- gradient ----------------------------------------------------------------
+// With n = h r and g = dy w:
+//   dx = dh + r (g - n mean(g n)),   dw = sum over rows of dy n
+// mean(g n) = r sum(g h) / cols, so one reduction gives sum(h^2) and sum(g h)
+// together and nothing but h need be kept from the forward pass.  Workgroups
+// walk over rows with dw of their columns in registers; each writes its sum to
+// the workspace, and a second kernel adds those in order.
+template <int WAVES, int CH, bool WF32>
+__global__ void __launch_bounds__(64 * (WAVES < 4 ? 4 : WAVES))
+rmsnorm_backward_kernel(const NormGradArgs p) {
+  constexpr int kRows = WAVES < 4 ? 4 / WAVES : 1;
+  constexpr int kThreads = 64 * WAVES;
+  const int tid = threadIdx.x % kThreads, in = threadIdx.x / kThreads;
+  const int cols = p.cols;
+  float w[CH][8], dw[CH][8];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int k0 = (tid + kThreads * i) * 8;
+    if (k0 < cols) load_weight8<WF32>(p.w, k0, w[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+  }
+  __shared__ float part[2][2][WAVES];
+  int turn = 0;
+  for (int64_t r = (int64_t)blockIdx.x * kRows + in; r < p.rows; r += (int64_t)gridDim.x * kRows, turn ^= 1) {
+    uint4 vd[CH], vh[CH], vr[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int k0 = (tid + kThreads * i) * 8, at = k0 < cols ? k0 : 0;
+      vd[i] = *reinterpret_cast<const uint4*>(p.dy + r * p.lddy + at);
+      vh[i] = *reinterpret_cast<const uint4*>(p.h + r * p.ldh + at);
+      if (p.dh) vr[i] = *reinterpret_cast<const uint4*>(p.dh + r * p.lddh + at);
+    }
+    float ss = 0.0f, c = 0.0f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      if ((tid + kThreads * i) * 8 < cols) {
+        float d[8], h[8];
+        unpack_bf16x8(vd[i], d);
+        unpack_bf16x8(vh[i], h);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          ss = __builtin_fmaf(h[j], h[j], ss);
+          c = __builtin_fmaf(d[j] * w[i][j], h[j], c);
+        }
+      }
+    }
+    ss = wave_sum(ss);
+    c = wave_sum(c);
+    if constexpr (WAVES > 1) {
+      // two sets in turn: a wave writes the next row's while others read this one's
+      if ((tid & 63) == 0) {
+        part[turn][0][tid >> 6] = ss;
+        part[turn][1][tid >> 6] = c;
+      }
+      __syncthreads();
+      ss = c = 0.0f;
+#pragma unroll
+      for (int v = 0; v < WAVES; ++v) {
+        ss += part[turn][0][v];
+        c += part[turn][1][v];
+      }
+    }
+    const float rstd = row_rstd(ss, cols, p.eps);
+    const float t = c / (float)cols * rstd * rstd;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int k0 = (tid + kThreads * i) * 8;
+      if (k0 < cols) {
+        float d[8], h[8], o[8];
+        unpack_bf16x8(vd[i], d);
+        unpack_bf16x8(vh[i], h);
+        if (p.dh) unpack_bf16x8(vr[i], o);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float e = rstd * __builtin_fmaf(-t, h[j], d[j] * w[i][j]);
+          o[j] = p.dh ? o[j] + e : e;
+          dw[i][j] = __builtin_fmaf(d[j], h[j] * rstd, dw[i][j]);
+        }
+        *reinterpret_cast<uint4*>(p.dx + r * p.lddx + k0) = pack_bf16x8(o);
+      }
+    }
+  }
+  if (!p.partial) return;
+  if constexpr (kRows > 1) {   // the rows side by side in a workgroup, added in order
+    __shared__ float side[kRows][CH * 512 * WAVES];
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) side[in][(tid + kThreads * i) * 8 + j] = dw[i][j];
+    __syncthreads();
+    for (int k = threadIdx.x; k < cols; k += kThreads * kRows) {
+      float s = 0.0f;
+#pragma unroll
+      for (int q = 0; q < kRows; ++q) s += side[q][k];
+      p.partial[(int64_t)blockIdx.x * cols + k] = s;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int k0 = (tid + kThreads * i) * 8;
+      if (k0 < cols) {
+        float4* o = reinterpret_cast<float4*>(p.partial + (int64_t)blockIdx.x * cols + k0);
+        o[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+        o[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+      }
+    }
+  }
+}
+
+// dw[k] (+)= sum over the workgroups' sums: 64 columns by 16 slices per
+// workgroup, the slices' sums added in order.
+__global__ void __launch_bounds__(1024)
+rmsnorm_weight_sum_kernel(const float* __restrict__ partial, int blocks, int cols, float* __restrict__ dw,
+                          int accumulate) {
+  __shared__ float part[16][64];
+  const int k = blockIdx.x * 64 + (threadIdx.x & 63), slice = threadIdx.x >> 6;
+  float s = 0.0f;
+  if (k < cols)
+    for (int b = slice; b < blocks; b += 16) s += partial[(int64_t)b * cols + k];
+  part[slice][threadIdx.x & 63] = s;
+  __syncthreads();
+  if (slice == 0 && k < cols) {
+#pragma unroll
+    for (int q = 1; q < 16; ++q) s += part[q][threadIdx.x];
+    dw[k] = accumulate ? dw[k] + s : s;
+  }
+}
+
+constexpr int kGradBlocks = 512;
+
+template <int WAVES, int CH>
+void norm(const NormArgs& a, int kind, hipStream_t stream) {
+  constexpr int kRows = WAVES < 4 ? 4 / WAVES : 1;
+  const unsigned grid = (unsigned)((a.srows + kRows - 1) / kRows), threads = 64 * WAVES * kRows;
+  auto kernel = kind == kRowInt8   ? (a.w_f32 ? rmsnorm_kernel<WAVES, CH, kRowInt8, true> : rmsnorm_kernel<WAVES, CH, kRowInt8, false>)
+                : kind == kRowE4m3 ? (a.w_f32 ? rmsnorm_kernel<WAVES, CH, kRowE4m3, true> : rmsnorm_kernel<WAVES, CH, kRowE4m3, false>)
+                                   : (a.w_f32 ? rmsnorm_kernel<WAVES, CH, -1, true> : rmsnorm_kernel<WAVES, CH, -1, false>);
+  kernel<<<grid, threads, 0, stream>>>(a);
+}
+
+int64_t grad_blocks(int64_t rows, int64_t cols) {
+  const int64_t per = cols <= 2048 ? 4 : 1;
+  const int64_t b = (rows + per - 1) / per;
+  return b < kGradBlocks ? b : kGradBlocks;
+}
+
+template <int WAVES, int CH>
+void norm_backward(const NormGradArgs& a, hipStream_t stream) {
+  constexpr int kRows = WAVES < 4 ? 4 / WAVES : 1;
+  auto kernel = a.w_f32 ? rmsnorm_backward_kernel<WAVES, CH, true> : rmsnorm_backward_kernel<WAVES, CH, false>;
+  kernel<<<(unsigned)grad_blocks(a.rows, a.cols), 64 * WAVES * kRows, 0, stream>>>(a);
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(int fmt, const NormArgs& a, hipStream_t stream) {
+  const int kind = fmt == 8 ? kRowInt8 : fmt == 3 ? kRowE4m3 : -1;
+  if (a.cols <= 512)
+    norm<1, 1>(a, kind, stream);
+  else if (a.cols <= 2048)
+    norm<1, 4>(a, kind, stream);
+  else if (a.cols <= 8192)
+    norm<4, 4>(a, kind, stream);
+  else
+    norm<16, 4>(a, kind, stream);
+  return hipGetLastError();
+}
+
+size_t rmsnorm_backward_workspace(int64_t rows, int64_t cols) {
+  return (size_t)grad_blocks(rows, cols) * (size_t)cols * 4;
+}
+
+hipError_t launch_rmsnorm_backward(const NormGradArgs& a, float* dweight, int accumulate, hipStream_t stream) {
+  if (a.rows > 0) {
+    if (a.cols <= 512)
+      norm_backward<1, 1>(a, stream);
+    else if (a.cols <= 2048)
+      norm_backward<1, 4>(a, stream);
+    else if (a.cols <= 8192)
+      norm_backward<4, 4>(a, stream);
+    else
+      norm_backward<16, 4>(a, stream);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (dweight)
+    rmsnorm_weight_sum_kernel<<<(unsigned)((a.cols + 63) / 64), 1024, 0, stream>>>(
+        a.partial, a.rows > 0 ? (int)grad_blocks(a.rows, a.cols) : 0, a.cols, dweight, accumulate);
+  return hipGetLastError();
+}
+
+}  // namespace q4
