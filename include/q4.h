@@ -488,6 +488,35 @@ q4_status q4_moe_topk_backward(const float* logits, int64_t ld, int64_t T, int32
                                int64_t lddl, void* stream);
 
 /*
+ * Balance of a router: the loss that grows where experts that receive many
+ * choices also have large probabilities, and the choices per expert.  Over the n
+ * tokens that count (mask[t] != 0, all with mask NULL), c[e] of whose choices are
+ * e and whose softmax probabilities of e add up to P[e]:
+ *     counts[e] = c[e]                                             (int32)
+ *     slopes[e] = coef * E * c[e] / (k * n^2)                      (fp32)
+ *     loss      = sum_e slopes[e] * P[e]                           (fp32 [1])
+ * so loss = coef for choices and probabilities spread evenly, and 0 (slopes too)
+ * with n = 0.  Choices with ids outside 0 .. E-1 are in no c[e].  Sums over
+ * tokens in 64 bits, in an order that the sizes alone decide.
+ * Backward (the counts have no gradient), with p the softmax of token t:
+ *     dlogits[t][e] (+)= dloss * p[e] * (slopes[e] - sum_e' p[e'] slopes[e'])
+ * 0 for tokens that do not count; dloss fp32 [1] on the device, NULL: 1;
+ * accumulate != 0 adds, e.g. to what q4_moe_topk_backward wrote.
+ * A token whose logits are all -inf has no probabilities: it adds nothing to P
+ * and its gradient is 0; one with a NaN or +inf makes the loss NaN and its own
+ * gradient alone NaN.
+ * logits [T][ld], dlogits [T][lddl] fp32, ids [T][k] int32, mask uint8 [T].
+ * 1 <= E <= 1024, 1 <= k <= 32, T <= 2^26 - 4.
+ */
+q4_status q4_moe_balance_workspace(int64_t T, int32_t E, size_t* bytes);
+q4_status q4_moe_balance(const float* logits, int64_t ld, int64_t T, int32_t E, int32_t k, const int32_t* topk_ids,
+                         const uint8_t* mask, float coef, float* loss, int32_t* counts, float* slopes,
+                         void* workspace, size_t workspace_bytes, void* stream);
+q4_status q4_moe_balance_backward(const float* logits, int64_t ld, int64_t T, int32_t E, const uint8_t* mask,
+                                  const float* slopes, const float* dloss, float* dlogits, int64_t lddl,
+                                  int accumulate, void* stream);
+
+/*
  * Tokens sorted by expert, for choices from any router and any number of
  * tokens: a stable sort of topk_ids [T][k] (read as T*k choices in order) by
  * expert.  Writes expert_offsets [E+1], gather (the token of each row) and inv
@@ -593,6 +622,36 @@ q4_status q4_grouped_gemm_wgrad(const void* dC_bf16, int64_t lddc, const void* A
                                 const int32_t* expert_offsets, int32_t E, int64_t P, int64_t N,
                                 int64_t K, void* dW, int dw_dtype, int64_t lddw, int accumulate,
                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The norm over all gradients of a step, and the gradients scaled down to a
+ * largest norm:
+ *     norm = sqrt(sum over all tensors of g^2)
+ *     out  = g * min(1, max_norm / (norm + 1e-6))
+ * grads, counts and dtypes are host arrays of n entries, read during the call:
+ * device pointers to counts[i] contiguous values, bf16 (dtypes[i] 0) or fp32 (1),
+ * aligned to their own size; empty tensors are allowed (and may be NULL), n <=
+ * 2^20.  norm: device fp32 [1].  The squares are added in 64 bits, in an order
+ * that sizes and alignment alone decide; a norm past fp32's range is inf in norm
+ * and as it is for the factor.  A NaN or an infinity among the gradients makes
+ * norm NaN or inf, as arithmetic has it: every output is then NaN, or 0 where g
+ * is finite and the norm inf.
+ * q4_grad_clip takes the norm from norm_in (e.g. one combined over ranks), or
+ * with norm_in NULL makes it in the same call and writes it to norm_out (which
+ * may be NULL; not written with norm_in).  out: host array of n pointers of the
+ * same counts and types, or NULL: in place (nothing is written where the factor
+ * is 1).  An out[i] may be grads[i] itself; otherwise outputs must overlap
+ * neither each other nor any gradient (Q4_ERR_ALIGN: also a tensor that is
+ * listed twice).  max_norm >= 0, inf for no limit.
+ * workspace: 16-byte aligned, of the size the query gives (not read with
+ * norm_in); the contents need not be kept.
+ */
+q4_status q4_grad_workspace(int64_t n, size_t* bytes);
+q4_status q4_grad_norm(int64_t n, const void* const* grads, const int64_t* counts, const int32_t* dtypes,
+                       float* norm, void* workspace, size_t workspace_bytes, void* stream);
+q4_status q4_grad_clip(int64_t n, const void* const* grads, const int64_t* counts, const int32_t* dtypes,
+                       void* const* out, const float* norm_in, float max_norm, float* norm_out, void* workspace,
+                       size_t workspace_bytes, void* stream);
 
 /*
  * Which kernel the products take for these sizes (host arithmetic only; the

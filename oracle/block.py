@@ -53,3 +53,51 @@ def rmsnorm_backward(dy: np.ndarray, x: np.ndarray, weight: np.ndarray, eps: flo
         dx[r] = d * w / root - np.sum(d * w * v) / root ** 2 * v / (v.size * root)
         dw += d * v / root
     return dx, dw
+
+
+def softmax(row: np.ndarray) -> np.ndarray:
+    """Softmax of one token's logits (fp64); zeros where all are -inf."""
+    v = row.astype(np.float64)
+    if np.all(v == -np.inf):
+        return np.zeros(v.size)
+    with np.errstate(invalid="ignore"):
+        e = np.exp(v - np.max(v))
+        return e / np.sum(e)
+
+
+def moe_balance(logits: np.ndarray, ids: np.ndarray, coef: float, mask=None):
+    """(loss, counts, slopes) over the tokens that count."""
+    T, E = logits.shape
+    k = ids.shape[1]
+    here = [t for t in range(T) if mask is None or mask[t]]
+    counts, total = np.zeros(E, np.int64), np.zeros(E)
+    for t in here:
+        for e in ids[t]:
+            if 0 <= e < E:
+                counts[e] += 1
+        total += softmax(logits[t])
+    n = len(here)
+    slopes = coef * E * counts / (k * float(n) * n) if n else np.zeros(E)
+    return float(np.sum(slopes * total)), counts, slopes
+
+
+def moe_balance_backward(logits: np.ndarray, slopes: np.ndarray, mask=None, dloss: float = 1.0) -> np.ndarray:
+    """Gradient of the loss for the logits, by the softmax's matrix of
+    derivatives dp_e / dl_j = p_e ([e = j] - p_j)."""
+    out = np.zeros(logits.shape)
+    for t in range(logits.shape[0]):
+        if mask is None or mask[t]:
+            p = softmax(logits[t])
+            out[t] = dloss * ((np.diag(p) - np.outer(p, p)) @ slopes)
+    return out
+
+
+def grad_norm(grads) -> float:
+    return float(np.sqrt(sum(np.sum(g.astype(np.float64) ** 2) for g in grads)))
+
+
+def grad_clip(grads, max_norm: float, norm: float):
+    with np.errstate(invalid="ignore"):
+        by = max_norm / (norm + 1e-6)
+        by = 1.0 if by > 1 else by
+        return [g.astype(np.float64) * by for g in grads]

@@ -47,3 +47,41 @@ def test_int8_product_by_hand():
     out = ob.int8_product(np.array([[1, -2]], np.int8), np.array([0.5], np.float32), np.array([[3, 4], [-128, 1]], np.int8),
                           np.array([2.0, 1.0], np.float32))
     assert out.tolist() == [[-5.0, -65.0]]
+
+
+def test_balance_by_hand():
+    logits = np.zeros((4, 2))
+    loss, counts, slopes = ob.moe_balance(logits, np.array([[0], [1], [0], [1]]), 0.5)
+    assert loss == 0.5 and counts.tolist() == [2, 2]               # spread evenly: coef
+    loss, counts, _ = ob.moe_balance(logits, np.array([[0], [0], [0], [5]]), 1.0, mask=[1, 1, 0, 1])
+    assert counts.tolist() == [2, 0] and np.isclose(loss, 2 * (2 / 3) * 0.5)
+    assert ob.moe_balance(logits, np.zeros((4, 1), int), 1.0, mask=[0] * 4)[0] == 0.0
+
+
+def test_balance_gradient_against_differences():
+    rng = np.random.default_rng(3)
+    logits = rng.standard_normal((5, 6))
+    logits[1, 2] = -np.inf
+    ids = np.stack([rng.permutation(6)[:2] for _ in range(5)])
+    mask = [1, 1, 0, 1, 1]
+    _, _, slopes = ob.moe_balance(logits, ids, 1.5, mask)
+    g = ob.moe_balance_backward(logits, slopes, mask, 2.0)
+    for i in np.ndindex(logits.shape):
+        if np.isinf(logits[i]):
+            assert g[i] == 0
+            continue
+        keep, step = logits[i], 1e-6
+        logits[i] = keep + step
+        up = ob.moe_balance(logits, ids, 1.5, mask)[0]
+        logits[i] = keep - step
+        down = ob.moe_balance(logits, ids, 1.5, mask)[0]
+        logits[i] = keep
+        assert abs(2.0 * (up - down) / (2 * step) - g[i]) < 1e-8
+
+
+def test_clip_by_hand():
+    g = [np.array([3.0]), np.array([4.0, 0.0])]
+    assert ob.grad_norm(g) == 5.0
+    out = ob.grad_clip(g, 2.5, 5.0)
+    assert np.allclose(out[0], 1.5, rtol=1e-6) and np.allclose(out[1], [2.0, 0.0], rtol=1e-6)
+    assert ob.grad_clip(g, 10.0, 5.0)[0] == 3.0

@@ -119,6 +119,12 @@ def _lib_handle():
             "q4_rmsnorm_backward_workspace": ([i64, i64, SZ], ctypes.c_int),
             "q4_rmsnorm_backward": ([vp, i64, vp, i64, vp, ctypes.c_int, ctypes.c_float, vp, i64, i64, i64, vp, i64,
                                      vp, ctypes.c_int, vp, sz, vp], ctypes.c_int),
+            "q4_moe_balance_workspace": ([i64, i32, SZ], ctypes.c_int),
+            "q4_moe_balance": ([vp, i64, i64, i32, i32, vp, vp, ctypes.c_float, vp, vp, vp, vp, sz, vp], ctypes.c_int),
+            "q4_moe_balance_backward": ([vp, i64, i64, i32, vp, vp, vp, vp, i64, ctypes.c_int, vp], ctypes.c_int),
+            "q4_grad_workspace": ([i64, SZ], ctypes.c_int),
+            "q4_grad_norm": ([i64, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int),
+            "q4_grad_clip": ([i64, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, sz, vp], ctypes.c_int),
             "q4_read_probe": ([vp, i64, vp, vp], ctypes.c_int),
             "q4_mfma_probe": ([ctypes.c_int32, i64, ctypes.c_uint32, vp, ctypes.POINTER(ctypes.c_double), vp],
                               ctypes.c_int),
@@ -629,6 +635,8 @@ __all__ += [
     "q4_swiglu_save", "q4_wgrad_plan",
 ]
 
-from .block import q4_rmsnorm, q4_rmsnorm_backward  # noqa: E402
+from .block import (  # noqa: E402
+    q4_grad_clip, q4_grad_norm, q4_moe_balance, q4_moe_balance_backward, q4_rmsnorm, q4_rmsnorm_backward)
 
-__all__ += ["q4_rmsnorm", "q4_rmsnorm_backward"]
+__all__ += ["q4_grad_clip", "q4_grad_norm", "q4_moe_balance", "q4_moe_balance_backward", "q4_rmsnorm",
+            "q4_rmsnorm_backward"]

@@ -5,6 +5,10 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+#include <memory>
+#include <new>
+
 #include "q4_launch.h"
 
 namespace {
@@ -14,6 +18,8 @@ thread_local int g_last_hip_error = 0;
 constexpr int64_t kMaxDim = (int64_t)1 << 31;  // kernels index rows/cols in int
 constexpr int64_t kMaxGradLd = (int64_t)1 << 21;      // the gradient products address 256 rows in 2^30 bytes
 constexpr int64_t kMaxRows = ((int64_t)1 << 22) - 1;    // up to 1024 threads per row: below 2^32 threads
+constexpr int64_t kMaxGrads = (int64_t)1 << 20;
+constexpr int64_t kMaxGradCount = (int64_t)1 << 44;   // sizes in bytes stay far below 2^63
 constexpr int64_t kMaxNormCols = 32768;               // a row in the registers of 16 waves
 constexpr int64_t kMaxIntK = (int64_t)1 << 17;        // 2^14 K < 2^31: sums of products of two bytes stay exact
 constexpr int64_t kMaxTopkTokens = ((int64_t)1 << 26) - 4;  // a wave per token, four a workgroup: below 2^32 threads
@@ -106,6 +112,62 @@ q4_status check_norm(const void* weight, int w_dtype, float eps, int64_t rows, i
   if (cols == 0) return Q4_OK;
   if (!weight) return Q4_ERR_NULL;
   return aligned(weight, 16) ? Q4_OK : Q4_ERR_ALIGN;
+}
+
+// The tensors of q4_grad_norm and q4_grad_clip (out NULL: none, or in place).
+q4_status check_grads(const q4::GradList& g, void* const* out) {
+  if (g.n < 0 || g.n > kMaxGrads) return Q4_ERR_SHAPE;
+  if (g.n > 0 && (!g.data || !g.count || !g.dtype)) return Q4_ERR_NULL;
+  for (int64_t i = 0; i < g.n; ++i) {
+    if (g.dtype[i] != 0 && g.dtype[i] != 1) return Q4_ERR_FORMAT;
+    if (g.count[i] < 0 || g.count[i] > kMaxGradCount) return Q4_ERR_SHAPE;
+    if (!g.count[i]) continue;
+    if (!g.data[i] || (out && !out[i])) return Q4_ERR_NULL;
+    const uintptr_t size = g.dtype[i] ? 4 : 2;
+    if (!aligned(g.data[i], size) || (out && !aligned(out[i], size))) return Q4_ERR_ALIGN;
+  }
+  return q4::grad_fits(g) ? Q4_OK : Q4_ERR_SHAPE;
+}
+
+q4_status check_grad_workspace(int64_t n, const void* workspace, size_t bytes) {
+  const size_t need = q4::grad_workspace(n);
+  if (need && !workspace) return Q4_ERR_NULL;
+  if (bytes < need) return Q4_ERR_SHAPE;
+  return need && !aligned(workspace, 16) ? Q4_ERR_ALIGN : Q4_OK;
+}
+
+// What is written overlaps nothing else: outputs (the gradients themselves in
+// place) neither each other nor a gradient that is not their own.
+q4_status check_apart(const q4::GradList& g, void* const* out) {
+  struct Span {
+    uintptr_t from, to;
+    bool written;
+  };
+  const std::unique_ptr<Span[]> spans(new (std::nothrow) Span[2 * (size_t)g.n + 1]);
+  if (!spans) return Q4_ERR_SHAPE;
+  size_t m = 0;
+  bool sorted = true;
+  auto add = [&](const void* p, uintptr_t bytes, bool written) {
+    const uintptr_t from = reinterpret_cast<uintptr_t>(p);
+    sorted = sorted && (m == 0 || spans[m - 1].from <= from);
+    spans[m++] = Span{from, from + bytes, written};
+  };
+  for (int64_t i = 0; i < g.n; ++i) {
+    if (!g.count[i]) continue;
+    const uintptr_t bytes = (uintptr_t)g.count[i] * (g.dtype[i] ? 4 : 2);
+    const bool own = !out || out[i] == g.data[i];
+    add(g.data[i], bytes, own);
+    if (!own) add(out[i], bytes, true);
+  }
+  if (!sorted) std::sort(spans.get(), spans.get() + m, [](const Span& a, const Span& b) { return a.from < b.from; });
+  uintptr_t read_to = 0, write_to = 0;   // ends of what lies before, read only and written
+  for (size_t i = 0; i < m; ++i) {
+    const Span& s = spans[i];
+    if (s.from < write_to || (s.written && s.from < read_to)) return Q4_ERR_ALIGN;
+    uintptr_t& to = s.written ? write_to : read_to;
+    if (s.to > to) to = s.to;
+  }
+  return Q4_OK;
 }
 
 // The arguments q4_gemm_dgrad and q4_grouped_gemm_dgrad share.
@@ -594,6 +656,100 @@ q4_status q4_moe_topk_backward(const float* logits, int64_t ld, int64_t T, int32
     return Q4_ERR_ALIGN;
   return hip_status(q4::launch_moe_topk_backward(logits, ld, T, E, k, topk_ids, dweights, dlogits, lddl,
                                                  as_stream(stream)));
+}
+
+q4_status q4_moe_balance_workspace(int64_t T, int32_t E, size_t* bytes) {
+  if (!bytes) return Q4_ERR_NULL;
+  if (T < 0 || T > kMaxTopkTokens || E < 1 || E > 1024) return Q4_ERR_SHAPE;
+  *bytes = T ? q4::moe_balance_workspace(T, E) : 0;
+  return Q4_OK;
+}
+
+q4_status q4_moe_balance(const float* logits, int64_t ld, int64_t T, int32_t E, int32_t k, const int32_t* topk_ids,
+                         const uint8_t* mask, float coef, float* loss, int32_t* counts, float* slopes,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  size_t need = 0;
+  const q4_status st = q4_moe_balance_workspace(T, E, &need);
+  if (st != Q4_OK) return st;
+  if (k < 1 || k > 32 || T * k >= kMaxDim) return Q4_ERR_SHAPE;
+  if (!loss || !counts || !slopes || (T > 0 && (!logits || !topk_ids)) || (need && !workspace)) return Q4_ERR_NULL;
+  if (T > 0 && ld < E) return Q4_ERR_SHAPE;
+  if (workspace_bytes < need) return Q4_ERR_SHAPE;
+  if (!aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(loss, 4) || !aligned(counts, 4) ||
+      !aligned(slopes, 4) || (need && !aligned(workspace, 16)))
+    return Q4_ERR_ALIGN;
+  q4::BalanceArgs a{};
+  a.logits = logits;
+  a.ld = ld;
+  a.T = T;
+  a.E = E;
+  a.k = k;
+  a.ids = topk_ids;
+  a.mask = mask;
+  a.coef = coef;
+  a.loss = loss;
+  a.counts = counts;
+  a.slopes = slopes;
+  return hip_status(q4::launch_moe_balance(a, workspace, as_stream(stream)));
+}
+
+q4_status q4_moe_balance_backward(const float* logits, int64_t ld, int64_t T, int32_t E, const uint8_t* mask,
+                                  const float* slopes, const float* dloss, float* dlogits, int64_t lddl,
+                                  int accumulate, void* stream) {
+  if (T < 0 || T > kMaxTopkTokens || E < 1 || E > 1024) return Q4_ERR_SHAPE;
+  if (T == 0) return Q4_OK;
+  if (!logits || !slopes || !dlogits) return Q4_ERR_NULL;
+  if (ld < E || lddl < E) return Q4_ERR_SHAPE;
+  if (!aligned(logits, 4) || !aligned(slopes, 4) || !aligned(dloss, 4) || !aligned(dlogits, 4)) return Q4_ERR_ALIGN;
+  q4::BalanceGradArgs a{};
+  a.logits = logits;
+  a.ld = ld;
+  a.T = T;
+  a.E = E;
+  a.mask = mask;
+  a.slopes = slopes;
+  a.dloss = dloss;
+  a.dlogits = dlogits;
+  a.lddl = lddl;
+  a.accumulate = accumulate;
+  return hip_status(q4::launch_moe_balance_backward(a, as_stream(stream)));
+}
+
+q4_status q4_grad_workspace(int64_t n, size_t* bytes) {
+  if (!bytes) return Q4_ERR_NULL;
+  if (n < 0 || n > kMaxGrads) return Q4_ERR_SHAPE;
+  *bytes = q4::grad_workspace(n);
+  return Q4_OK;
+}
+
+q4_status q4_grad_norm(int64_t n, const void* const* grads, const int64_t* counts, const int32_t* dtypes,
+                       float* norm, void* workspace, size_t workspace_bytes, void* stream) {
+  const q4::GradList g{n, grads, counts, dtypes};
+  q4_status st = check_grads(g, nullptr);
+  if (st != Q4_OK) return st;
+  if (!norm) return Q4_ERR_NULL;
+  if (!aligned(norm, 4)) return Q4_ERR_ALIGN;
+  st = check_grad_workspace(n, workspace, workspace_bytes);
+  if (st != Q4_OK) return st;
+  return hip_status(q4::launch_grad_norm(g, norm, static_cast<double*>(workspace), as_stream(stream)));
+}
+
+q4_status q4_grad_clip(int64_t n, const void* const* grads, const int64_t* counts, const int32_t* dtypes,
+                       void* const* out, const float* norm_in, float max_norm, float* norm_out, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  const q4::GradList g{n, grads, counts, dtypes};
+  q4_status st = check_grads(g, out);
+  if (st != Q4_OK) return st;
+  if (!(max_norm >= 0.0f)) return Q4_ERR_SHAPE;
+  if (!aligned(norm_in, 4) || !aligned(norm_out, 4)) return Q4_ERR_ALIGN;
+  if (!norm_in) {
+    st = check_grad_workspace(n, workspace, workspace_bytes);
+    if (st != Q4_OK) return st;
+  }
+  st = check_apart(g, out);
+  if (st != Q4_OK) return st;
+  return hip_status(q4::launch_grad_clip(g, out, norm_in, max_norm, norm_in ? nullptr : norm_out,
+                                         static_cast<double*>(workspace), as_stream(stream)));
 }
 
 q4_status q4_moe_sort_workspace(int64_t T, int32_t k, int32_t E, size_t* bytes) {

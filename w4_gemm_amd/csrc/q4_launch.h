@@ -173,6 +173,49 @@ struct NormGradArgs {
 size_t rmsnorm_backward_workspace(int64_t rows, int64_t cols);
 hipError_t launch_rmsnorm_backward(const NormGradArgs& a, float* dweight, int accumulate, hipStream_t stream);
 
+// A router's balance loss (moe_balance.hip): 1 <= E <= 1024.
+struct BalanceArgs {
+  const float* logits;       // [T][ld]
+  int64_t ld, T;
+  int32_t E, k;
+  const int32_t* ids;        // [T][k]
+  const uint8_t* mask;       // [T] or NULL
+  float coef;
+  float* loss;               // [1]
+  int32_t* counts;           // [E]
+  float* slopes;             // [E]
+  float* sums;               // (of the workspace, set by the launch)
+  int32_t *part_counts, *part_tokens;
+};
+size_t moe_balance_workspace(int64_t T, int32_t E);
+hipError_t launch_moe_balance(BalanceArgs a, void* workspace, hipStream_t stream);
+struct BalanceGradArgs {
+  const float* logits;
+  int64_t ld, T;
+  int32_t E;
+  const uint8_t* mask;
+  const float* slopes;
+  const float* dloss;        // [1] or NULL (1)
+  float* dlogits;            // [T][lddl]
+  int64_t lddl;
+  int accumulate;
+};
+hipError_t launch_moe_balance_backward(const BalanceGradArgs& a, hipStream_t stream);
+
+// Gradients as host arrays (grad_clip.hip): contiguous, fp32 (dtype 1) or bf16.
+struct GradList {
+  int64_t n;
+  const void* const* data;
+  const int64_t* count;
+  const int32_t* dtype;
+};
+size_t grad_workspace(int64_t n);
+bool grad_fits(const GradList& g);
+hipError_t launch_grad_norm(const GradList& g, float* norm, double* sums, hipStream_t stream);
+// out NULL: in place; given NULL: the norm is made first, and written to norm.
+hipError_t launch_grad_clip(const GradList& g, void* const* out, const float* given, float max_norm, float* norm,
+                            double* sums, hipStream_t stream);
+
 // MoE routing: top-k experts per token (ids, softmax gates) from fp32
 // logits [T][ld], then the expert-major dispatch (offsets [E+1], gather
 // [T*k], inv [T][k]) in one workgroup whose LDS holds per-expert token
