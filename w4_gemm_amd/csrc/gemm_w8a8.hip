@@ -5,81 +5,417 @@
 //
 // The sum is exact in 32-bit integers (|code| <= 128, K < 2^17), so no split of
 // K changes the result.
+//
+// Both operands are row-major.  Their rows are copied to LDS by direct
+// global->LDS loads (1 KB per wave instruction, whole 128-byte lines of a row),
+// the 16-byte chunk c of row r to place c ^ key(r): a copy permutes chunks within
+// a line, a fragment read meets eight rows of different keys at once, and so
+// neither side has bank conflicts.
+//
+// v_mfma_i32_16x16x64_i8: lane l supplies row l % 16, k = 16 (l / 16) .. +15 of
+// both operands.  The weight is the instruction's row operand, so a lane ends
+// with 4 columns of one row of C; two tiles take the weight's rows
+// 32 q + 8 (i / 4) + i % 4 and the same + 4 (i = l % 16), which leaves 8
+// consecutive columns, 16 bytes of bf16, in a lane and 64 in four lanes.
 #include "q4_launch.h"
 #include "q4_lds.h"
 #include "q4_mma.h"
+
+#include <type_traits>
 
 namespace q4 {
 namespace {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
 
-constexpr int kB = 64;     // rows of A and of W per workgroup
-constexpr int kK = 128;    // k per stage
+struct Args {
+  const uint8_t* a;
+  const float* sa;
+  const uint8_t* w;
+  const float* sw;
+  uint16_t* c;
+  int64_t M, N, K, ldc;
+  int whole;    // rows of C at multiples of 16 bytes
+};
 
-// Four waves of 32 x 32 outputs; both operands' rows staged in LDS, the 16-byte
-// chunk c of row r at place c ^ (r & 7) so that the eight rows that a fragment
-// read meets at once lie in different banks.
-__global__ void __launch_bounds__(256)
-w8a8_kernel(const uint8_t* __restrict__ a, const float* __restrict__ sa, int64_t M, const uint8_t* __restrict__ w,
-            const float* __restrict__ sw, int64_t N, int64_t K, uint16_t* __restrict__ C, int64_t ldc) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][kB * kK];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t m0 = (int64_t)blockIdx.y * kB, n0 = (int64_t)blockIdx.x * kB;
-  i32x4_t acc[2][2];
+// Keys of a row of A (fragments take 16 rows in order) and of W (the order above).
+__device__ __forceinline__ int key_a(int r) { return r & 7; }
+__device__ __forceinline__ int key_w(int r) { return (r & 3) | ((r >> 1) & 4); }
+
+__device__ __forceinline__ i32x4_t mma(i32x4_t w, i32x4_t a, i32x4_t c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(w, a, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ i32x4_t read16(const uint8_t* p) { return *reinterpret_cast<const i32x4_t*>(p); }
+
+// Eight columns n .. n + 7 of row m from two tiles' sums.
+__device__ __forceinline__ void store8(const Args& p, int64_t m, int64_t n, i32x4_t lo, i32x4_t hi, float sa,
+                                       const float* sw) {
+  if (m >= p.M) return;
+  const float4 u = *reinterpret_cast<const float4*>(sw), v = *reinterpret_cast<const float4*>(sw + 4);
+  const uint32_t o[4] = {pk_bf16((float)lo[0] * (sa * u.x), (float)lo[1] * (sa * u.y)),
+                         pk_bf16((float)lo[2] * (sa * u.z), (float)lo[3] * (sa * u.w)),
+                         pk_bf16((float)hi[0] * (sa * v.x), (float)hi[1] * (sa * v.y)),
+                         pk_bf16((float)hi[2] * (sa * v.z), (float)hi[3] * (sa * v.w))};
+  uint16_t* c = p.c + m * p.ldc + n;
+  if (p.whole && n + 8 <= p.N) {
+    *reinterpret_cast<uint4*>(c) = make_uint4(o[0], o[1], o[2], o[3]);
+  } else {
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 8; ++j)
+      if (n + j < p.N) c[j] = (uint16_t)(o[j >> 1] >> (16 * (j & 1)));
+  }
+}
+
+// The block of C of a workgroup: an XCD's workgroups (every eighth) take
+// consecutive blocks of groups of `rows` block rows, so that those running at
+// once share panels of both operands in its L2.
+__device__ __forceinline__ void block_of(int rows, int64_t& bm, int64_t& bn) {
+  const uint32_t tn = gridDim.x, tm = gridDim.y, t = tm * tn;
+  const uint32_t b = blockIdx.y * tn + blockIdx.x;
+  const uint32_t lin = t % 8 == 0 ? (b % 8) * (t / 8) + b / 8 : b;
+  const uint32_t group = rows * tn, first = lin / group * rows, in = lin % group;
+  const uint32_t g = tm - first < (uint32_t)rows ? tm - first : (uint32_t)rows;
+  bm = first + in % g;
+  bn = in / g;
+}
+
+// ---- many rows ----------------------------------------------------------------
+// 256 x 256 of C by four waves of 128 x 128 (4 x 4 tiles of v_mfma_i32_32x32x32_i8,
+// 256 sums per lane, one wave per SIMD).  A stage is 128 k: 32 KB of A and 32 KB of
+// W, which take turns in a ring of five places, all of the LDS.  A stage has two
+// halves of 64 k; while the products of one run, one behind each of them a wave
+// issues the reads of the next half's fragments into the other register set and
+// its copies of stage u + 2: A's in the first half, into the place that W of stage
+// u - 1 left, W's in the second, into that of A of stage u, which every wave has
+// read by then.  One barrier per stage, in its middle.
+// Fragments of 32 rows: lane l supplies row l % 32, k = 16 (l / 32) .. +15.  The
+// weight's row for index i of a tile is 16 (i / 16) + 8 (i / 4 % 2) +
+// 4 (i / 8 % 2) + i % 4, which leaves twice 8 consecutive columns in a lane.
+constexpr int kBig = 256;
+constexpr int kPlace = kBig * 128;
+constexpr int kBigLds = 5 * kPlace;
+
+// Keys of rows for these fragments: of the 16 rows that a read meets in two lines
+// of 128 bytes, the even ones have different keys, and so have the odd ones.
+__device__ __forceinline__ int key32_a(int r) { return (r >> 1) & 7; }
+__device__ __forceinline__ int key32_w(int r) { return ((r >> 1) & 1) | ((r >> 2) & 2) | (r & 4); }
+
+// A buffer descriptor of `rows` rows of K bytes (raw bytes, bounds checked).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const uint8_t* p, int rows, int K) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, rows * K, 0x00020000);
+}
+
+__global__ void __launch_bounds__(256, 1)
+w8a8_big_kernel(const Args p) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  int64_t bm, bn;
+  block_of(4, bm, bn);
+  const int64_t m0 = bm * kBig, n0 = bn * kBig;
+  const int K = (int)p.K, U = K >> 7;
+  const int left_m = (int)(p.M - m0 < kBig ? p.M - m0 : kBig), left_n = (int)(p.N - n0 < kBig ? p.N - n0 : kBig);
+
+  // copies: wave w takes rows 64 w .. of A and of W, eight rows at a time
+  const uint8_t* src_a = uniform_ptr(p.a + m0 * K);
+  const uint8_t* src_w = uniform_ptr(p.w + n0 * K);
+  uint32_t at_a[8], at_w[8];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
-  for (int64_t k0 = 0; k0 < K; k0 += kK) {
-    __syncthreads();
+  for (int i = 0; i < 8; ++i) {
+    const int r = 64 * wave + 8 * i + (lane >> 3);
+    at_a[i] = (uint32_t)(r < left_m ? r : left_m - 1) * (uint32_t)K + 16 * ((lane & 7) ^ key32_a(r));
+    at_w[i] = (uint32_t)(r < left_n ? r : left_n - 1) * (uint32_t)K + 16 * ((lane & 7) ^ key32_w(r));
+  }
+  // (buffer loads: a descriptor of the rows, one offset per lane and copy, the stage's
+  // offset in a scalar; nothing is computed per copy)
+  const __amdgpu_buffer_rsrc_t rows_a = rows_of(src_a, left_m, K), rows_w = rows_of(src_w, left_n, K);
+  auto copy_a = [&](int place, int u, int i) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rows_a, (lptr_t)(smem + place + (64 * wave + 8 * i) * 128), 16, at_a[i], u * 128, 0, 0);
+  };
+  auto copy_w = [&](int place, int u, int i) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rows_w, (lptr_t)(smem + place + (64 * wave + 8 * i) * 128), 16, at_w[i], u * 128, 0, 0);
+  };
+
+  const int i32 = lane & 31, half = lane >> 5;
+  const int row_a = 128 * wm + i32;
+  const int row_w = 128 * wn + 16 * (i32 >> 4) + 8 * ((i32 >> 2) & 1) + 4 * ((i32 >> 3) & 1) + (i32 & 3);
+  const int pa = row_a * 128 + 16 * (half ^ key32_a(row_a)), pw = row_w * 128 + 16 * (half ^ key32_w(row_w));
+  i32x4_t fa[2][8], fw[2][8];
+  i32x16_t acc[4][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int c = threadIdx.x + 256 * i, r = c >> 3, p = c & 7;
-      const int64_t ra = m0 + r < M ? m0 + r : M - 1, rw = n0 + r < N ? n0 + r : N - 1;
-      *reinterpret_cast<uint4*>(&lds[0][r * kK + 16 * (p ^ (r & 7))]) =
-          *reinterpret_cast<const uint4*>(a + ra * K + k0 + 16 * p);
-      *reinterpret_cast<uint4*>(&lds[1][r * kK + 16 * (p ^ (r & 7))]) =
-          *reinterpret_cast<const uint4*>(w + rw * K + k0 + 16 * p);
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+  // fragment i of sixteen (A and W in turn, tile i / 4, k 32 (i / 2 % 2) ..) of half s
+  auto read = [&](int place_a, int place_w, int s, int i) {
+    const int f = i >> 1, x = 64 * s + 32 * (f & 1), t = (i >> 2) * 4096;
+    if (i & 1) fw[s][f] = read16(smem + place_w + (pw ^ x) + t); else fa[s][f] = read16(smem + place_a + (pa ^ x) + t);
+  };
+  auto product = [&](int s, int i) {   // i of 32: k half i / 16, tile (i / 4 % 4, i % 4)
+    const int h = i >> 4, r = (i >> 2) & 3, c = i & 3;
+    acc[r][c] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[s][2 * c + h], fa[s][2 * r + h], acc[r][c], 0, 0, 0);
+  };
+
+  const int second = U > 1 ? 1 : 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) copy_a(0, 0, i);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) copy_w(kPlace, 0, i);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) copy_a(2 * kPlace, second, i);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) copy_w(3 * kPlace, second, i);
+  wait_vmcnt_lgkm0<16>();
+  stage_barrier();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) read(0, kPlace, 0, i);
+  // places of A and W of this stage and the next, and the free one
+  int a0 = 0, w0 = kPlace, a1 = 2 * kPlace, w1 = 3 * kPlace, spare = 4 * kPlace;
+  for (int u = 0; u < U; ++u) {
+    const int from = u + 2 < U ? u + 2 : U - 1;   // (past the end: the last stage again, never read)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      copy_a(spare, from, i);
+      product(0, 4 * i);
+      read(a0, w0, 1, 2 * i);
+      product(0, 4 * i + 1);
+      read(a0, w0, 1, 2 * i + 1);
+      product(0, 4 * i + 2);
+      product(0, 4 * i + 3);
     }
-    __syncthreads();
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      i32x4_t fa[2], fw[2];
+    for (int i = 0; i < 8; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);   // a copy
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // a product
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // a read
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+    }
+    // this wave's part of stage u + 1 is there (of the later copies only A's eight
+    // may be on their way), and it has read all of stage u
+    wait_vmcnt_lgkm0<8>();
+    stage_barrier();
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int p = 16 * ((4 * s + (lane >> 4)) ^ (lane & 7));
-        fa[i] = *reinterpret_cast<const i32x4_t*>(&lds[0][(32 * (wave >> 1) + 16 * i + (lane & 15)) * kK + p]);
-        fw[i] = *reinterpret_cast<const i32x4_t*>(&lds[1][(32 * (wave & 1) + 16 * i + (lane & 15)) * kK + p]);
+    for (int i = 0; i < 8; ++i) {
+      copy_w(a0, from, i);
+      product(1, 4 * i);
+      read(a1, w1, 0, 2 * i);
+      product(1, 4 * i + 1);
+      read(a1, w1, 0, 2 * i + 1);
+      product(1, 4 * i + 2);
+      product(1, 4 * i + 3);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);   // a copy
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // a product
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // a read
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    const int a2 = spare, w2 = a0;
+    spare = w0;
+    a0 = a1;
+    w0 = w1;
+    a1 = a2;
+    w1 = w2;
+  }
+
+  // the scales, where the stages were
+  wait_vmcnt<0>();
+  __syncthreads();
+  float* scale_a = reinterpret_cast<float*>(smem);
+  float* scale_w = scale_a + kBig;
+  {
+    const int t = threadIdx.x;
+    scale_a[t] = p.sa[m0 + (t < left_m ? t : left_m - 1)];
+    scale_w[t] = p.sw[n0 + (t < left_n ? t : left_n - 1)];
+  }
+  __syncthreads();
+  // lane l, register 4 q + e of tile (i, j): row 32 i + l % 32, column 32 j + 16 (q / 2) + 8 (l / 32) + 4 (q % 2) + e
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 128 * wm + 32 * i + i32;
+    const float s = scale_a[r];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int n = 128 * wn + 32 * j + 16 * q + 8 * half;
+        const i32x16_t v = acc[i][j];
+        store8(p, m0 + r, n0 + n, i32x4_t{v[8 * q], v[8 * q + 1], v[8 * q + 2], v[8 * q + 3]},
+               i32x4_t{v[8 * q + 4], v[8 * q + 5], v[8 * q + 6], v[8 * q + 7]}, s, scale_w + n);
       }
+  }
+}
+
+// ---- fewer rows ----------------------------------------------------------------
+// WM x WN x WK waves of 16 TM x 32 TN outputs; the WK waves of a place share its k
+// and add their sums through LDS at the end.  Stages of BK k in S buffers, S - 1
+// of them on their way.
+template <int WM, int WN, int WK, int TM, int TN, int BK, int S>
+struct Tile {
+  static constexpr int kWaves = WM * WN * WK, kThreads = 64 * kWaves;
+  static constexpr int kM = 16 * TM * WM, kN = 32 * TN * WN, kRows = kM + kN;
+  static constexpr int kStage = kRows * BK, kCopies = kStage / 1024 / kWaves;
+  static constexpr size_t kLds = (size_t)S * kStage + (size_t)kRows * 4;
+  static_assert(kStage % (1024 * kWaves) == 0, "whole copies for every wave");
+  static_assert(BK % (64 * WK) == 0 && (WK - 1) * WM * WN * TM * TN * 2048 <= S * kStage, "sums fit into the stages");
+};
+
+template <int WM, int WN, int WK, int TM, int TN, int BK, int S>
+__global__ void __launch_bounds__((Tile<WM, WN, WK, TM, TN, BK, S>::kThreads))
+w8a8_tile_kernel(const Args p) {
+  using T = Tile<WM, WN, WK, TM, TN, BK, S>;
+  constexpr int kChunks = BK / 16, kCopyRows = 1024 / BK, kSteps = BK / 64 / WK;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  float* scale_a = reinterpret_cast<float*>(smem + (size_t)S * T::kStage);
+  float* scale_w = scale_a + T::kM;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wk = wave % WK, wn = wave / WK % WN, wm = wave / (WK * WN);
+  int64_t bm, bn;
+  block_of(4, bm, bn);
+  const int64_t m0 = bm * T::kM, n0 = bn * T::kN;
+  const int K = (int)p.K, U = (K + BK - 1) / BK;
+  const int left_m = (int)(p.M - m0 < T::kM ? p.M - m0 : T::kM), left_n = (int)(p.N - n0 < T::kN ? p.N - n0 : T::kN);
+
+  const uint8_t* src[T::kCopies];
+  uint32_t row_at[T::kCopies], chunk_at[T::kCopies];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < T::kCopies; ++i) {
+    const int r0 = (wave * T::kCopies + i) * kCopyRows;          // (uniform: all of A or all of W)
+    const int r = r0 + lane / kChunks;
+    const bool is_w = r0 >= T::kM;
+    src[i] = uniform_ptr(is_w ? p.w + n0 * K : p.a + m0 * K);
+    const int at = is_w ? r - T::kM : r, left = is_w ? left_n : left_m;
+    row_at[i] = (uint32_t)(at < left ? at : left - 1) * (uint32_t)K;
+    chunk_at[i] = 16 * ((lane % kChunks) ^ (is_w ? key_w(at) : key_a(at)));
+  }
+  auto copy = [&](int u) {
+    uint8_t* d = smem + (u % S) * T::kStage + wave * T::kCopies * 1024;
+    const int64_t k0 = (int64_t)u * BK;
+    if (BK == 128 || k0 + BK <= K) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[j], fa[i], acc[i][j], 0, 0, 0);
+      for (int i = 0; i < T::kCopies; ++i) copy16_to_lds(src[i] + k0 + (row_at[i] + chunk_at[i]), d + i * 1024);
+    } else {      // the last stage of a K that is no multiple: chunks behind it read its first one, and are not used
+      const uint32_t left = (uint32_t)(K - k0);
+#pragma unroll
+      for (int i = 0; i < T::kCopies; ++i)
+        copy16_to_lds(src[i] + k0 + (row_at[i] + (chunk_at[i] < left ? chunk_at[i] : 0u)), d + i * 1024);
+    }
+  };
+  // loads on their way when stage u is needed: the later stages that were begun
+  auto wait = [&](int u) {
+    const int later = (U - 1 - u) < S - 2 ? U - 1 - u : S - 2;
+    if (later <= 0) wait_vmcnt_lgkm0<0>();
+    else if (later == 1) wait_vmcnt_lgkm0<T::kCopies>();
+    else wait_vmcnt_lgkm0<2 * T::kCopies>();
+  };
+  static_assert(S >= 2 && S <= 4, "the counts above");
+
+  for (int t = threadIdx.x; t < T::kRows; t += T::kThreads)
+    scale_a[t] = t < T::kM ? p.sa[m0 + (t < left_m ? t : left_m - 1)]
+                           : p.sw[n0 + (t - T::kM < left_n ? t - T::kM : left_n - 1)];
+#pragma unroll
+  for (int u = 0; u < S - 1; ++u)
+    if (u < U) copy(u);
+
+  const int i16 = lane & 15, g = lane >> 4;
+  const int row_a = 16 * TM * wm + i16, row_w = 32 * TN * wn + 8 * (i16 >> 2) + (i16 & 3);
+  const int pa = row_a * BK, pw = (T::kM + row_w) * BK, ka = key_a(row_a), kw = key_w(row_w);
+  i32x4_t acc[TM][2 * TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < 2 * TN; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
+  for (int u = 0; u < U; ++u) {
+    wait(u);
+    stage_barrier();
+    if (u + S - 1 < U) copy(u + S - 1);
+    const uint8_t* b = smem + (u % S) * T::kStage;
+    const int left = K - u * BK;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int step = wk * kSteps + s;
+      if (BK > 128 && step * 64 >= left) break;
+      i32x4_t fa[TM], fw[2 * TN];
+#pragma unroll
+      for (int j = 0; j < 2 * TN; ++j)
+        fw[j] = read16(b + pw + 16 * ((4 * step + g) ^ kw) + (32 * (j >> 1) + 4 * (j & 1)) * BK);
+#pragma unroll
+      for (int i = 0; i < TM; ++i) fa[i] = read16(b + pa + 16 * ((4 * step + g) ^ ka) + 16 * i * BK);
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < 2 * TN; ++j) acc[i][j] = mma(fw[j], fa[i], acc[i][j]);
     }
   }
-  // lane l, register r of tile (i, j): row 16i + l % 16, column 16j + 4 (l / 16) + r
+  if constexpr (WK > 1) {
+    __syncthreads();     // every stage has been read
+    i32x4_t* side = reinterpret_cast<i32x4_t*>(smem);
+    const int place = (wm * WN + wn) * (WK - 1);
+    if (wk > 0) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t m = m0 + 32 * (wave >> 1) + 16 * i + (lane & 15);
-    if (m >= M) continue;
+      for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2 * TN; ++j) side[((place + wk - 1) * TM * 2 * TN + i * 2 * TN + j) * 64 + lane] = acc[i][j];
+    }
+    __syncthreads();
+    if (wk > 0) return;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t n = n0 + 32 * (wave & 1) + 16 * j + 4 * (lane >> 4) + r;
-        if (n < N) C[m * ldc + n] = (uint16_t)pk_bf16((float)acc[i][j][r] * (sa[m] * sw[n]), 0.0f);
-      }
+    for (int v = 0; v < WK - 1; ++v)
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < 2 * TN; ++j) acc[i][j] += side[((place + v) * TM * 2 * TN + i * 2 * TN + j) * 64 + lane];
   }
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int r = 16 * (TM * wm + i) + i16;
+    const float s = scale_a[r];
+#pragma unroll
+    for (int q = 0; q < TN; ++q) {
+      const int n = 32 * (TN * wn + q) + 8 * g;
+      store8(p, m0 + r, n0 + n, acc[i][2 * q], acc[i][2 * q + 1], s, scale_w + n);
+    }
+  }
+}
+
+template <int WM, int WN, int WK, int TM, int TN, int BK, int S>
+hipError_t run_tile(const Args& p, hipStream_t stream) {
+  using T = Tile<WM, WN, WK, TM, TN, BK, S>;
+  const hipError_t attr = set_max_lds<&w8a8_tile_kernel<WM, WN, WK, TM, TN, BK, S>>(T::kLds);
+  if (attr != hipSuccess) return attr;
+  const dim3 grid((unsigned)((p.N + T::kN - 1) / T::kN), (unsigned)((p.M + T::kM - 1) / T::kM));
+  w8a8_tile_kernel<WM, WN, WK, TM, TN, BK, S><<<grid, T::kThreads, T::kLds, stream>>>(p);
+  return hipGetLastError();
+}
+
+hipError_t run_big(const Args& p, hipStream_t stream) {
+  const hipError_t attr = set_max_lds<&w8a8_big_kernel>(kBigLds);
+  if (attr != hipSuccess) return attr;
+  const dim3 grid((unsigned)((p.N + kBig - 1) / kBig), (unsigned)((p.M + kBig - 1) / kBig));
+  w8a8_big_kernel<<<grid, 256, kBigLds, stream>>>(p);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_gemm_w8a8(const uint8_t* a, const float* sa, int64_t M, const uint8_t* w, const float* sw, int64_t N,
                             int64_t K, uint16_t* C, int64_t ldc, hipStream_t stream) {
-  const dim3 grid((unsigned)((N + kB - 1) / kB), (unsigned)((M + kB - 1) / kB));
-  w8a8_kernel<<<grid, 256, 0, stream>>>(a, sa, M, w, sw, N, K, C, ldc);
-  return hipGetLastError();
+  const Args p{a, sa, w, sw, C, M, N, K, ldc, (reinterpret_cast<uintptr_t>(C) & 15) == 0 && (ldc % 8 == 0 || M == 1)};
+  if (M <= 16) return run_tile<1, 1, 4, 1, 1, 512, 3>(p, stream);
+  if (M <= 32) return run_tile<1, 2, 2, 2, 1, 256, 3>(p, stream);
+  if (M <= 64) return run_tile<2, 2, 1, 2, 1, 256, 3>(p, stream);
+  if (M <= 512) return run_tile<2, 2, 1, 4, 2, 128, 2>(p, stream);
+  return run_big(p, stream);
 }
 
 }  // namespace q4
