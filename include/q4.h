@@ -278,8 +278,8 @@ q4_status q4_gemv(const q4_tensor* W, const void* x_bf16, int64_t B, int64_t ldx
  *                       per-block promotion of block-scaled FP8 GEMMs);
  *                       C = s_a[m] * sum_g s_w[n][g] * sum_(k in g) a8*q.
  *   A_q (Q4_INT8_ROW, rows M, cols K) with W Q4_INT8_ROW -> W8A8: sums of
- *                       products of bytes, exact in 32-bit integers (K < 2^17,
- *                       else Q4_ERR_SHAPE), one scale of the token and one of
+ *                       products of bytes, exact in 32-bit integers (K < 2^17
+ *                       and N < 2^27, else Q4_ERR_SHAPE), one scale of the token and one of
  *                       the channel on the sum:
  *                       C = (s_a[m] * s_w[n]) * sum_k a8*w8.
  * Other format pairs, and a Q4_FP8_ROW W: Q4_ERR_FORMAT.

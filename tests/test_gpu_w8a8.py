@@ -90,7 +90,12 @@ def test_quantize_strided_rows():
 SHAPES = [(1, 16, 128), (1, 1, 128), (2, 17, 256), (16, 64, 384), (17, 96, 512), (33, 130, 640), (64, 256, 1024),
           (65, 257, 1152), (127, 1000, 512), (128, 128, 128), (130, 512, 2048), (205, 1016, 896), (256, 256, 4096),
           (257, 264, 1280), (300, 1, 256), (512, 768, 1024), (1, 4096, 8192), (8, 2048, 7168), (48, 7168, 2048),
-          (1000, 1000, 1024)]
+          (1000, 1000, 1024),
+          # every kind of block, with one workgroup per CU and with two: 16 x 32, 32 x 64, 64 x 64, 128 x 64, 128 x 128,
+          # 256 x 256 (ragged in both directions, the shortest and odd numbers of stages)
+          (5, 8199, 640), (3, 16400, 128), (31, 8200, 384), (20, 24000, 256), (60, 20000, 128), (60, 30000, 384),
+          (250, 8100, 1152), (500, 8192, 640), (511, 8070, 2304), (1020, 8150, 1152), (2040, 8190, 128),
+          (2040, 8190, 1408), (4090, 1020, 4224)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)

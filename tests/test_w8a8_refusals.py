@@ -57,6 +57,7 @@ def test_gemm_refuses():
     assert gemm(64, desc(cols=1040), desc(rows=256, cols=1040)) == SHAPE     # K % 128
     assert gemm(64, desc(cols=1 << 17), desc(rows=256, cols=1 << 17)) == SHAPE
     assert gemm(64, desc(cols=0), desc(rows=256, cols=0)) == SHAPE
+    assert gemm(64, a, desc(rows=1 << 27), ldc=1 << 27) == SHAPE
     assert gemm(64, a, w, ldc=255) == SHAPE
     assert gemm(64, a, w, C=None) == NULL
     assert gemm(64, a, w, C=A16 + 1) == ALIGN

@@ -21,6 +21,7 @@ constexpr int64_t kMaxRows = ((int64_t)1 << 22) - 1;    // up to 1024 threads pe
 constexpr int64_t kMaxGrads = (int64_t)1 << 20;
 constexpr int64_t kMaxGradCount = (int64_t)1 << 44;   // sizes in bytes stay far below 2^63
 constexpr int64_t kMaxNormCols = 32768;               // a row in the registers of 16 waves
+constexpr int64_t kMaxIntN = (int64_t)1 << 27;        // 512 threads per 32 columns: below 2^32 threads
 constexpr int64_t kMaxIntK = (int64_t)1 << 17;        // 2^14 K < 2^31: sums of products of two bytes stay exact
 constexpr int64_t kMaxTopkTokens = ((int64_t)1 << 26) - 4;  // a wave per token, four a workgroup: below 2^32 threads
 
@@ -342,7 +343,7 @@ q4_status q4_gemm(int64_t M, const void* A_bf16, int64_t lda, const q4_tensor* A
     const bool w8a8 = A_q->fmt == Q4_INT8_ROW && w8;
     if (!w4a4 && !w4a8 && !w8a8) return Q4_ERR_FORMAT;
     if (A_q->rows != M || A_q->cols != K) return Q4_ERR_SHAPE;
-    if (w8a8 && K >= kMaxIntK) return Q4_ERR_SHAPE;
+    if (w8a8 && (K >= kMaxIntK || N >= kMaxIntN)) return Q4_ERR_SHAPE;
   }
   if (M == 0 || N == 0) return Q4_OK;
   if (K == 0) return Q4_ERR_SHAPE;

@@ -36,7 +36,8 @@ struct Args {
   const float* sw;
   uint16_t* c;
   int64_t M, N, K, ldc;
-  int whole;    // rows of C at multiples of 16 bytes
+  int whole;        // rows of C at multiples of 16 bytes
+  uint32_t tm, tn;  // blocks of C
 };
 
 // Keys of a row of A (fragments take 16 rows in order) and of W (the order above).
@@ -71,9 +72,8 @@ __device__ __forceinline__ void store8(const Args& p, int64_t m, int64_t n, i32x
 // The block of C of a workgroup: an XCD's workgroups (every eighth) take
 // consecutive blocks of groups of `rows` block rows, so that those running at
 // once share panels of both operands in its L2.
-__device__ __forceinline__ void block_of(int rows, int64_t& bm, int64_t& bn) {
-  const uint32_t tn = gridDim.x, tm = gridDim.y, t = tm * tn;
-  const uint32_t b = blockIdx.y * tn + blockIdx.x;
+__device__ __forceinline__ void block_of(const Args& p, int rows, int64_t& bm, int64_t& bn) {
+  const uint32_t tn = p.tn, tm = p.tm, t = tm * tn, b = blockIdx.x;
   const uint32_t lin = t % 8 == 0 ? (b % 8) * (t / 8) + b / 8 : b;
   const uint32_t group = rows * tn, first = lin / group * rows, in = lin % group;
   const uint32_t g = tm - first < (uint32_t)rows ? tm - first : (uint32_t)rows;
@@ -113,7 +113,7 @@ w8a8_big_kernel(const Args p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   int64_t bm, bn;
-  block_of(4, bm, bn);
+  block_of(p, 4, bm, bn);
   const int64_t m0 = bm * kBig, n0 = bn * kBig;
   const int K = (int)p.K, U = K >> 7;
   const int left_m = (int)(p.M - m0 < kBig ? p.M - m0 : kBig), left_n = (int)(p.N - n0 < kBig ? p.N - n0 : kBig);
@@ -264,11 +264,25 @@ template <int WM, int WN, int WK, int TM, int TN, int BK, int S>
 struct Tile {
   static constexpr int kWaves = WM * WN * WK, kThreads = 64 * kWaves;
   static constexpr int kM = 16 * TM * WM, kN = 32 * TN * WN, kRows = kM + kN;
-  static constexpr int kStage = kRows * BK, kCopies = kStage / 1024 / kWaves;
+  static constexpr int kStage = kRows * BK;
+  static constexpr int kCopiesA = kM * BK / 1024 / kWaves, kCopiesW = kN * BK / 1024 / kWaves;   // of a wave per stage
   static constexpr size_t kLds = (size_t)S * kStage + (size_t)kRows * 4;
-  static_assert(kStage % (1024 * kWaves) == 0, "whole copies for every wave");
+  static_assert(kM * BK % (1024 * kWaves) == 0 && kN * BK % (1024 * kWaves) == 0, "whole copies for every wave");
   static_assert(BK % (64 * WK) == 0 && (WK - 1) * WM * WN * TM * TN * 2048 <= S * kStage, "sums fit into the stages");
 };
+
+// Waits until only the copies of STAGES later stages may be on their way, W + a of
+// them in each (a <= A, the same in every stage).
+template <int W, int A, int STAGES, bool FEWER>
+__device__ __forceinline__ void wait_copies(int a) {
+  if constexpr (FEWER && A > 0) {
+    if (a < A) {
+      wait_copies<W, A - 1, STAGES, true>(a);
+      return;
+    }
+  }
+  wait_vmcnt_lgkm0<STAGES * (W + A)>();
+}
 
 template <int WM, int WN, int WK, int TM, int TN, int BK, int S>
 __global__ void __launch_bounds__((Tile<WM, WN, WK, TM, TN, BK, S>::kThreads))
@@ -281,42 +295,52 @@ w8a8_tile_kernel(const Args p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wk = wave % WK, wn = wave / WK % WN, wm = wave / (WK * WN);
   int64_t bm, bn;
-  block_of(4, bm, bn);
+  block_of(p, 4, bm, bn);
   const int64_t m0 = bm * T::kM, n0 = bn * T::kN;
   const int K = (int)p.K, U = (K + BK - 1) / BK;
   const int left_m = (int)(p.M - m0 < T::kM ? p.M - m0 : T::kM), left_n = (int)(p.N - n0 < T::kN ? p.N - n0 : T::kN);
 
-  const uint8_t* src[T::kCopies];
-  uint32_t row_at[T::kCopies], chunk_at[T::kCopies];
+  // Copy i of a wave: W's first, then A's, each kCopyRows rows.  The block of 16
+  // rows, whose copies of A are a third of all, leaves out those behind A's last row
+  // (what LDS holds there makes outputs that are not stored; one row of 28672 x 8192:
+  // 39.7 -> 38.7 us); for the others the branches cost more than they save.
+  constexpr bool kLeaveOut = T::kM == 16;
+  constexpr int kCopies = T::kCopiesW + T::kCopiesA;
+  const uint8_t* src_w = uniform_ptr(p.w + n0 * K);
+  const uint8_t* src_a = uniform_ptr(p.a + m0 * K);
+  uint32_t row_at[kCopies], chunk_at[kCopies];
 #pragma unroll
-  for (int i = 0; i < T::kCopies; ++i) {
-    const int r0 = (wave * T::kCopies + i) * kCopyRows;          // (uniform: all of A or all of W)
-    const int r = r0 + lane / kChunks;
-    const bool is_w = r0 >= T::kM;
-    src[i] = uniform_ptr(is_w ? p.w + n0 * K : p.a + m0 * K);
-    const int at = is_w ? r - T::kM : r, left = is_w ? left_n : left_m;
-    row_at[i] = (uint32_t)(at < left ? at : left - 1) * (uint32_t)K;
-    chunk_at[i] = 16 * ((lane % kChunks) ^ (is_w ? key_w(at) : key_a(at)));
+  for (int i = 0; i < kCopies; ++i) {
+    const bool is_w = i < T::kCopiesW;
+    const int r = ((is_w ? i : i - T::kCopiesW) * T::kWaves + wave) * kCopyRows + lane / kChunks;
+    const int left = is_w ? left_n : left_m;
+    row_at[i] = (uint32_t)(r < left ? r : left - 1) * (uint32_t)K;
+    chunk_at[i] = 16 * ((lane % kChunks) ^ (is_w ? key_w(r) : key_a(r)));
   }
+  int copies_a = kLeaveOut ? 0 : T::kCopiesA;
+  if (kLeaveOut)
+#pragma unroll
+    for (int i = 0; i < T::kCopiesA; ++i) copies_a += (i * T::kWaves + wave) * kCopyRows < left_m;
   auto copy = [&](int u) {
-    uint8_t* d = smem + (u % S) * T::kStage + wave * T::kCopies * 1024;
+    uint8_t* d = smem + (u % S) * T::kStage + wave * 1024;
     const int64_t k0 = (int64_t)u * BK;
-    if (BK == 128 || k0 + BK <= K) {
+    const uint32_t left = (uint32_t)(K - k0);
 #pragma unroll
-      for (int i = 0; i < T::kCopies; ++i) copy16_to_lds(src[i] + k0 + (row_at[i] + chunk_at[i]), d + i * 1024);
-    } else {      // the last stage of a K that is no multiple: chunks behind it read its first one, and are not used
-      const uint32_t left = (uint32_t)(K - k0);
-#pragma unroll
-      for (int i = 0; i < T::kCopies; ++i)
-        copy16_to_lds(src[i] + k0 + (row_at[i] + (chunk_at[i] < left ? chunk_at[i] : 0u)), d + i * 1024);
+    for (int i = 0; i < kCopies; ++i) {
+      const bool is_w = i < T::kCopiesW;
+      if (kLeaveOut && !is_w && i - T::kCopiesW >= copies_a) break;
+      // (in the last stage of a K that is no multiple, chunks behind it read its first one, and are not used)
+      const uint32_t c = BK == 128 || chunk_at[i] < left ? chunk_at[i] : 0u;
+      copy16_to_lds((is_w ? src_w : src_a) + k0 + (row_at[i] + c),
+                    d + (is_w ? T::kM * BK + i * T::kWaves * 1024 : (i - T::kCopiesW) * T::kWaves * 1024));
     }
   };
-  // loads on their way when stage u is needed: the later stages that were begun
+  // loads on their way when stage u is needed: those of the later stages that were begun
   auto wait = [&](int u) {
-    const int later = (U - 1 - u) < S - 2 ? U - 1 - u : S - 2;
+    const int later = U - 1 - u < S - 2 ? U - 1 - u : S - 2;
     if (later <= 0) wait_vmcnt_lgkm0<0>();
-    else if (later == 1) wait_vmcnt_lgkm0<T::kCopies>();
-    else wait_vmcnt_lgkm0<2 * T::kCopies>();
+    else if (later == 1) wait_copies<T::kCopiesW, T::kCopiesA, 1, kLeaveOut>(copies_a);
+    else wait_copies<T::kCopiesW, T::kCopiesA, 2, kLeaveOut>(copies_a);
   };
   static_assert(S >= 2 && S <= 4, "the counts above");
 
@@ -393,29 +417,62 @@ hipError_t run_tile(const Args& p, hipStream_t stream) {
   using T = Tile<WM, WN, WK, TM, TN, BK, S>;
   const hipError_t attr = set_max_lds<&w8a8_tile_kernel<WM, WN, WK, TM, TN, BK, S>>(T::kLds);
   if (attr != hipSuccess) return attr;
-  const dim3 grid((unsigned)((p.N + T::kN - 1) / T::kN), (unsigned)((p.M + T::kM - 1) / T::kM));
-  w8a8_tile_kernel<WM, WN, WK, TM, TN, BK, S><<<grid, T::kThreads, T::kLds, stream>>>(p);
+  w8a8_tile_kernel<WM, WN, WK, TM, TN, BK, S><<<p.tm * p.tn, T::kThreads, T::kLds, stream>>>(p);
   return hipGetLastError();
 }
 
 hipError_t run_big(const Args& p, hipStream_t stream) {
   const hipError_t attr = set_max_lds<&w8a8_big_kernel>(kBigLds);
   if (attr != hipSuccess) return attr;
-  const dim3 grid((unsigned)((p.N + kBig - 1) / kBig), (unsigned)((p.M + kBig - 1) / kBig));
-  w8a8_big_kernel<<<grid, 256, kBigLds, stream>>>(p);
+  w8a8_big_kernel<<<p.tm * p.tn, 256, kBigLds, stream>>>(p);
   return hipGetLastError();
 }
+
+// ---- which block ---------------------------------------------------------------
+// The block whose estimated time is least.  256 CUs hold one or two workgroups of
+// each kind at once; a round of up to 256 workgroups takes `one`, a round of up to
+// 512 takes `two` (big blocks: one per CU), in units of 0.01 us per 128 k, plus
+// `fixed` for the first copies and the stores, all measured on 128 x 8192 x 8192
+// and the like.  So 256 rows of 8192 x 8192 take 256 workgroups of 128 x 64 (34
+// us; 512 of 64 x 64: 37, 128 of 128 x 128: 44), 1024 rows 512 of 128 x 128 (70
+// us; 128 of 256 x 256: 82), 2048 rows 256 of 256 x 256 (108 us; 128 x 128: 137).
+struct Choice {
+  int rows, cols, one, two, fixed;
+  hipError_t (*few)(const Args&, hipStream_t);    // up to 256 workgroups
+  hipError_t (*run)(const Args&, hipStream_t);
+};
+
+const Choice kChoices[] = {
+    {16, 32, 12, 20, 150, run_tile<1, 1, 8, 1, 1, 512, 3>, run_tile<1, 1, 8, 1, 1, 512, 3>},
+    {32, 64, 25, 40, 200, run_tile<1, 2, 4, 2, 1, 256, 3>, run_tile<1, 2, 4, 2, 1, 256, 3>},
+    {64, 64, 31, 53, 200, run_tile<2, 2, 2, 2, 1, 128, 4>, run_tile<2, 2, 2, 2, 1, 128, 4>},
+    {128, 64, 48, 78, 300, run_tile<2, 2, 1, 4, 1, 128, 3>, run_tile<2, 2, 1, 4, 1, 128, 3>},
+    // (one workgroup per CU: a third stage on its way, 46 us for 512 x 8192 x 8192 and 56 without)
+    {128, 128, 70, 106, 500, run_tile<2, 2, 1, 4, 2, 128, 3>, run_tile<2, 2, 1, 4, 2, 128, 2>},
+    {256, 256, 166, 332, 800, run_big, run_big},
+};
 
 }  // namespace
 
 hipError_t launch_gemm_w8a8(const uint8_t* a, const float* sa, int64_t M, const uint8_t* w, const float* sw, int64_t N,
                             int64_t K, uint16_t* C, int64_t ldc, hipStream_t stream) {
-  const Args p{a, sa, w, sw, C, M, N, K, ldc, (reinterpret_cast<uintptr_t>(C) & 15) == 0 && (ldc % 8 == 0 || M == 1)};
-  if (M <= 16) return run_tile<1, 1, 4, 1, 1, 512, 3>(p, stream);
-  if (M <= 32) return run_tile<1, 2, 2, 2, 1, 256, 3>(p, stream);
-  if (M <= 64) return run_tile<2, 2, 1, 2, 1, 256, 3>(p, stream);
-  if (M <= 512) return run_tile<2, 2, 1, 4, 2, 128, 2>(p, stream);
-  return run_big(p, stream);
+  Args p{a, sa, w, sw, C, M, N, K, ldc, (reinterpret_cast<uintptr_t>(C) & 15) == 0 && (ldc % 8 == 0 || M == 1), 0, 0};
+  const Choice* best = nullptr;
+  int64_t least = 0;
+  for (const Choice& c : kChoices) {
+    const int64_t blocks = ((M + c.rows - 1) / c.rows) * ((N + c.cols - 1) / c.cols);
+    const int64_t rest = blocks % 512, rounds = blocks / 512 * c.two + (rest > 256 ? c.two : rest > 0 ? c.one : 0);
+    const int64_t t = rounds * (K / 128) + c.fixed;
+    if (!best || t < least) {
+      best = &c;
+      least = t;
+    }
+  }
+  const int64_t tm = (M + best->rows - 1) / best->rows, tn = (N + best->cols - 1) / best->cols;
+  if (tm * tn >= (int64_t)1 << 23) return hipErrorInvalidConfiguration;   // 2^32 threads: no C that large exists
+  p.tm = (uint32_t)tm;
+  p.tn = (uint32_t)tn;
+  return (tm * tn <= 256 ? best->few : best->run)(p, stream);
 }
 
 }  // namespace q4
