@@ -12,7 +12,7 @@ BF16, F32, I32 = torch.bfloat16, torch.float32, torch.int32
 
 
 def balance(**kw):
-    a = dict(lg=B, ld=64, T=8, E=64, k=4, ids=B, mask=B, coef=1.0, loss=B, counts=B, slopes=B, ws=B, wb=1 << 20)
+    a = dict(lg=B, ld=64, T=50000, E=64, k=4, ids=B, mask=B, coef=1.0, loss=B, counts=B, slopes=B, ws=B, wb=1 << 20)
     a.update(kw)
     return q4.lib().q4_moe_balance(a["lg"], a["ld"], a["T"], a["E"], a["k"], a["ids"], a["mask"], a["coef"], a["loss"],
                                    a["counts"], a["slopes"], a["ws"], a["wb"], None)
@@ -33,7 +33,7 @@ def test_balance():
         assert balance(**{p: None}) == NULL, p
         assert balance(**{p: B + 2}) == ALIGN, p
     n = ctypes.c_size_t()
-    assert q4.lib().q4_moe_balance_workspace(8, 64, ctypes.byref(n)) == OK
+    assert q4.lib().q4_moe_balance_workspace(50000, 64, ctypes.byref(n)) == OK
     assert balance(wb=n.value - 1) == SHAPE
     assert q4.lib().q4_moe_balance_workspace(8, 64, None) == NULL
     assert q4.lib().q4_moe_balance_workspace(8, 1025, ctypes.byref(n)) == SHAPE

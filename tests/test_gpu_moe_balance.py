@@ -51,7 +51,7 @@ def check(logits, ids, coef=1.0, mask=None, dloss=None, pad=0):
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 64, 8), (2, 3, 2), (5, 8, 8), (16, 64, 8), (63, 16, 1), (64, 64, 2),
                                    (65, 37, 4), (130, 65, 3), (257, 128, 8), (300, 129, 2), (511, 256, 8), (100, 250, 5),
                                    (77, 257, 3), (40, 512, 32), (33, 1000, 8), (12, 1024, 32), (3000, 64, 8),
-                                   (2500, 256, 4)])
+                                   (2500, 256, 4), (1025, 62, 2), (513, 100, 4), (300, 1021, 8), (700, 768, 8)])
 def test_all(T, E, k):
     logits, ids = make(T, E, k)
     check(logits, ids)

@@ -51,7 +51,7 @@ int8_rows_quantize_kernel(const uint16_t* __restrict__ src, int64_t ld, int64_t 
     unpack_bf16x8(v[i], x);
     m = max_bits8(x, m);
   }
-  m = wave_max(m);
+  m = lanes_max_bits(m);
   if constexpr (WAVES > 1) {
     __shared__ uint32_t part[kRows][WAVES];
     if ((tid & 63) == 0) part[in][tid >> 6] = m;
@@ -86,7 +86,7 @@ int8_rows_quantize_long_kernel(const uint16_t* __restrict__ src, int64_t ld, int
     unpack_bf16x8(*reinterpret_cast<const uint4*>(row + k0), x);
     m = max_bits8(x, m);
   }
-  m = wave_max(m);
+  m = lanes_max_bits(m);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
   __syncthreads();
 #pragma unroll

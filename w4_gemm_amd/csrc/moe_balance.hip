@@ -11,155 +11,272 @@
 // (the counts are whole numbers and have no gradient).  Workgroups walk over the
 // tokens and write their sums of p, their counts and their tokens to the
 // workspace; a second kernel adds those in order, in 64 bits, so the results do
-// not vary.
+// not vary.  Where there is little to read, one workgroup does it all in one
+// launch.
 #include "q4_launch.h"
-#include "q4_row8.h"
+#include "q4_wave.h"
 
 namespace q4 {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 1024;        // of the forward kernels
 constexpr int kWaves = kThreads / 64;
-constexpr int kBlocks = 256;         // workgroups of the first kernel at most
+constexpr int kBlocks = 256;          // workgroups of the first kernel at most
+constexpr int kBackThreads = 256;
+constexpr int kBackWaves = kBackThreads / 64;
 
-// LPT lanes hold a token's E <= LPT * PER logits, lane i of them the experts
-// i, i + LPT, ...
+// Entries of a workgroup's row in the workspace: whole pieces of 16 bytes.
+__host__ __device__ __forceinline__ int padded(int E) { return (E + 3) & ~3; }
+
+// LPT lanes hold a token's E <= LPT * PER logits, in groups of four: value 4 q + j
+// of lane i is expert 4 LPT q + 4 i + j.
 template <int LPT>
-__device__ __forceinline__ float part_max(float v) {
+__device__ __forceinline__ int expert_of(int sub, int i) { return 4 * LPT * (i >> 2) + 4 * sub + (i & 3); }
+
+// WIDE: E, the leading dimension and the address allow loads of 16 bytes.  `there`:
+// the token exists.  (A masked token's logits are read all the same, so that they
+// need not wait for its mask, and are replaced behind it.)
+template <int LPT, int PER, bool WIDE>
+__device__ __forceinline__ void load_logits(const float* row, int sub, int E, bool there, float (&v)[PER]) {
 #pragma unroll
-  for (int off = LPT / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off));
-  return v;
-}
-template <int LPT>
-__device__ __forceinline__ float part_sum(float v) {
+  for (int q = 0; q < PER / 4; ++q) {
+    const int e = expert_of<LPT>(sub, 4 * q);
+    if constexpr (WIDE) {
+      float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (there && e < E) f = *reinterpret_cast<const float4*>(row + e);
+      v[4 * q] = f.x;
+      v[4 * q + 1] = f.y;
+      v[4 * q + 2] = f.z;
+      v[4 * q + 3] = f.w;
+    } else {
 #pragma unroll
-  for (int off = LPT / 2; off > 0; off >>= 1) v += __shfl_xor(v, off);
-  return v;
+      for (int j = 0; j < 4; ++j) v[4 * q + j] = there && e + j < E ? row[e + j] : -INFINITY;
+    }
+  }
 }
 
-// Softmax of the token's logits v; all zeros where every logit is -inf, NaN
-// where one is NaN (the sum carries it: a maximum passes over NaN).
+// Softmax of a token's logits (-inf behind the last one); all zeros where every
+// logit is -inf and for a token that does not count, NaN where one is NaN (the sum
+// carries it: a maximum passes over NaN).
 template <int LPT, int PER>
-__device__ __forceinline__ void softmax(float (&v)[PER], int sub, int E) {
+__device__ __forceinline__ void softmax(float (&v)[PER], bool here) {
+#pragma unroll
+  for (int i = 0; i < PER; ++i) v[i] = here ? v[i] : -INFINITY;
   float m = v[0];
 #pragma unroll
   for (int i = 1; i < PER; ++i) m = fmaxf(m, v[i]);
-  m = part_max<LPT>(m);
+  m = lanes_max<LPT>(m);
   const float from = m == -INFINITY ? 0.0f : m;
+  // exp(d) as 2^(d log2 e) in one instruction (within a few 2^-24 of it times 1 + |d|;
+  // expf's further steps and a division made 22.6 us of the 17.7 that 65537 tokens of
+  // 256 experts take)
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    v[i] = sub + LPT * i < E ? expf(v[i] - from) : 0.0f;
+    v[i] = __builtin_amdgcn_exp2f((v[i] - from) * 1.44269504f);
     s += v[i];
   }
-  s = part_sum<LPT>(s);
-  const float by = s == 0.0f ? 0.0f : 1.0f / s;
+  s = lanes_sum<LPT>(s);
+  const float by = s == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(s);   // (within 1 ulp; 1 <= s <= 1024, or NaN)
 #pragma unroll
   for (int i = 0; i < PER; ++i) v[i] *= by;
 }
 
-template <int LPT, int PER>
+// slope and loss's part of an expert with c choices and probabilities p among n
+// tokens.
+__device__ __forceinline__ double finish_expert(const BalanceArgs& a, int e, double p, int64_t c, int64_t n) {
+  const double slope = n ? (double)a.coef * a.E * (double)c / ((double)a.k * (double)n * (double)n) : 0.0;
+  a.counts[e] = (int32_t)c;
+  a.slopes[e] = (float)slope;
+  return slope * p;
+}
+
+// Sum of the threads' parts of the loss, in order (in the first thread).
+__device__ __forceinline__ double block_loss(double l, double (&part)[kWaves]) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) l += __shfl_xor(l, off);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = l;
+  __syncthreads();
+  if (threadIdx.x == 0)
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) l += part[w];
+  return l;
+}
+
+// What a lane needs of a token.
+template <int LPT, int PER, int IDS>
+struct Turn {
+  float v[PER];
+  uint32_t id[IDS];
+  uint8_t mask;
+  bool there;
+  template <bool WIDE>
+  __device__ __forceinline__ void load(const BalanceArgs& a, int64_t t, int sub) {
+    there = t < a.T;
+    mask = 1;
+    if (there && a.mask) mask = a.mask[t];
+    load_logits<LPT, PER, WIDE>(a.logits + t * a.ld, sub, a.E, there, v);
+#pragma unroll
+    for (int j = 0; j < IDS; ++j)
+      id[j] = there && sub + LPT * j < a.k ? (uint32_t)a.ids[t * a.k + sub + LPT * j] : ~0u;
+  }
+};
+
+// ONE: a single workgroup, which finishes by itself.
+template <int LPT, int PER, bool WIDE, bool ONE>
 __global__ void __launch_bounds__(kThreads)
 moe_balance_kernel(const BalanceArgs a) {
-  constexpr int kTokens = 64 / LPT;   // of a wave at once
+  constexpr int kTokens = 64 / LPT;          // of a wave side by side
+  constexpr int kTurns = PER == 4 ? 4 : 1;   // and one behind the other with their loads on the way together
+  constexpr int kIds = LPT == 16 ? 2 : 1;    // choices of a lane (k <= 32)
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane % LPT;
   const int E = a.E;
-  extern __shared__ uint32_t lds[];
-  uint32_t* count = lds;                                    // [E]
-  uint32_t* tokens = lds + E;                               // [1]
-  float* side = reinterpret_cast<float*>(lds + E + 1);      // [kWaves][E]
-  for (int e = threadIdx.x; e < E + 1; e += kThreads) lds[e] = 0u;
+  __shared__ uint32_t count[1024];
+  __shared__ uint32_t tokens;
+  __shared__ double part[kWaves];
+  extern __shared__ float side[];            // [kWaves][E]
+  for (int e = threadIdx.x; e < E; e += kThreads) count[e] = 0u;
+  if (threadIdx.x == 0) tokens = 0u;
   __syncthreads();
   float sum[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) sum[i] = 0.0f;
   uint32_t mine = 0;
   const int64_t step = (int64_t)gridDim.x * kWaves * kTokens;
-  for (int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * kTokens; t0 < a.T; t0 += step) {
-    const int64_t t = t0 + lane / LPT;
-    const bool here = t < a.T && (!a.mask || a.mask[t] != 0);
-    float v[PER];
+  Turn<LPT, PER, kIds> now[kTurns], next[kTurns];
+  auto load = [&](Turn<LPT, PER, kIds> (&g)[kTurns], int64_t t0) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = sub + LPT * i;
-      v[i] = here && e < E ? a.logits[t * a.ld + e] : -INFINITY;
-    }
-    if (here) {
-      for (int j = sub; j < a.k; j += LPT) {
-        const uint32_t id = (uint32_t)a.ids[t * a.k + j];
-        if (id < (uint32_t)E) atomicAdd(&count[id], 1u);
-      }
-      if (sub == 0) ++mine;
-    }
-    softmax<LPT, PER>(v, sub, E);
+    for (int u = 0; u < kTurns; ++u) g[u].template load<WIDE>(a, t0 + u * step + lane / LPT, sub);
+  };
+  int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * kTokens;
+  if (t0 < a.T) load(next, t0);
+  for (; t0 < a.T; t0 += step * kTurns) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) sum[i] += v[i];
+    for (int u = 0; u < kTurns; ++u) now[u] = next[u];
+    if (t0 + step * kTurns < a.T) load(next, t0 + step * kTurns);   // on the way while these are worked on
+#pragma unroll
+    for (int u = 0; u < kTurns; ++u) {
+      const bool here = now[u].there && now[u].mask != 0;
+#pragma unroll
+      for (int j = 0; j < kIds; ++j)
+        if (here && now[u].id[j] < (uint32_t)E) atomicAdd(&count[now[u].id[j]], 1u);
+      if (here && sub == 0) ++mine;
+      softmax<LPT, PER>(now[u].v, here);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) sum[i] += now[u].v[i];
+    }
   }
-  if (mine) atomicAdd(tokens, mine);
+  if (mine) atomicAdd(&tokens, mine);
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
 #pragma unroll
     for (int off = LPT; off < 64; off <<= 1) sum[i] += __shfl_xor(sum[i], off);
-    const int e = sub + LPT * i;
+    const int e = expert_of<LPT>(sub, i);
     if (lane < LPT && e < E) side[wave * E + e] = sum[i];
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kThreads) {
-    float s = 0.0f;
+  double l = 0.0;
+  if (threadIdx.x < E) {   // (E <= 1024 = kThreads)
+    const int e = threadIdx.x;
+    if constexpr (ONE) {
+      double p = 0.0;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) s += side[w * E + e];
-    a.sums[(int64_t)blockIdx.x * E + e] = s;
-    a.part_counts[(int64_t)blockIdx.x * E + e] = (int32_t)count[e];
+      for (int w = 0; w < kWaves; ++w) p += (double)side[w * E + e];
+      l = finish_expert(a, e, p, count[e], tokens);
+    } else {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) s += side[w * E + e];
+      a.sums[(int64_t)blockIdx.x * padded(E) + e] = s;
+      a.part_counts[(int64_t)blockIdx.x * padded(E) + e] = (int32_t)count[e];
+    }
   }
-  if (threadIdx.x == 0) a.part_tokens[blockIdx.x] = (int32_t)*tokens;
+  if constexpr (ONE) {
+    l = block_loss(l, part);
+    if (threadIdx.x == 0) *a.loss = (float)l;
+  } else if (threadIdx.x == 0) {
+    a.part_tokens[blockIdx.x] = (int32_t)tokens;
+    if (blockIdx.x == 0) *a.ticket = 0u;
+  }
 }
 
-// The workgroups' sums, added in order: a thread per expert and slice of them.
-constexpr int kFinish = 1024;
-__global__ void __launch_bounds__(kFinish)
+// The workgroups' sums, added in order: a workgroup per 64 experts, in it a thread
+// per four of them and 64th of the sums, then 16 threads per expert.  The last
+// workgroup to end (the ticket was cleared by the first kernel) adds their parts
+// of the loss, in their order.
+constexpr int kFinishExperts = 64;
+constexpr int kFinishMost = 1024 / kFinishExperts;   // workgroups
+__global__ void __launch_bounds__(kThreads)
 moe_balance_finish_kernel(const BalanceArgs a, int blocks) {
-  __shared__ double psum[kFinish];
-  __shared__ int64_t csum[kFinish];
-  __shared__ double loss[kFinish / 64];
-  const int E = a.E, tid = threadIdx.x;
-  int lanes = 64;                       // experts side by side
-  while (lanes < E) lanes <<= 1;        // (E <= 1024 = kFinish)
-  const int slices = kFinish / lanes, e = tid % lanes, slice = tid / lanes;
-  int64_t n = 0;
-  for (int b = 0; b < blocks; ++b) n += a.part_tokens[b];
-  double p = 0.0;
-  int64_t c = 0;
-  if (e < E)
-    for (int b = slice; b < blocks; b += slices) {
-      p += (double)a.sums[(int64_t)b * E + e];
-      c += a.part_counts[(int64_t)b * E + e];
+  constexpr int kSlices = kThreads / (kFinishExperts / 4);
+  __shared__ double psum[kSlices][kFinishExperts];
+  __shared__ int32_t csum[kSlices][kFinishExperts];
+  __shared__ double part[kWaves];
+  __shared__ uint32_t tokens;
+  const int row = padded(a.E), tid = threadIdx.x, quad = tid % 16, slice = tid / 16;
+  const int e0 = blockIdx.x * kFinishExperts;
+  if (tid == 0) tokens = 0u;
+  const uint32_t here = tid < blocks ? (uint32_t)a.part_tokens[tid] : 0u;
+  double p[4] = {0.0, 0.0, 0.0, 0.0};
+  int32_t c[4] = {0, 0, 0, 0};
+  if (e0 + 4 * quad < row) {
+#pragma unroll
+    for (int i = 0; i < (kBlocks + kSlices - 1) / kSlices; ++i) {
+      const int b = slice + i * kSlices;
+      if (b >= blocks) break;
+      const float4 s = *reinterpret_cast<const float4*>(a.sums + (int64_t)b * row + e0 + 4 * quad);
+      const int4 n = *reinterpret_cast<const int4*>(a.part_counts + (int64_t)b * row + e0 + 4 * quad);
+      p[0] += (double)s.x;
+      p[1] += (double)s.y;
+      p[2] += (double)s.z;
+      p[3] += (double)s.w;
+      c[0] += n.x;
+      c[1] += n.y;
+      c[2] += n.z;
+      c[3] += n.w;
     }
-  psum[tid] = p;
-  csum[tid] = c;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    psum[slice][4 * quad + j] = p[j];
+    csum[slice][4 * quad + j] = c[j];
+  }
+  __syncthreads();
+  if (here) atomicAdd(&tokens, here);
+  const int e = tid / 16;              // (64 experts of 16 threads)
+  double ps = 0.0;
+  int32_t cs = 0;
+#pragma unroll
+  for (int i = 0; i < kSlices / 16; ++i) {
+    ps += psum[tid % 16 + 16 * i][e];
+    cs += csum[tid % 16 + 16 * i][e];
+  }
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) {
+    ps += __shfl_xor(ps, off);
+    cs += __shfl_xor(cs, off);
+  }
   __syncthreads();
   double l = 0.0;
-  if (slice == 0 && e < E) {
-    for (int s = 1; s < slices; ++s) {
-      p += psum[s * lanes + e];
-      c += csum[s * lanes + e];
-    }
-    const double slope = n ? (double)a.coef * E * (double)c / ((double)a.k * (double)n * (double)n) : 0.0;
-    l = slope * p;
-    a.counts[e] = (int32_t)c;
-    a.slopes[e] = (float)slope;
-  }
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) l += __shfl_xor(l, off);
-  if ((tid & 63) == 0) loss[tid >> 6] = l;
-  __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < kFinish / 64; ++w) l += loss[w];
+  if (tid % 16 == 0 && e0 + e < a.E) l = finish_expert(a, e0 + e, ps, cs, tokens);
+  l = block_loss(l, part);
+  if (tid != 0) return;
+  if (gridDim.x == 1) {
     *a.loss = (float)l;
+    return;
   }
+  // (the parts and the ticket pass between XCDs: agent scope)
+  uint64_t* parts = reinterpret_cast<uint64_t*>(a.parts);
+  __hip_atomic_store(parts + blockIdx.x, __builtin_bit_cast(uint64_t, l), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (__hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) != gridDim.x - 1) return;
+  l = 0.0;
+  for (unsigned b = 0; b < gridDim.x; ++b)
+    l += __builtin_bit_cast(double, __hip_atomic_load(parts + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+  *a.loss = (float)l;
 }
 
-template <int LPT, int PER>
-__global__ void __launch_bounds__(kThreads)
+template <int LPT, int PER, bool WIDE>
+__global__ void __launch_bounds__(kBackThreads)
 moe_balance_backward_kernel(const BalanceGradArgs a) {
   constexpr int kTokens = 64 / LPT;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane % LPT;
@@ -167,72 +284,121 @@ moe_balance_backward_kernel(const BalanceGradArgs a) {
   const float dloss = a.dloss ? *a.dloss : 1.0f;
   float slope[PER];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) slope[i] = sub + LPT * i < E ? a.slopes[sub + LPT * i] : 0.0f;
-  const int64_t step = (int64_t)gridDim.x * kWaves * kTokens;
-  for (int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * kTokens; t0 < a.T; t0 += step) {
+  for (int i = 0; i < PER; ++i) {
+    const int e = expert_of<LPT>(sub, i);
+    slope[i] = e < E ? a.slopes[e] : 0.0f;
+  }
+  const int64_t step = (int64_t)gridDim.x * kBackWaves * kTokens;
+  for (int64_t t0 = ((int64_t)blockIdx.x * kBackWaves + wave) * kTokens; t0 < a.T; t0 += step) {
     const int64_t t = t0 + lane / LPT;
     const bool here = t < a.T && (!a.mask || a.mask[t] != 0);
     float v[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = sub + LPT * i;
-      v[i] = here && e < E ? a.logits[t * a.ld + e] : -INFINITY;
-    }
-    softmax<LPT, PER>(v, sub, E);
+    load_logits<LPT, PER, WIDE>(a.logits + t * a.ld, sub, E, t < a.T, v);
+    softmax<LPT, PER>(v, here);
     float c = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) c = __builtin_fmaf(v[i], slope[i], c);
-    c = part_sum<LPT>(c);
+    c = lanes_sum<LPT>(c);
     if (t >= a.T || (a.accumulate && !here)) continue;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = sub + LPT * i;
-      if (e < E) {
-        float* o = a.dlogits + t * a.lddl + e;
-        const float g = dloss * (v[i] * (slope[i] - c));
-        *o = here ? (a.accumulate ? *o + g : g) : 0.0f;
+    for (int i = 0; i < PER; ++i) v[i] = here ? dloss * (v[i] * (slope[i] - c)) : 0.0f;
+    float* row = a.dlogits + t * a.lddl;
+#pragma unroll
+    for (int q = 0; q < PER / 4; ++q) {
+      const int e = expert_of<LPT>(sub, 4 * q);
+      if constexpr (WIDE) {
+        if (e >= E) continue;
+        float4* o = reinterpret_cast<float4*>(row + e);
+        float4 f = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        if (a.accumulate) {
+          const float4 b = *o;
+          f = make_float4(b.x + f.x, b.y + f.y, b.z + f.z, b.w + f.w);
+        }
+        *o = f;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (e + j < E) row[e + j] = a.accumulate ? row[e + j] + v[4 * q + j] : v[4 * q + j];
       }
     }
   }
 }
 
-// Tokens per workgroup at once for E experts.
-int tokens_at_once(int E) { return kWaves * (E <= 64 ? 4 : E <= 128 ? 2 : 1); }
+// Tokens of a wave side by side.
+int tokens_at_once(int E) { return E <= 64 ? 4 : E <= 128 ? 2 : 1; }
 
+// One workgroup up to 8 turns of all its waves (512 tokens of 64 experts): 1024
+// tokens take it 13 us, and 5.5 us and a second launch of 5.5 us over the card; each
+// launch costs the caller 3.3 us besides.
 unsigned balance_blocks(int64_t T, int E) {
-  const int64_t per = tokens_at_once(E), b = (T + per - 1) / per;
-  return (unsigned)(b < kBlocks ? b : kBlocks);
+  const int64_t per = kWaves * tokens_at_once(E), turns = (T + per - 1) / per;
+  if (turns <= 8) return 1;
+  return (unsigned)(turns < kBlocks ? turns : kBlocks);
+}
+
+bool wide(const void* p, int64_t ld, int E) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 4 == 0 && E % 4 == 0;
+}
+
+template <int LPT, int PER, bool WIDE, bool ONE>
+hipError_t balance_as(const BalanceArgs& a, unsigned blocks, hipStream_t stream) {
+  const size_t side = (size_t)a.E * kWaves * 4;
+  if (side > 32768) {   // (with the kernel's own LDS past 64 KB at the most experts)
+    const hipError_t attr = set_max_lds<&moe_balance_kernel<LPT, PER, WIDE, ONE>>(65536);
+    if (attr != hipSuccess) return attr;
+  }
+  moe_balance_kernel<LPT, PER, WIDE, ONE><<<blocks, kThreads, side, stream>>>(a);
+  return hipGetLastError();
+}
+
+template <int LPT, int PER, bool ONE>
+hipError_t balance(const BalanceArgs& a, unsigned blocks, hipStream_t stream) {
+  return wide(a.logits, a.ld, a.E) ? balance_as<LPT, PER, true, ONE>(a, blocks, stream)
+                                   : balance_as<LPT, PER, false, ONE>(a, blocks, stream);
+}
+
+template <int LPT, int PER>
+void balance_backward(const BalanceGradArgs& a, hipStream_t stream) {
+  const int64_t per = kBackWaves * tokens_at_once(a.E), b = (a.T + per - 1) / per;
+  auto kernel = wide(a.logits, a.ld, a.E) && wide(a.dlogits, a.lddl, a.E) ? moe_balance_backward_kernel<LPT, PER, true>
+                                                                         : moe_balance_backward_kernel<LPT, PER, false>;
+  kernel<<<(unsigned)(b < 4096 ? b : 4096), kBackThreads, 0, stream>>>(a);
+}
+
+template <bool ONE>
+hipError_t balance_of(const BalanceArgs& a, unsigned blocks, hipStream_t stream) {
+  if (a.E <= 64) return balance<16, 4, ONE>(a, blocks, stream);
+  if (a.E <= 128) return balance<32, 4, ONE>(a, blocks, stream);
+  if (a.E <= 256) return balance<64, 4, ONE>(a, blocks, stream);
+  return balance<64, 16, ONE>(a, blocks, stream);
 }
 
 }  // namespace
 
-size_t moe_balance_workspace(int64_t T, int32_t E) { return (size_t)balance_blocks(T, E) * ((size_t)E * 8 + 4); }
+size_t moe_balance_workspace(int64_t T, int32_t E) {
+  const unsigned b = balance_blocks(T, E);
+  return b > 1 ? kFinishMost * 8 + (size_t)b * ((size_t)padded(E) * 8 + 4) + 4 : 0;
+}
 
 hipError_t launch_moe_balance(BalanceArgs a, void* workspace, hipStream_t stream) {
-  const unsigned blocks = a.T ? balance_blocks(a.T, a.E) : 0;
-  a.sums = static_cast<float*>(workspace);
-  a.part_counts = reinterpret_cast<int32_t*>(a.sums + (size_t)blocks * a.E);
-  a.part_tokens = a.part_counts + (size_t)blocks * a.E;
-  if (blocks) {
-    auto kernel = a.E <= 64    ? moe_balance_kernel<16, 4>
-                  : a.E <= 128 ? moe_balance_kernel<32, 4>
-                  : a.E <= 256 ? moe_balance_kernel<64, 4>
-                               : moe_balance_kernel<64, 16>;
-    kernel<<<blocks, kThreads, ((size_t)a.E * (1 + kWaves) + 1) * 4, stream>>>(a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  moe_balance_finish_kernel<<<1, kFinish, 0, stream>>>(a, (int)blocks);
+  const unsigned blocks = balance_blocks(a.T, a.E);
+  if (blocks == 1) return balance_of<true>(a, 1, stream);
+  a.parts = static_cast<double*>(workspace);
+  a.sums = reinterpret_cast<float*>(a.parts + kFinishMost);
+  a.part_counts = reinterpret_cast<int32_t*>(a.sums + (size_t)blocks * padded(a.E));
+  a.part_tokens = a.part_counts + (size_t)blocks * padded(a.E);
+  a.ticket = reinterpret_cast<uint32_t*>(a.part_tokens + blocks);
+  const hipError_t e = balance_of<false>(a, blocks, stream);
+  if (e != hipSuccess) return e;
+  moe_balance_finish_kernel<<<(a.E + kFinishExperts - 1) / kFinishExperts, kThreads, 0, stream>>>(a, (int)blocks);
   return hipGetLastError();
 }
 
 hipError_t launch_moe_balance_backward(const BalanceGradArgs& a, hipStream_t stream) {
-  const int64_t per = tokens_at_once(a.E), b = (a.T + per - 1) / per;
-  auto kernel = a.E <= 64    ? moe_balance_backward_kernel<16, 4>
-                : a.E <= 128 ? moe_balance_backward_kernel<32, 4>
-                : a.E <= 256 ? moe_balance_backward_kernel<64, 4>
-                             : moe_balance_backward_kernel<64, 16>;
-  kernel<<<(unsigned)(b < 4096 ? b : 4096), kThreads, 0, stream>>>(a);
+  if (a.E <= 64) balance_backward<16, 4>(a, stream);
+  else if (a.E <= 128) balance_backward<32, 4>(a, stream);
+  else if (a.E <= 256) balance_backward<64, 4>(a, stream);
+  else balance_backward<64, 16>(a, stream);
   return hipGetLastError();
 }
 

@@ -184,8 +184,10 @@ struct BalanceArgs {
   float* loss;               // [1]
   int32_t* counts;           // [E]
   float* slopes;             // [E]
-  float* sums;               // (of the workspace, set by the launch)
+  double* parts;             // (of the workspace, set by the launch)
+  float* sums;
   int32_t *part_counts, *part_tokens;
+  uint32_t* ticket;
 };
 size_t moe_balance_workspace(int64_t T, int32_t E);
 hipError_t launch_moe_balance(BalanceArgs a, void* workspace, hipStream_t stream);

@@ -8,6 +8,7 @@
 #pragma once
 
 #include "q4_device.h"
+#include "q4_wave.h"
 
 namespace q4 {
 
@@ -42,6 +43,22 @@ __device__ __forceinline__ uint2 e4m3_pack8(const float (&x)[8], float f) {
   return p;
 }
 
+// 16 bytes read or written with (PAST) or without the hint that they are not used
+// again: streams longer than the caches then do not turn over what they hold.
+template <bool PAST>
+__device__ __forceinline__ uint4 load16(const void* p) {
+  typedef uint32_t quad_t __attribute__((ext_vector_type(4)));
+  const quad_t* q = static_cast<const quad_t*>(p);
+  return __builtin_bit_cast(uint4, PAST ? __builtin_nontemporal_load(q) : *q);
+}
+template <bool PAST>
+__device__ __forceinline__ void store16(void* p, uint4 v) {
+  typedef uint32_t quad_t __attribute__((ext_vector_type(4)));
+  quad_t* q = static_cast<quad_t*>(p);
+  if (PAST) __builtin_nontemporal_store(__builtin_bit_cast(quad_t, v), q);
+  else *q = __builtin_bit_cast(quad_t, v);
+}
+
 __device__ __forceinline__ void unpack_bf16x8(const uint4& v, float (&x)[8]) {
   x[0] = bf16_lo(v.x); x[1] = bf16_hi(v.x);
   x[2] = bf16_lo(v.y); x[3] = bf16_hi(v.y);
@@ -58,21 +75,6 @@ __device__ __forceinline__ uint32_t max_bits8(const float (&x)[8], uint32_t m) {
     m = b > m ? b : m;
   }
   return m;
-}
-
-__device__ __forceinline__ uint32_t wave_max(uint32_t m) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) {
-    const uint32_t o = (uint32_t)__shfl_xor((int)m, off);
-    m = o > m ? o : m;
-  }
-  return m;
-}
-
-__device__ __forceinline__ float wave_sum(float s) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
-  return s;
 }
 
 }  // namespace q4

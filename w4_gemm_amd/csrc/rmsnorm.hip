@@ -45,8 +45,11 @@ __device__ __forceinline__ float row_rstd(float ss, int cols, float eps) {
   return ss <= 3.402823466e+38f ? 1.0f / __builtin_sqrtf(ss / (float)cols + eps) : u2f(0x7FC00000u);
 }
 
-// KIND: kRowInt8, kRowE4m3, or -1 for no output in 8 bits.
-template <int WAVES, int CH, int KIND, bool WF32>
+// KIND: kRowInt8, kRowE4m3, or -1 for no output in 8 bits.  PAST: rows are read and h
+// is written past the caches (kPastForward values and more: 16385 x 8192 in 143 us,
+// 6.6 TB/s, 164 without; 4096 x 8192, which they hold, 39 us and 42 with it).  The
+// codes are not: the product reads them next, and 8 bytes at a time they gain nothing.
+template <int WAVES, int CH, int KIND, bool WF32, bool PAST>
 __global__ void __launch_bounds__(64 * (WAVES < 4 ? 4 : WAVES))
 rmsnorm_kernel(const NormArgs p) {
   constexpr int kRows = WAVES < 4 ? 4 / WAVES : 1;
@@ -66,7 +69,7 @@ rmsnorm_kernel(const NormArgs p) {
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int k0 = (tid + 64 * WAVES * i) * 8;
-    v[i] = *reinterpret_cast<const uint4*>(x + (k0 < cols ? k0 : 0));
+    v[i] = load16<PAST>(x + (k0 < cols ? k0 : 0));
   }
   if (p.residual) {
     const uint16_t* res = p.residual + r * p.ldr;
@@ -74,7 +77,7 @@ rmsnorm_kernel(const NormArgs p) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int k0 = (tid + 64 * WAVES * i) * 8;
-      u[i] = *reinterpret_cast<const uint4*>(res + (k0 < cols ? k0 : 0));
+      u[i] = load16<PAST>(res + (k0 < cols ? k0 : 0));
     }
     uint16_t* h = p.h + r * p.ldh;
 #pragma unroll
@@ -86,7 +89,7 @@ rmsnorm_kernel(const NormArgs p) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) a[j] += b[j];
       v[i] = pack_bf16x8(a);
-      if (k0 < cols) *reinterpret_cast<uint4*>(h + k0) = v[i];
+      if (k0 < cols) store16<PAST>(h + k0, v[i]);
     }
   }
   float hw[CH][8];
@@ -107,8 +110,8 @@ rmsnorm_kernel(const NormArgs p) {
       if (KIND >= 0) most = max_bits8(hw[i], most);
     }
   }
-  ss = wave_sum(ss);
-  if (KIND >= 0) most = wave_max(most);
+  ss = lanes_sum(ss);
+  if (KIND >= 0) most = lanes_max_bits(most);
   if constexpr (WAVES > 1) {
     __shared__ float sum[WAVES];
     __shared__ uint32_t top[WAVES];
@@ -162,8 +165,10 @@ rmsnorm_kernel(const NormArgs p) {
 // mean(g n) = r sum(g h) / cols, so one reduction gives sum(h^2) and sum(g h)
 // together and nothing but h need be kept from the forward pass.  Workgroups
 // walk over rows with dw of their columns in registers; each writes its sum to
-// the workspace, and a second kernel adds those in order.
-template <int WAVES, int CH, bool WF32>
+// the workspace, and a second kernel adds those in order.  PAST: rows are read past
+// the caches (kPastBackward values and more: 16384 x 8192 in 182 us, 205 without;
+// 512 x 8192 in 19 us, 21 with it); dx, which is read next, is not written so.
+template <int WAVES, int CH, bool WF32, bool PAST>
 __global__ void __launch_bounds__(64 * (WAVES < 4 ? 4 : WAVES))
 rmsnorm_backward_kernel(const NormGradArgs p) {
   constexpr int kRows = WAVES < 4 ? 4 / WAVES : 1;
@@ -185,9 +190,9 @@ rmsnorm_backward_kernel(const NormGradArgs p) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int k0 = (tid + kThreads * i) * 8, at = k0 < cols ? k0 : 0;
-      vd[i] = *reinterpret_cast<const uint4*>(p.dy + r * p.lddy + at);
-      vh[i] = *reinterpret_cast<const uint4*>(p.h + r * p.ldh + at);
-      if (p.dh) vr[i] = *reinterpret_cast<const uint4*>(p.dh + r * p.lddh + at);
+      vd[i] = load16<PAST>(p.dy + r * p.lddy + at);
+      vh[i] = load16<PAST>(p.h + r * p.ldh + at);
+      if (p.dh) vr[i] = load16<PAST>(p.dh + r * p.lddh + at);
     }
     float ss = 0.0f, c = 0.0f;
 #pragma unroll
@@ -203,8 +208,8 @@ rmsnorm_backward_kernel(const NormGradArgs p) {
         }
       }
     }
-    ss = wave_sum(ss);
-    c = wave_sum(c);
+    ss = lanes_sum(ss);
+    c = lanes_sum(c);
     if constexpr (WAVES > 1) {
       // two sets in turn: a wave writes the next row's while others read this one's
       if ((tid & 63) == 0) {
@@ -266,35 +271,55 @@ rmsnorm_backward_kernel(const NormGradArgs p) {
   }
 }
 
-// dw[k] (+)= sum over the workgroups' sums: 64 columns by 16 slices per
-// workgroup, the slices' sums added in order.
+// dw[k] (+)= sum over the workgroups' sums: 32 columns by 32 slices per
+// workgroup, a slice's loads on the way together, the slices' sums added in order.
+constexpr int kGradBlocks = 512;
 __global__ void __launch_bounds__(1024)
 rmsnorm_weight_sum_kernel(const float* __restrict__ partial, int blocks, int cols, float* __restrict__ dw,
                           int accumulate) {
-  __shared__ float part[16][64];
-  const int k = blockIdx.x * 64 + (threadIdx.x & 63), slice = threadIdx.x >> 6;
+  __shared__ float part[32][33];
+  const int k = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
   float s = 0.0f;
-  if (k < cols)
-    for (int b = slice; b < blocks; b += 16) s += partial[(int64_t)b * cols + k];
-  part[slice][threadIdx.x & 63] = s;
+  if (k < cols) {
+#pragma unroll
+    for (int i = 0; i < kGradBlocks / 32; ++i) {
+      const int b = slice + 32 * i;
+      if (b < blocks) s += partial[(int64_t)b * cols + k];
+    }
+  }
+  part[slice][threadIdx.x & 31] = s;
   __syncthreads();
   if (slice == 0 && k < cols) {
 #pragma unroll
-    for (int q = 1; q < 16; ++q) s += part[q][threadIdx.x];
+    for (int q = 1; q < 32; ++q) s += part[q][threadIdx.x];
     dw[k] = accumulate ? dw[k] + s : s;
   }
 }
 
-constexpr int kGradBlocks = 512;
+constexpr int64_t kPastForward = (int64_t)48 << 20;    // values of a tensor
+constexpr int64_t kPastBackward = (int64_t)16 << 20;
+
+template <int WAVES, int CH, int KIND, bool WF32>
+void norm_as(const NormArgs& a, hipStream_t stream) {
+  constexpr int kRows = WAVES < 4 ? 4 / WAVES : 1;
+  const unsigned grid = (unsigned)((a.srows + kRows - 1) / kRows), threads = 64 * WAVES * kRows;
+  if (a.rows * a.cols >= kPastForward)
+    rmsnorm_kernel<WAVES, CH, KIND, WF32, true><<<grid, threads, 0, stream>>>(a);
+  else
+    rmsnorm_kernel<WAVES, CH, KIND, WF32, false><<<grid, threads, 0, stream>>>(a);
+}
+
+template <int WAVES, int CH, bool WF32>
+void norm_kind(const NormArgs& a, int kind, hipStream_t stream) {
+  if (kind == kRowInt8) norm_as<WAVES, CH, kRowInt8, WF32>(a, stream);
+  else if (kind == kRowE4m3) norm_as<WAVES, CH, kRowE4m3, WF32>(a, stream);
+  else norm_as<WAVES, CH, -1, WF32>(a, stream);
+}
 
 template <int WAVES, int CH>
 void norm(const NormArgs& a, int kind, hipStream_t stream) {
-  constexpr int kRows = WAVES < 4 ? 4 / WAVES : 1;
-  const unsigned grid = (unsigned)((a.srows + kRows - 1) / kRows), threads = 64 * WAVES * kRows;
-  auto kernel = kind == kRowInt8   ? (a.w_f32 ? rmsnorm_kernel<WAVES, CH, kRowInt8, true> : rmsnorm_kernel<WAVES, CH, kRowInt8, false>)
-                : kind == kRowE4m3 ? (a.w_f32 ? rmsnorm_kernel<WAVES, CH, kRowE4m3, true> : rmsnorm_kernel<WAVES, CH, kRowE4m3, false>)
-                                   : (a.w_f32 ? rmsnorm_kernel<WAVES, CH, -1, true> : rmsnorm_kernel<WAVES, CH, -1, false>);
-  kernel<<<grid, threads, 0, stream>>>(a);
+  if (a.w_f32) norm_kind<WAVES, CH, true>(a, kind, stream);
+  else norm_kind<WAVES, CH, false>(a, kind, stream);
 }
 
 int64_t grad_blocks(int64_t rows, int64_t cols) {
@@ -306,7 +331,9 @@ int64_t grad_blocks(int64_t rows, int64_t cols) {
 template <int WAVES, int CH>
 void norm_backward(const NormGradArgs& a, hipStream_t stream) {
   constexpr int kRows = WAVES < 4 ? 4 / WAVES : 1;
-  auto kernel = a.w_f32 ? rmsnorm_backward_kernel<WAVES, CH, true> : rmsnorm_backward_kernel<WAVES, CH, false>;
+  const bool past = a.rows * a.cols >= kPastBackward;
+  auto kernel = a.w_f32 ? (past ? rmsnorm_backward_kernel<WAVES, CH, true, true> : rmsnorm_backward_kernel<WAVES, CH, true, false>)
+                        : (past ? rmsnorm_backward_kernel<WAVES, CH, false, true> : rmsnorm_backward_kernel<WAVES, CH, false, false>);
   kernel<<<(unsigned)grad_blocks(a.rows, a.cols), 64 * WAVES * kRows, 0, stream>>>(a);
 }
 
@@ -343,7 +370,7 @@ hipError_t launch_rmsnorm_backward(const NormGradArgs& a, float* dweight, int ac
     if (e != hipSuccess) return e;
   }
   if (dweight)
-    rmsnorm_weight_sum_kernel<<<(unsigned)((a.cols + 63) / 64), 1024, 0, stream>>>(
+    rmsnorm_weight_sum_kernel<<<(unsigned)((a.cols + 31) / 32), 1024, 0, stream>>>(
         a.partial, a.rows > 0 ? (int)grad_blocks(a.rows, a.cols) : 0, a.cols, dweight, accumulate);
   return hipGetLastError();
 }
