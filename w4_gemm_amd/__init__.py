@@ -220,9 +220,11 @@ def _q4(q: "Q4Tensor", name: str):
     if not isinstance(q, Q4Tensor):
         raise ValueError(f"{name} must be a Q4Tensor")
     cb, sb = _sizes(q.fmt, q.layout, q.rows, q.cols)
-    for part, t, need in (("codes", q.codes, cb), ("scales", q.scales, sb)):
-        if not t.is_contiguous() or t.nbytes < need:
-            raise ValueError(f"{name}.{part} must be contiguous and hold {need} bytes")
+    codes, scales = q.codes, q.scales
+    if not codes.is_contiguous() or codes.nbytes < cb:
+        raise ValueError(f"{name}.codes must be contiguous and hold {cb} bytes")
+    if not scales.is_contiguous() or scales.nbytes < sb:
+        raise ValueError(f"{name}.scales must be contiguous and hold {sb} bytes")
     if q.fmt == NVFP4:
         if q.global_scale is None:
             raise ValueError(f"{name}.global_scale is required for NVFP4")
@@ -299,7 +301,7 @@ def q4_sizes(fmt, rows: int, cols: int, layout=LAYOUT_ROWS):
 def empty_q4(fmt, rows: int, cols: int, device="cuda", layout=LAYOUT_ROWS) -> Q4Tensor:
     """Allocate (with torch) the buffers of a quantized tensor."""
     f, lay = _fmt(fmt), _layout(layout)
-    cb, sb = q4_sizes(f, rows, cols, lay)
+    cb, sb = _sizes(f, lay, rows, cols)
     if f == FP8_ROW:
         codes = torch.empty((rows, cols) if lay == LAYOUT_ROWS else (cb,), dtype=torch.uint8,
                             device=device)

@@ -8,6 +8,7 @@ device, and nothing records itself for torch's differentiation.
 from __future__ import annotations
 
 import ctypes
+from array import array
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -20,9 +21,25 @@ def _norm_weight(weight: torch.Tensor, cols: int) -> int:
     """Checks a norm's weight; its dtype code."""
     if not isinstance(weight, torch.Tensor) or weight.dtype not in (BF16, F32):
         raise ValueError("weight must be a bf16 or float32 tensor")
-    if weight.dim() != 1 or weight.shape[0] != cols or not weight.is_contiguous():
+    if weight.shape != (cols,) or not weight.is_contiguous():
         raise ValueError(f"weight must be contiguous of shape ({cols},) (got {tuple(weight.shape)})")
     return 1 if weight.dtype is F32 else 0
+
+
+def _rows(t: Optional[torch.Tensor], name: str, rows: int, cols: int) -> int:
+    """Checks a bf16 matrix of at least `rows` rows of exactly `cols` columns
+    (None: no such argument); its leading dimension."""
+    if t is None:
+        return 0
+    if isinstance(t, torch.Tensor) and t.dtype is BF16:
+        shape = t.shape
+        if len(shape) == 2:     # the usual case, with few looks at the tensor
+            r, c = shape
+            step, unit = t.stride()
+            if r > 1 and r >= rows and c == cols and unit == 1 and step >= c:
+                return step
+    _matrix(t, name, BF16, rows, cols, exact_cols=True)
+    return _ld(t)
 
 
 def q4_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
@@ -32,17 +49,14 @@ def q4_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residua
     residual): (h, y, y_q).  y in bf16 [rows, cols] is written if it is given or
     y_q is not; y_q, if given, receives y in 8 bits (fp8_row or int8_row), ready
     for q4_gemm.  weight [cols] in bf16 or float32.  h may be x or residual."""
-    _matrix(x, "x", BF16, 0, 0)
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be a 2-D bf16 tensor")
     rows, cols = x.shape
+    ldx, ldr = _rows(x, "x", rows, cols), _rows(residual, "residual", rows, cols)
     wt = _norm_weight(weight, cols)
-    if residual is not None:
-        _matrix(residual, "residual", BF16, rows, cols, exact_cols=True)
-    if h is not None:
-        if residual is None:
-            raise ValueError("h is written only with a residual")
-        _matrix(h, "h", BF16, rows, cols, exact_cols=True)
-    if y is not None:
-        _matrix(y, "y", BF16, rows, cols, exact_cols=True)
+    if h is not None and residual is None:
+        raise ValueError("h is written only with a residual")
+    ldh, ldy = _rows(h, "h", rows, cols), _rows(y, "y", rows, cols)
     if y_q is not None:
         _q4(y_q, "y_q")
         if y_q.fmt not in (FP8_ROW, INT8_ROW):
@@ -53,14 +67,14 @@ def q4_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residua
                 ("y_q", y_q)) as (dev, s):
         if residual is not None and h is None:
             h = torch.empty(rows, cols, dtype=BF16, device=dev)
+            ldh = _ld(h)
         if y is None and y_q is None:
             y = torch.empty(rows, cols, dtype=BF16, device=dev)
+            ldy = _ld(y)
         if rows and cols:
-            d = y_q.c() if y_q is not None else None
-            _check(lib().q4_rmsnorm(_ptr(x), _ld(x), _ptr(residual), _ld(residual) if residual is not None else 0,
-                                    _ptr(weight), wt, eps, rows, cols, _ptr(h), _ld(h) if h is not None else 0,
-                                    _ptr(y), _ld(y) if y is not None else 0, ctypes.byref(d) if d else None, s),
-                   "q4_rmsnorm")
+            d = ctypes.byref(y_q.c()) if y_q is not None else None
+            _check(lib().q4_rmsnorm(x.data_ptr(), ldx, _ptr(residual), ldr, weight.data_ptr(), wt, eps, rows, cols,
+                                    _ptr(h), ldh, _ptr(y), ldy, d, s), "q4_rmsnorm")
     return x if residual is None else h, y, y_q
 
 
@@ -72,16 +86,14 @@ def q4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
     its own path) added, and for the weight: (dx bf16 [rows, cols], dweight
     float32 [cols]).  h as q4_rmsnorm returned it.  accumulate adds to dweight;
     weight_grad=False: none (None is returned).  dx may be dh or dy."""
-    _matrix(dy, "dy", BF16, 0, 0)
+    if not isinstance(dy, torch.Tensor) or dy.dim() != 2:
+        raise ValueError("dy must be a 2-D bf16 tensor")
     rows, cols = dy.shape
+    lddy = _rows(dy, "dy", rows, cols)
     wt = _norm_weight(weight, cols)
-    _matrix(h, "h", BF16, 0, cols, exact_cols=True)
+    ldh, lddh, lddx = _rows(h, "h", rows, cols), _rows(dh, "dh", rows, cols), _rows(dx, "dx", rows, cols)
     if h.shape[0] != rows:
         raise ValueError(f"h must have {rows} rows like dy (got {h.shape[0]})")
-    if dh is not None:
-        _matrix(dh, "dh", BF16, rows, cols, exact_cols=True)
-    if dx is not None:
-        _matrix(dx, "dx", BF16, rows, cols, exact_cols=True)
     if dweight is not None:
         if not weight_grad:
             raise ValueError("dweight given with weight_grad=False")
@@ -92,14 +104,15 @@ def q4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
                 ("dweight", dweight)) as (dev, s):
         if dx is None:
             dx = torch.empty(rows, cols, dtype=BF16, device=dev)
+            lddx = _ld(dx)
         ws, need = None, 0
         if weight_grad:
             if dweight is None:
                 dweight = torch.empty(cols, dtype=F32, device=dev)
             ws, need = _workspace("q4_rmsnorm_backward_workspace", dev, rows, cols)
-        _check(lib().q4_rmsnorm_backward(_ptr(dy), _ld(dy), _ptr(h), _ld(h), _ptr(weight), wt, eps, _ptr(dh),
-                                         _ld(dh) if dh is not None else 0, rows, cols, _ptr(dx), _ld(dx),
-                                         _ptr(dweight), int(accumulate), _ptr(ws), need, s), "q4_rmsnorm_backward")
+        _check(lib().q4_rmsnorm_backward(dy.data_ptr(), lddy, h.data_ptr(), ldh, weight.data_ptr(), wt, eps, _ptr(dh),
+                                         lddh, rows, cols, dx.data_ptr(), lddx, _ptr(dweight), int(accumulate),
+                                         _ptr(ws), need, s), "q4_rmsnorm_backward")
     return dx, dweight
 
 
@@ -161,26 +174,33 @@ def q4_moe_balance_backward(logits: torch.Tensor, slopes: torch.Tensor, mask: Op
     return dlogits
 
 
+_KINDS = {BF16: 0, F32: 1}
+
+
 def _tensors(grads: Sequence[torch.Tensor], name: str):
     """Checks gradients (contiguous, bf16 or float32, on one device) and lays
-    their pointers, sizes and types out for the library."""
-    n = len(grads)
-    ptrs, counts, dtypes = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)(), (ctypes.c_int32 * n)()
-    where = grads[0].device if n and isinstance(grads[0], torch.Tensor) else None
-    for i, t in enumerate(grads):
-        if not isinstance(t, torch.Tensor):
-            raise ValueError(f"{name}[{i}] must be a tensor")
-        dt = t.dtype
-        if dt is F32:
-            dtypes[i] = 1
-        elif dt is not BF16:
-            raise ValueError(f"{name}[{i}] must be bf16 or float32 (got {dt})")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}[{i}] must be contiguous")
-        if t.device != where:
-            raise ValueError(f"{name}[{i}] must be on {where} like the others (got {t.device})")
-        ptrs[i], counts[i] = t.data_ptr(), t.numel()
-    return ptrs, counts, dtypes
+    their pointers, sizes and types out for the library, as arrays."""
+    try:
+        fine = (all(map(torch.Tensor.is_contiguous, grads)) and len(set(map(torch.Tensor.get_device, grads))) == 1)
+        kinds = array("i", [_KINDS[t.dtype] for t in grads]) if fine else None
+    except (TypeError, KeyError):
+        fine = False
+    if not fine:    # which one, and why
+        for i, t in enumerate(grads):
+            if not isinstance(t, torch.Tensor):
+                raise ValueError(f"{name}[{i}] must be a tensor")
+            if t.dtype not in _KINDS:
+                raise ValueError(f"{name}[{i}] must be bf16 or float32 (got {t.dtype})")
+            if not t.is_contiguous():
+                raise ValueError(f"{name}[{i}] must be contiguous")
+            if t.device != grads[0].device:
+                raise ValueError(f"{name}[{i}] must be on {grads[0].device} like the others (got {t.device})")
+    return (array("Q", map(torch.Tensor.data_ptr, grads)), array("q", map(torch.Tensor.numel, grads)), kinds)
+
+
+def _at(a: Optional[array]):
+    """Address of an array's values (it has to outlive the call)."""
+    return None if a is None else a.buffer_info()[0]
 
 
 def q4_grad_norm(grads: Sequence[torch.Tensor], stream=None) -> torch.Tensor:
@@ -194,7 +214,8 @@ def q4_grad_norm(grads: Sequence[torch.Tensor], stream=None) -> torch.Tensor:
     with _place(stream, ("grads[0]", grads[0])) as (dev, s):
         norm = torch.empty((), dtype=F32, device=dev)
         ws, need = _workspace("q4_grad_workspace", dev, len(grads))
-        _check(lib().q4_grad_norm(len(grads), ptrs, counts, dtypes, _ptr(norm), _ptr(ws), need, s), "q4_grad_norm")
+        _check(lib().q4_grad_norm(len(grads), _at(ptrs), _at(counts), _at(dtypes), _ptr(norm), _ptr(ws), need, s),
+               "q4_grad_norm")
     return norm
 
 
@@ -214,9 +235,9 @@ def q4_grad_clip(grads: Sequence[torch.Tensor], max_norm: float, norm: Optional[
         if len(out) != len(grads):
             raise ValueError(f"out must hold {len(grads)} tensors like grads (got {len(out)})")
         outs, sizes, kinds = _tensors(out, "out")
-        for i in range(len(out)):
-            if sizes[i] != counts[i] or kinds[i] != dtypes[i]:
-                raise ValueError(f"out[{i}] must have the size and dtype of grads[{i}]")
+        if sizes != counts or kinds != dtypes:
+            i = next(i for i in range(len(out)) if sizes[i] != counts[i] or kinds[i] != dtypes[i])
+            raise ValueError(f"out[{i}] must have the size and dtype of grads[{i}]")
     if norm is not None:
         _vector(norm, "norm", F32, 1)
     with _place(stream, ("grads[0]", grads[0]), ("norm", norm), ("out[0]", out[0] if out else None)) as (dev, s):
@@ -224,6 +245,6 @@ def q4_grad_clip(grads: Sequence[torch.Tensor], max_norm: float, norm: Optional[
         if norm is None:
             made = torch.empty((), dtype=F32, device=dev)
             ws, need = _workspace("q4_grad_workspace", dev, len(grads))
-        _check(lib().q4_grad_clip(len(grads), ptrs, counts, dtypes, outs, _ptr(norm), max_norm, _ptr(made), _ptr(ws),
-                                  need, s), "q4_grad_clip")
+        _check(lib().q4_grad_clip(len(grads), _at(ptrs), _at(counts), _at(dtypes), _at(outs), _ptr(norm), max_norm,
+                                  _ptr(made), _ptr(ws), need, s), "q4_grad_clip")
     return made

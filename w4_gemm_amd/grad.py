@@ -62,27 +62,50 @@ class _There:
         return self.outer.__exit__(*exc)
 
 
+# the current device's index, without a check that the GPU was initialised (asked only with a GPU tensor in hand)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _one_device(args) -> int:
+    """Index of the GPU that all tensors of (name, tensor) pairs are on; -1 if
+    they are on none or on several."""
+    where = -2
+    for _, t in args:
+        if t is None:
+            continue
+        if isinstance(t, Q4Tensor):
+            i = t.codes.get_device()
+            if t.scales.get_device() != i or (t.global_scale is not None and t.global_scale.get_device() != i):
+                return -1
+        else:
+            i = t.get_device()
+        if i != where:
+            if where != -2:
+                return -1
+            where = i
+    return where
+
+
 def _place(stream, *args):
     """Checks that every (name, tensor) is on the GPU, all on one; `with` it the
     call is on that device and the stream it runs on, as (device, stream) ready
     for torch and for the library."""
-    where = -1
-    for name, t in args:
-        if t is None:
-            continue
-        i = t.get_device() if isinstance(t, torch.Tensor) else t.codes.get_device()
-        if where < 0:
-            where = i
-        if i < 0 or i != where or isinstance(t, Q4Tensor):
+    where = _one_device(args)
+    if where < 0:
+        for name, t in args:
+            if t is None:
+                continue
             for part, x in _parts(t):
                 if x is None:
                     continue
                 if not x.is_cuda:
                     raise ValueError(f"{name}{part} must be a GPU tensor (got device {x.device})")
+                if where < 0:
+                    where = x.get_device()
                 if x.get_device() != where:
                     raise ValueError(f"{name}{part} must be on cuda:{where} like the other tensors (got cuda:{x.get_device()})")
     if stream is None:
-        if where == torch.cuda.current_device():
+        if where == _current_device():
             return _Here(where, _raw_stream(where))
         return _There(where, None)
     if not isinstance(stream, torch.cuda.Stream):
