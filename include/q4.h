@@ -506,7 +506,7 @@ q4_status q4_moe_topk_backward(const float* logits, int64_t ld, int64_t T, int32
  * and its gradient is 0; one with a NaN or +inf makes the loss NaN and its own
  * gradient alone NaN.
  * logits [T][ld], dlogits [T][lddl] fp32, ids [T][k] int32, mask uint8 [T].
- * 1 <= E <= 1024, 1 <= k <= 32, T <= 2^26 - 4.
+ * 1 <= E <= 1024, 1 <= k <= 32, T <= 2^26 - 4, leading dimensions <= 2^27.
  */
 q4_status q4_moe_balance_workspace(int64_t T, int32_t E, size_t* bytes);
 q4_status q4_moe_balance(const float* logits, int64_t ld, int64_t T, int32_t E, int32_t k, const int32_t* topk_ids,

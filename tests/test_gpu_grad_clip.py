@@ -84,6 +84,20 @@ def test_large():
         assert ((a.double() - b.double() * by).abs() <= rel * b.double().abs() * by + 2.0 ** -133).all()
 
 
+def test_longer_than_the_caches():
+    """More bytes than are kept between the two passes, in tensors of both types with odd beginnings."""
+    buf = torch.randn(70_000_003, device="cuda")
+    g = [buf[3:69_999_990], torch.randn(9_000_001, device="cuda").to(BF16)[1:], buf[69_999_990:]]
+    keep = [t.clone() for t in g]
+    norm = torch.sqrt(sum(t.double().square().sum() for t in g)).item()
+    got = q4.q4_grad_clip(g, 2.0)
+    assert abs(got.item() - norm) <= 2.0 ** -22 * norm and torch.equal(buf[:3], buf[:3].clone())
+    by = 2.0 / (norm + 1e-6)
+    for a, b in zip(g, keep):
+        rel = 2.0 ** -22 if a.dtype is F32 else 2.0 ** -8 + 2.0 ** -22
+        assert ((a.double() - b.double() * by).abs() <= rel * b.double().abs() * by + 2.0 ** -133).all()
+
+
 def test_past_32_bits():
     """A tensor of more than 2^31 values: its last ones are counted and scaled."""
     n = (1 << 31) + 40

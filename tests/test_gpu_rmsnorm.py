@@ -275,3 +275,28 @@ def test_feeds_the_products():
         wd = n64(q4.q4_dequant(W, torch.empty(N, K, dtype=F32, device="cuda")))
         ref, size = ad @ wd.T, np.abs(ad) @ np.abs(wd).T
         near(C, ref, 2.0 ** -8, 2.0 ** -16 * size, fmt)
+
+
+@pytest.mark.parametrize("rows,cols", [(6200, 8192), (50000, 1008)])
+def test_longer_than_the_caches(rows, cols):
+    """Sizes at which rows are read and written past the caches: the same values as for the rows alone."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x, res, dy, dh = (torch.randn(rows, cols, device="cuda", generator=g).to(BF16) for _ in range(4))
+    w = torch.rand(cols, device="cuda", generator=g).to(BF16)
+    pick = [0, 1, rows // 2, rows - 2, rows - 1]
+    for fmt in ("int8_row", "fp8_row"):
+        q, y = q4.empty_q4(fmt, rows, cols), torch.empty_like(x)
+        h, _, _ = q4.q4_rmsnorm(x, w, EPS, residual=res, y=y, y_q=q)
+        small = q4.empty_q4(fmt, len(pick), cols)
+        hs, ys, _ = q4.q4_rmsnorm(x[pick], w, EPS, residual=res[pick], y=torch.empty_like(x[pick]), y_q=small)
+        assert torch.equal(h[pick], hs) and torch.equal(y[pick], ys)
+        assert torch.equal(q.codes[pick], small.codes) and torch.equal(q.scales[pick], small.scales)
+    assert torch.equal(h, (x.float() + res.float()).to(BF16))
+    dx, dw = q4.q4_rmsnorm_backward(dy, h, w, EPS, dh=dh)
+    assert torch.equal(dx[pick], q4.q4_rmsnorm_backward(dy[pick], h[pick], w, EPS, dh=dh[pick])[0])
+    ref, size = torch.zeros(cols, dtype=torch.float64, device="cuda"), torch.zeros(cols, dtype=torch.float64, device="cuda")
+    for a, b in zip(dy.split(4096), h.split(4096)):
+        n = b.double() * torch.rsqrt(b.double().square().mean(1, keepdim=True) + EPS) * a.double()
+        ref, size = ref + n.sum(0), size + n.abs().sum(0)
+    # sums of at most 98 rows one behind the other, then of 16 and 32 parts: below 2^-17 of the magnitudes
+    assert ((dw.double() - ref).abs() <= 2.0 ** -16 * size).all()

@@ -23,6 +23,7 @@ constexpr int64_t kMaxGradCount = (int64_t)1 << 44;   // sizes in bytes stay far
 constexpr int64_t kMaxNormCols = 32768;               // a row in the registers of 16 waves
 constexpr int64_t kMaxIntN = (int64_t)1 << 27;        // 512 threads per 32 columns: below 2^32 threads
 constexpr int64_t kMaxIntK = (int64_t)1 << 17;        // 2^14 K < 2^31: sums of products of two bytes stay exact
+constexpr int64_t kMaxBalanceLd = (int64_t)1 << 27;   // three rows on in 32 bits of values
 constexpr int64_t kMaxTopkTokens = ((int64_t)1 << 26) - 4;  // a wave per token, four a workgroup: below 2^32 threads
 
 int block_of(int fmt) {
@@ -675,13 +676,14 @@ q4_status q4_moe_balance(const float* logits, int64_t ld, int64_t T, int32_t E, 
   if (k < 1 || k > 32 || T * k >= kMaxDim) return Q4_ERR_SHAPE;
   if (!loss || !counts || !slopes || (T > 0 && (!logits || !topk_ids)) || (need && !workspace)) return Q4_ERR_NULL;
   if (T > 0 && ld < E) return Q4_ERR_SHAPE;
+  if (T > 1 && ld > kMaxBalanceLd) return Q4_ERR_SHAPE;
   if (workspace_bytes < need) return Q4_ERR_SHAPE;
   if (!aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(loss, 4) || !aligned(counts, 4) ||
       !aligned(slopes, 4) || (need && !aligned(workspace, 16)))
     return Q4_ERR_ALIGN;
   q4::BalanceArgs a{};
   a.logits = logits;
-  a.ld = ld;
+  a.ld = T > 1 ? ld : (E + 3) / 4 * 4;  // (a single row's stride is never used)
   a.T = T;
   a.E = E;
   a.k = k;
@@ -700,18 +702,18 @@ q4_status q4_moe_balance_backward(const float* logits, int64_t ld, int64_t T, in
   if (T < 0 || T > kMaxTopkTokens || E < 1 || E > 1024) return Q4_ERR_SHAPE;
   if (T == 0) return Q4_OK;
   if (!logits || !slopes || !dlogits) return Q4_ERR_NULL;
-  if (ld < E || lddl < E) return Q4_ERR_SHAPE;
+  if (ld < E || lddl < E || (T > 1 && (ld > kMaxBalanceLd || lddl > kMaxBalanceLd))) return Q4_ERR_SHAPE;
   if (!aligned(logits, 4) || !aligned(slopes, 4) || !aligned(dloss, 4) || !aligned(dlogits, 4)) return Q4_ERR_ALIGN;
   q4::BalanceGradArgs a{};
   a.logits = logits;
-  a.ld = ld;
+  a.ld = T > 1 ? ld : (E + 3) / 4 * 4;
   a.T = T;
   a.E = E;
   a.mask = mask;
   a.slopes = slopes;
   a.dloss = dloss;
   a.dlogits = dlogits;
-  a.lddl = lddl;
+  a.lddl = T > 1 ? lddl : (E + 3) / 4 * 4;
   a.accumulate = accumulate;
   return hip_status(q4::launch_moe_balance_backward(a, as_stream(stream)));
 }

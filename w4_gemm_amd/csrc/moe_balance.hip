@@ -33,43 +33,64 @@ __host__ __device__ __forceinline__ int padded(int E) { return (E + 3) & ~3; }
 template <int LPT>
 __device__ __forceinline__ int expert_of(int sub, int i) { return 4 * LPT * (i >> 2) + 4 * sub + (i & 3); }
 
-// WIDE: E, the leading dimension and the address allow loads of 16 bytes.  `there`:
-// the token exists.  (A masked token's logits are read all the same, so that they
-// need not wait for its mask, and are replaced behind it.)
+// What lane `lane` reads of a token: offsets from the first token of its wave (the
+// same for every turn, so that a load's address is a scalar and one of these), at a
+// valid place also where the lane has nothing to read.
 template <int LPT, int PER, bool WIDE>
-__device__ __forceinline__ void load_logits(const float* row, int sub, int E, bool there, float (&v)[PER]) {
+struct Lane {
+  uint32_t at[WIDE ? PER / 4 : PER];
+  bool has[WIDE ? PER / 4 : PER];
+  __device__ __forceinline__ Lane(int lane, int E, int64_t ld) {
 #pragma unroll
-  for (int q = 0; q < PER / 4; ++q) {
-    const int e = expert_of<LPT>(sub, 4 * q);
-    if constexpr (WIDE) {
-      float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (there && e < E) f = *reinterpret_cast<const float4*>(row + e);
-      v[4 * q] = f.x;
-      v[4 * q + 1] = f.y;
-      v[4 * q + 2] = f.z;
-      v[4 * q + 3] = f.w;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[4 * q + j] = there && e + j < E ? row[e + j] : -INFINITY;
+    for (int i = 0; i < (WIDE ? PER / 4 : PER); ++i) {
+      const int e = expert_of<LPT>(lane % LPT, WIDE ? 4 * i : i);
+      has[i] = e < E;
+      at[i] = (uint32_t)(lane / LPT) * (uint32_t)ld + (uint32_t)(has[i] ? e : 0);
     }
   }
-}
-
-// Softmax of a token's logits (-inf behind the last one); all zeros where every
-// logit is -inf and for a token that does not count, NaN where one is NaN (the sum
-// carries it: a maximum passes over NaN).
-template <int LPT, int PER>
-__device__ __forceinline__ void softmax(float (&v)[PER], bool here) {
+  // (row: of the wave's first token)
+  __device__ __forceinline__ void load(const float* row, float (&v)[PER]) const {
+    if constexpr (WIDE) {
 #pragma unroll
-  for (int i = 0; i < PER; ++i) v[i] = here ? v[i] : -INFINITY;
+      for (int q = 0; q < PER / 4; ++q) {
+        const float4 f = *reinterpret_cast<const float4*>(row + at[q]);
+        v[4 * q] = f.x;
+        v[4 * q + 1] = f.y;
+        v[4 * q + 2] = f.z;
+        v[4 * q + 3] = f.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) v[i] = row[at[i]];
+    }
+  }
+  // -inf for what is no expert of a token that counts
+  __device__ __forceinline__ void keep(float (&v)[PER], bool here) const {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) v[i] = here && has[WIDE ? i / 4 : i] ? v[i] : -INFINITY;
+  }
+};
+
+// The greater of two, in one instruction (fmaxf first makes a quiet NaN of each
+// loaded value); what it makes of a NaN does not matter here.
+__device__ __forceinline__ float greater(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, INFINITY); }
+struct GreaterOp {
+  __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const {
+    return __builtin_bit_cast(uint32_t, greater(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)));
+  }
+};
+
+// Exponentials of a token's logits, v[e] = exp(l[e] - max), and the reciprocal of
+// their sum: p[e] = v[e] * by.  by is 0 where every logit is -inf; NaN where one is
+// NaN: its exponential and so the sum are.  exp(d) as 2^(d log2 e) in one
+// instruction, within a few 2^-24 of it times 1 + |d|.
+template <int LPT, int PER>
+__device__ __forceinline__ float exponentials(float (&v)[PER]) {
   float m = v[0];
 #pragma unroll
-  for (int i = 1; i < PER; ++i) m = fmaxf(m, v[i]);
-  m = lanes_max<LPT>(m);
+  for (int i = 1; i < PER; ++i) m = greater(m, v[i]);
+  m = __builtin_bit_cast(float, reduce_lanes<LPT>(__builtin_bit_cast(uint32_t, m), GreaterOp()));
   const float from = m == -INFINITY ? 0.0f : m;
-  // exp(d) as 2^(d log2 e) in one instruction (within a few 2^-24 of it times 1 + |d|;
-  // expf's further steps and a division made 22.6 us of the 17.7 that 65537 tokens of
-  // 256 experts take)
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
@@ -77,9 +98,7 @@ __device__ __forceinline__ void softmax(float (&v)[PER], bool here) {
     s += v[i];
   }
   s = lanes_sum<LPT>(s);
-  const float by = s == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(s);   // (within 1 ulp; 1 <= s <= 1024, or NaN)
-#pragma unroll
-  for (int i = 0; i < PER; ++i) v[i] *= by;
+  return s == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(s);   // (within 1 ulp; 1 <= s <= 1024, or NaN)
 }
 
 // slope and loss's part of an expert with c choices and probabilities p among n
@@ -103,34 +122,18 @@ __device__ __forceinline__ double block_loss(double l, double (&part)[kWaves]) {
   return l;
 }
 
-// What a lane needs of a token.
-template <int LPT, int PER, int IDS>
-struct Turn {
-  float v[PER];
-  uint32_t id[IDS];
-  uint8_t mask;
-  bool there;
-  template <bool WIDE>
-  __device__ __forceinline__ void load(const BalanceArgs& a, int64_t t, int sub) {
-    there = t < a.T;
-    mask = 1;
-    if (there && a.mask) mask = a.mask[t];
-    load_logits<LPT, PER, WIDE>(a.logits + t * a.ld, sub, a.E, there, v);
-#pragma unroll
-    for (int j = 0; j < IDS; ++j)
-      id[j] = there && sub + LPT * j < a.k ? (uint32_t)a.ids[t * a.k + sub + LPT * j] : ~0u;
-  }
-};
-
-// ONE: a single workgroup, which finishes by itself.
+// ONE: a single workgroup, which finishes by itself.  Bound by its VALU instructions,
+// 75 a token in 60% of its cycles, and by the loads of its first turns: 65537 tokens
+// of 256 experts in 16.7 us, 4.1 TB/s (eight turns together: 18 us).
 template <int LPT, int PER, bool WIDE, bool ONE>
 __global__ void __launch_bounds__(kThreads)
 moe_balance_kernel(const BalanceArgs a) {
   constexpr int kTokens = 64 / LPT;          // of a wave side by side
   constexpr int kTurns = PER == 4 ? 4 : 1;   // and one behind the other with their loads on the way together
   constexpr int kIds = LPT == 16 ? 2 : 1;    // choices of a lane (k <= 32)
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane % LPT;
-  const int E = a.E;
+  const int lane = threadIdx.x & 63, sub = lane % LPT;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int E = a.E, k = a.k;
   __shared__ uint32_t count[1024];
   __shared__ uint32_t tokens;
   __shared__ double part[kWaves];
@@ -138,35 +141,62 @@ moe_balance_kernel(const BalanceArgs a) {
   for (int e = threadIdx.x; e < E; e += kThreads) count[e] = 0u;
   if (threadIdx.x == 0) tokens = 0u;
   __syncthreads();
+  const Lane<LPT, PER, WIDE> mine(lane, E, a.ld);
+  uint32_t id_at[kIds];
+#pragma unroll
+  for (int j = 0; j < kIds; ++j)
+    id_at[j] = (uint32_t)(lane / LPT * k + (sub + LPT * j < k ? sub + LPT * j : 0));
   float sum[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) sum[i] = 0.0f;
-  uint32_t mine = 0;
-  const int64_t step = (int64_t)gridDim.x * kWaves * kTokens;
-  Turn<LPT, PER, kIds> now[kTurns], next[kTurns];
-  auto load = [&](Turn<LPT, PER, kIds> (&g)[kTurns], int64_t t0) {
+  uint32_t seen = 0;
+  auto use = [&](float (&v)[PER], const uint32_t (&id)[kIds], bool here) {
 #pragma unroll
-    for (int u = 0; u < kTurns; ++u) g[u].template load<WIDE>(a, t0 + u * step + lane / LPT, sub);
+    for (int j = 0; j < kIds; ++j)
+      if (here && sub + LPT * j < k && id[j] < (uint32_t)E) atomicAdd(&count[id[j]], 1u);
+    seen += here;
+    mine.keep(v, here);
+    const float by = exponentials<LPT, PER>(v);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) sum[i] = __builtin_fmaf(v[i], by, sum[i]);
   };
-  int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * kTokens;
-  if (t0 < a.T) load(next, t0);
-  for (; t0 < a.T; t0 += step * kTurns) {
-#pragma unroll
-    for (int u = 0; u < kTurns; ++u) now[u] = next[u];
-    if (t0 + step * kTurns < a.T) load(next, t0 + step * kTurns);   // on the way while these are worked on
+  const int T = (int)a.T;                    // (below 2^26)
+  const int step = (int)gridDim.x * kWaves * kTokens;
+  int t0 = ((int)blockIdx.x * kWaves + wave) * kTokens;
+  for (; t0 + (kTurns - 1) * step + kTokens <= T; t0 += kTurns * step) {
+    float v[kTurns][PER];
+    uint32_t id[kTurns][kIds];
+    uint8_t mask[kTurns];
 #pragma unroll
     for (int u = 0; u < kTurns; ++u) {
-      const bool here = now[u].there && now[u].mask != 0;
+      const int64_t t = t0 + u * step;
+      mine.load(a.logits + t * a.ld, v[u]);
+      mask[u] = a.mask ? a.mask[t + lane / LPT] : 1;
 #pragma unroll
-      for (int j = 0; j < kIds; ++j)
-        if (here && now[u].id[j] < (uint32_t)E) atomicAdd(&count[now[u].id[j]], 1u);
-      if (here && sub == 0) ++mine;
-      softmax<LPT, PER>(now[u].v, here);
-#pragma unroll
-      for (int i = 0; i < PER; ++i) sum[i] += now[u].v[i];
+      for (int j = 0; j < kIds; ++j) id[u][j] = (uint32_t)a.ids[t * k + id_at[j]];
     }
+#pragma unroll
+    for (int u = 0; u < kTurns; ++u) use(v[u], id[u], mask[u] != 0);
   }
-  if (mine) atomicAdd(&tokens, mine);
+  for (; t0 < T; t0 += step) {               // the last turns, one at a time
+    const int64_t t = t0;
+    const bool there = t0 + lane / LPT < T;
+    float v[PER];
+    uint32_t id[kIds];
+    uint8_t mask = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) v[i] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kIds; ++j) id[j] = ~0u;
+    if (there) {
+      mine.load(a.logits + t * a.ld, v);
+      mask = a.mask ? a.mask[t + lane / LPT] : 1;
+#pragma unroll
+      for (int j = 0; j < kIds; ++j) id[j] = (uint32_t)a.ids[t * k + id_at[j]];
+    }
+    use(v, id, mask != 0);
+  }
+  if (seen && sub == 0) atomicAdd(&tokens, seen);
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
 #pragma unroll
@@ -203,7 +233,8 @@ moe_balance_kernel(const BalanceArgs a) {
 // The workgroups' sums, added in order: a workgroup per 64 experts, in it a thread
 // per four of them and 64th of the sums, then 16 threads per expert.  The last
 // workgroup to end (the ticket was cleared by the first kernel) adds their parts
-// of the loss, in their order.
+// of the loss, in their order.  256 workgroups' sums of 256 experts: 8 us, latency
+// (10 us in a single workgroup).
 constexpr int kFinishExperts = 64;
 constexpr int kFinishMost = 1024 / kFinishExperts;   // workgroups
 __global__ void __launch_bounds__(kThreads)
@@ -275,51 +306,70 @@ moe_balance_finish_kernel(const BalanceArgs a, int blocks) {
   *a.loss = (float)l;
 }
 
+// The gradient: the same softmax again, from the logits alone.  65537 tokens of 256
+// experts in 21.8 us, 6.2 TB/s: bound by HBM.
 template <int LPT, int PER, bool WIDE>
 __global__ void __launch_bounds__(kBackThreads)
 moe_balance_backward_kernel(const BalanceGradArgs a) {
   constexpr int kTokens = 64 / LPT;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane % LPT;
+  const int lane = threadIdx.x & 63, sub = lane % LPT;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int E = a.E;
   const float dloss = a.dloss ? *a.dloss : 1.0f;
+  const Lane<LPT, PER, WIDE> mine(lane, E, a.ld), out(lane, E, a.lddl);
   float slope[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = expert_of<LPT>(sub, i);
     slope[i] = e < E ? a.slopes[e] : 0.0f;
   }
-  const int64_t step = (int64_t)gridDim.x * kBackWaves * kTokens;
-  for (int64_t t0 = ((int64_t)blockIdx.x * kBackWaves + wave) * kTokens; t0 < a.T; t0 += step) {
-    const int64_t t = t0 + lane / LPT;
-    const bool here = t < a.T && (!a.mask || a.mask[t] != 0);
+  const int T = (int)a.T, step = (int)gridDim.x * kBackWaves * kTokens;
+  for (int t0 = ((int)blockIdx.x * kBackWaves + wave) * kTokens; t0 < T; t0 += step) {
+    const int64_t t = t0;
+    const bool there = t0 + lane / LPT < T;
     float v[PER];
-    load_logits<LPT, PER, WIDE>(a.logits + t * a.ld, sub, E, t < a.T, v);
-    softmax<LPT, PER>(v, here);
+    uint8_t mask = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) v[i] = 0.0f;
+    if (there) {
+      mine.load(a.logits + t * a.ld, v);
+      mask = a.mask ? a.mask[t + lane / LPT] : 1;
+    }
+    const bool here = mask != 0;
+    mine.keep(v, here);
+    const float by = exponentials<LPT, PER>(v);
     float c = 0.0f;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) c = __builtin_fmaf(v[i], slope[i], c);
+    for (int i = 0; i < PER; ++i) {
+      v[i] *= by;
+      c = __builtin_fmaf(v[i], slope[i], c);
+    }
     c = lanes_sum<LPT>(c);
-    if (t >= a.T || (a.accumulate && !here)) continue;
+    if (!there || (a.accumulate && !here)) continue;
+    // (not here: v and c are 0)
 #pragma unroll
-    for (int i = 0; i < PER; ++i) v[i] = here ? dloss * (v[i] * (slope[i] - c)) : 0.0f;
+    for (int i = 0; i < PER; ++i) v[i] = dloss * (v[i] * (slope[i] - c));
+    if (!here) {   // (not NaN or inf times 0)
+#pragma unroll
+      for (int i = 0; i < PER; ++i) v[i] = 0.0f;
+    }
     float* row = a.dlogits + t * a.lddl;
+    if constexpr (WIDE) {
 #pragma unroll
-    for (int q = 0; q < PER / 4; ++q) {
-      const int e = expert_of<LPT>(sub, 4 * q);
-      if constexpr (WIDE) {
-        if (e >= E) continue;
-        float4* o = reinterpret_cast<float4*>(row + e);
+      for (int q = 0; q < PER / 4; ++q) {
+        if (!out.has[q]) continue;
+        float4* o = reinterpret_cast<float4*>(row + out.at[q]);
         float4 f = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
         if (a.accumulate) {
           const float4 b = *o;
           f = make_float4(b.x + f.x, b.y + f.y, b.z + f.z, b.w + f.w);
         }
         *o = f;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (e + j < E) row[e + j] = a.accumulate ? row[e + j] + v[4 * q + j] : v[4 * q + j];
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (out.has[i]) row[out.at[i]] = a.accumulate ? row[out.at[i]] + v[i] : v[i];
     }
   }
 }
