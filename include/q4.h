@@ -665,6 +665,14 @@ q4_status q4_wgrad_plan(int64_t P, int32_t E, int64_t N, int64_t K, int a_is_bf1
                         int32_t* parts);
 
 /*
+ * The same of the W8A8 product: the block of C that a workgroup makes and how many
+ * workgroups there are (0, 0 and 0 where nothing is launched).  Up to 256 of them
+ * take a variant of their kind with more on the way.
+ */
+q4_status q4_w8a8_plan(int64_t M, int64_t N, int64_t K, int32_t* block_rows, int32_t* block_cols,
+                       int64_t* workgroups);
+
+/*
  * Measurement helper, not a step of the method: reads `bytes` of device
  * memory at src with a plain streaming kernel (16-byte non-temporal loads,
  * each wave 8 KB in flight) and discards the data.  Decode GEMVs are bound

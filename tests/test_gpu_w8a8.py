@@ -91,11 +91,14 @@ SHAPES = [(1, 16, 128), (1, 1, 128), (2, 17, 256), (16, 64, 384), (17, 96, 512),
           (65, 257, 1152), (127, 1000, 512), (128, 128, 128), (130, 512, 2048), (205, 1016, 896), (256, 256, 4096),
           (257, 264, 1280), (300, 1, 256), (512, 768, 1024), (1, 4096, 8192), (8, 2048, 7168), (48, 7168, 2048),
           (1000, 1000, 1024),
-          # every kind of block, with one workgroup per CU and with two: 16 x 32, 32 x 64, 64 x 64, 128 x 64, 128 x 128,
-          # 256 x 256 (ragged in both directions, the shortest and odd numbers of stages)
+          # every kind of block, with one workgroup per CU and with two: 16 x 32, 32 x 32, 48 x 32, 32 x 64, 64 x 64,
+          # 128 x 64, 128 x 128, 256 x 256 (ragged in both directions, the shortest and odd numbers of stages)
+          (9, 8000, 2176), (1, 2048, 7168), (30, 8190, 1152), (125, 2040, 3200), (45, 8100, 2176), (40, 8192, 128),
+          (62, 8170, 1664), (64, 8192, 128), (121, 8150, 896), (250, 8192, 128),
           (5, 8199, 640), (3, 16400, 128), (31, 8200, 384), (20, 24000, 256), (60, 20000, 128), (60, 30000, 384),
           (250, 8100, 1152), (500, 8192, 640), (511, 8070, 2304), (1020, 8150, 1152), (2040, 8190, 128),
-          (2040, 8190, 1408), (4090, 1020, 4224)]
+          (2040, 8190, 1408), (4090, 1020, 4224),
+          (24, 28000, 640), (100, 9000, 2560), (511, 8180, 1024), (3620, 6700, 1280)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)

@@ -85,3 +85,32 @@ def test_binding_checks():
         q4.q4_gemm(A, W, C)
     with pytest.raises(ValueError, match="hold"):
         q4.q4_gemm(q4.Q4Tensor(q4.INT8_ROW, 4, 256, A.codes[:3], A.scales), W, C)
+
+
+def test_plan():
+    L = q4.lib()
+    a, b, c = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int64()
+    ref = [ctypes.byref(v) for v in (a, b, c)]
+    assert L.q4_w8a8_plan(1, 1, 128, None, *ref[1:]) == NULL
+    for M, N, K in ((-1, 1, 128), (1, -1, 128), (1, 1 << 27, 128), (1, 1, 64), (1, 1, 1 << 17), (65535 * 64 + 1, 1, 128)):
+        assert L.q4_w8a8_plan(M, N, K, *ref) == SHAPE
+    assert q4.q4_w8a8_plan(0, 5, 128) == (0, 0, 0) == q4.q4_w8a8_plan(5, 0, 128)
+    # the smallest and the largest, and a launch that stays below 2^32 threads at the limits
+    assert q4.q4_w8a8_plan(1, 1, 128)[2] == 1
+    assert q4.q4_w8a8_plan(4096, 8192, 8192) == (256, 256, 512)
+    for M in (1, 16, 17, 33, 64, 65, 128, 129, 160, 200, 256):
+        assert q4.q4_w8a8_plan(M, (1 << 27) - 1, 128)[2] < 1 << 23
+    assert q4.q4_w8a8_plan(65535 * 64, 1, 128)[2] < 1 << 22
+
+
+def test_the_gpu_tests_reach_every_kind():
+    """Every block with up to 256 workgroups and with more is among the sizes that the GPU tests run."""
+    from test_gpu_w8a8 import SHAPES
+    kinds = set()
+    for M, N, K in SHAPES:
+        r, c, n = q4.q4_w8a8_plan(M, N, K)
+        kinds.add((r, c, n <= 256))
+    blocks = [(16, 32), (32, 32), (48, 32), (32, 64), (64, 64), (128, 64), (128, 128), (256, 256)]
+    # (48 x 32 and 32 x 32 have one variant)
+    want = {(r, c, few) for r, c in blocks for few in (True, False)} - {(48, 32, False), (32, 32, False)}
+    assert kinds >= want, want - kinds

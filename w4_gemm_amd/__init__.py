@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -63,6 +64,8 @@ class _Q4TensorC(ctypes.Structure):
     ]
 
 
+_PACK = struct.Struct("=iiqqQQQ").pack    # the fields of _Q4TensorC
+
 _LIB = None
 
 
@@ -74,7 +77,7 @@ def _lib_handle():
             _build.build()
         L = ctypes.CDLL(LIB_PATH)
         i64, vp, i32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32
-        P = ctypes.POINTER(_Q4TensorC)
+        P = vp      # a descriptor: byref of a _Q4TensorC, or its bytes
         sz, SZ, I32P = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(i32)
         sig = {
             "q4_version": ([], ctypes.c_int),
@@ -114,6 +117,7 @@ def _lib_handle():
                               ctypes.c_int),
             "q4_grouped_gemm_wgrad": ([vp, i64, vp, i64, P, i64, vp, vp, i32, i64, i64, i64, vp, ctypes.c_int, i64,
                                        ctypes.c_int, vp, sz, vp], ctypes.c_int),
+            "q4_w8a8_plan": ([i64, i64, i64, I32P, I32P, ctypes.POINTER(i64)], ctypes.c_int),
             "q4_rmsnorm": ([vp, i64, vp, i64, vp, ctypes.c_int, ctypes.c_float, i64, i64, vp, i64, vp, i64, P, vp],
                            ctypes.c_int),
             "q4_rmsnorm_backward_workspace": ([i64, i64, SZ], ctypes.c_int),
@@ -271,6 +275,12 @@ class Q4Tensor:
                           self.scales.data_ptr() if self.scales.numel() else None,
                           None if self.global_scale is None else self.global_scale.data_ptr())
 
+    def packed(self) -> bytes:
+        """What c() holds, as bytes (made in half the time)."""
+        gs = self.global_scale
+        return _PACK(self.fmt, self.layout, self.rows, self.cols, self.codes.data_ptr(), self.scales.data_ptr(),
+                     0 if gs is None else gs.data_ptr())
+
     @property
     def nbytes(self) -> int:
         n = self.codes.numel() + self.scales.numel() * self.scales.element_size()
@@ -328,13 +338,17 @@ def empty_q4(fmt, rows: int, cols: int, device="cuda", layout=LAYOUT_ROWS) -> Q4
 def q4_quantize(src: torch.Tensor, dst: Q4Tensor, nv_global_in: Optional[torch.Tensor] = None,
                 stream=None) -> Q4Tensor:
     """Quantize bf16 src [rows, >= cols] (row stride src.stride(0)) into dst."""
-    _matrix(src, "src", torch.bfloat16, dst.rows, dst.cols)
     _q4(dst, "dst")
+    return _quantize(src, dst, nv_global_in, stream)
+
+
+def _quantize(src, dst, nv_global_in, stream) -> Q4Tensor:
+    """q4_quantize into a tensor whose buffers are as they should be."""
+    _matrix(src, "src", torch.bfloat16, dst.rows, dst.cols)
     if nv_global_in is not None:
         _vector(nv_global_in, "nv_global_in", torch.float32, 1)
     with _place(stream, ("src", src), ("dst", dst), ("nv_global_in", nv_global_in)) as (_, s):
-        desc = dst.c()
-        _check(lib().q4_quantize(_ptr(src), src.stride(0), ctypes.byref(desc), _ptr(nv_global_in), s), "q4_quantize")
+        _check(lib().q4_quantize(src.data_ptr(), src.stride(0), dst.packed(), _ptr(nv_global_in), s), "q4_quantize")
     return dst
 
 
@@ -343,7 +357,7 @@ def quantize(src: torch.Tensor, fmt, nv_global_in: Optional[torch.Tensor] = None
     """Allocate a Q4Tensor on src's device and quantize src into it."""
     dst = empty_q4(fmt, src.shape[0], src.shape[1], device=src.get_device() if src.is_cuda else src.device,
                    layout=layout)
-    return q4_quantize(src, dst, nv_global_in, stream)
+    return _quantize(src, dst, nv_global_in, stream)
 
 
 def q4_relayout(src: Q4Tensor, dst: Q4Tensor, stream=None) -> Q4Tensor:
@@ -377,8 +391,7 @@ def q4_dequant(src: Q4Tensor, dst: torch.Tensor, stream=None) -> torch.Tensor:
     _matrix(dst, "dst", dst.dtype, src.rows, src.cols)
     _q4(src, "src")
     with _place(stream, ("src", src), ("dst", dst)) as (_, s):
-        desc = src.c()
-        _check(lib().q4_dequant(ctypes.byref(desc), _ptr(dst), dt, dst.stride(0), s), "q4_dequant")
+        _check(lib().q4_dequant(src.packed(), dst.data_ptr(), dt, dst.stride(0), s), "q4_dequant")
     return dst
 
 
@@ -409,12 +422,10 @@ def q4_gemm(A, W: Q4Tensor, C: torch.Tensor, stream=None) -> torch.Tensor:
         M = A.shape[0]
     _matrix(C, "C", torch.bfloat16, M, W.rows)
     with _place(stream, ("W", W), ("A", A), ("C", C)) as (_, s):
-        wd = W.c()
         if isinstance(A, Q4Tensor):
-            ad = A.c()
-            st = lib().q4_gemm(A.rows, None, 0, ctypes.byref(ad), ctypes.byref(wd), _ptr(C), C.stride(0), s)
+            st = lib().q4_gemm(A.rows, None, 0, A.packed(), W.packed(), C.data_ptr(), C.stride(0), s)
         else:
-            st = lib().q4_gemm(A.shape[0], _ptr(A), A.stride(0), None, ctypes.byref(wd), _ptr(C), C.stride(0), s)
+            st = lib().q4_gemm(A.shape[0], A.data_ptr(), A.stride(0), None, W.packed(), C.data_ptr(), C.stride(0), s)
         _check(st, "q4_gemm")
     return C
 
@@ -638,7 +649,8 @@ __all__ += [
 ]
 
 from .block import (  # noqa: E402
-    q4_grad_clip, q4_grad_norm, q4_moe_balance, q4_moe_balance_backward, q4_rmsnorm, q4_rmsnorm_backward)
+    q4_grad_clip, q4_grad_norm, q4_moe_balance, q4_moe_balance_backward, q4_rmsnorm, q4_rmsnorm_backward,
+    q4_w8a8_plan)
 
 __all__ += ["q4_grad_clip", "q4_grad_norm", "q4_moe_balance", "q4_moe_balance_backward", "q4_rmsnorm",
-            "q4_rmsnorm_backward"]
+            "q4_rmsnorm_backward", "q4_w8a8_plan"]

@@ -17,13 +17,26 @@ from . import FP8_ROW, INT8_ROW, Q4Tensor, _check, _matrix, _q4, _vector, lib
 from .grad import BF16, F32, I32, _ids, _ld, _place, _ptr, _workspace
 
 
+_KINDS = {BF16: 0, F32: 1}    # dtype codes of the library
+
+
+def q4_w8a8_plan(M: int, N: int, K: int) -> Tuple[int, int, int]:
+    """(rows, columns) of the block of C that a workgroup of the W8A8 product
+    makes for these sizes, and the number of workgroups; zeros where nothing is
+    launched."""
+    rows, cols, n = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int64()
+    _check(lib().q4_w8a8_plan(M, N, K, ctypes.byref(rows), ctypes.byref(cols), ctypes.byref(n)), "q4_w8a8_plan")
+    return rows.value, cols.value, n.value
+
+
 def _norm_weight(weight: torch.Tensor, cols: int) -> int:
     """Checks a norm's weight; its dtype code."""
-    if not isinstance(weight, torch.Tensor) or weight.dtype not in (BF16, F32):
+    kind = _KINDS.get(weight.dtype) if isinstance(weight, torch.Tensor) else None
+    if kind is None:
         raise ValueError("weight must be a bf16 or float32 tensor")
     if weight.shape != (cols,) or not weight.is_contiguous():
         raise ValueError(f"weight must be contiguous of shape ({cols},) (got {tuple(weight.shape)})")
-    return 1 if weight.dtype is F32 else 0
+    return kind
 
 
 def _rows(t: Optional[torch.Tensor], name: str, rows: int, cols: int) -> int:
@@ -72,7 +85,7 @@ def q4_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residua
             y = torch.empty(rows, cols, dtype=BF16, device=dev)
             ldy = _ld(y)
         if rows and cols:
-            d = ctypes.byref(y_q.c()) if y_q is not None else None
+            d = y_q.packed() if y_q is not None else None
             _check(lib().q4_rmsnorm(x.data_ptr(), ldx, _ptr(residual), ldr, weight.data_ptr(), wt, eps, rows, cols,
                                     _ptr(h), ldh, _ptr(y), ldy, d, s), "q4_rmsnorm")
     return x if residual is None else h, y, y_q
@@ -172,9 +185,6 @@ def q4_moe_balance_backward(logits: torch.Tensor, slopes: torch.Tensor, mask: Op
                                              _ptr(dloss), _ptr(dlogits), max(dlogits.stride(0), E), int(accumulate),
                                              s), "q4_moe_balance_backward")
     return dlogits
-
-
-_KINDS = {BF16: 0, F32: 1}
 
 
 def _tensors(grads: Sequence[torch.Tensor], name: str):

@@ -21,7 +21,7 @@ constexpr int64_t kMaxRows = ((int64_t)1 << 22) - 1;    // up to 1024 threads pe
 constexpr int64_t kMaxGrads = (int64_t)1 << 20;
 constexpr int64_t kMaxGradCount = (int64_t)1 << 44;   // sizes in bytes stay far below 2^63
 constexpr int64_t kMaxNormCols = 32768;               // a row in the registers of 16 waves
-constexpr int64_t kMaxIntN = (int64_t)1 << 27;        // 512 threads per 32 columns: below 2^32 threads
+constexpr int64_t kMaxIntN = (int64_t)1 << 27;        // at least 32 columns per workgroup of up to 1024 threads
 constexpr int64_t kMaxIntK = (int64_t)1 << 17;        // 2^14 K < 2^31: sums of products of two bytes stay exact
 constexpr int64_t kMaxBalanceLd = (int64_t)1 << 27;   // three rows on in 32 bits of values
 constexpr int64_t kMaxTopkTokens = ((int64_t)1 << 26) - 4;  // a wave per token, four a workgroup: below 2^32 threads
@@ -424,6 +424,16 @@ q4_status q4_gemm_quantized(int64_t M, const void* A_bf16, int64_t lda, const q4
                                                      W->scales, W->global_scale, N, K,
                                                      static_cast<const uint16_t*>(A_bf16), lda, M, qo,
                                                      as_stream(stream)));
+}
+
+q4_status q4_w8a8_plan(int64_t M, int64_t N, int64_t K, int32_t* block_rows, int32_t* block_cols,
+                       int64_t* workgroups) {
+  if (!block_rows || !block_cols || !workgroups) return Q4_ERR_NULL;
+  if (M < 0 || M > (int64_t)65535 * 64 || N < 0 || N >= kMaxIntN || K < 0 || K >= kMaxIntK || K % 128) return Q4_ERR_SHAPE;
+  *block_rows = *block_cols = 0;
+  *workgroups = 0;
+  if (M && N && K) q4::w8a8_plan(M, N, K, *block_rows, *block_cols, *workgroups);
+  return Q4_OK;
 }
 
 q4_status q4_rmsnorm(const void* x_bf16, int64_t ldx, const void* residual_bf16, int64_t ldr, const void* weight,

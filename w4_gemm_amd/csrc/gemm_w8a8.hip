@@ -429,13 +429,17 @@ hipError_t run_big(const Args& p, hipStream_t stream) {
 }
 
 // ---- which block ---------------------------------------------------------------
-// The block whose estimated time is least.  256 CUs hold one or two workgroups of
-// each kind at once; a round of up to 256 workgroups takes `one`, a round of up to
-// 512 takes `two` (big blocks: one per CU), in units of 0.01 us per 128 k, plus
-// `fixed` for the first copies and the stores, all measured on 128 x 8192 x 8192
-// and the like.  So 256 rows of 8192 x 8192 take 256 workgroups of 128 x 64 (34
-// us; 512 of 64 x 64: 37, 128 of 128 x 128: 44), 1024 rows 512 of 128 x 128 (70
-// us; 128 of 256 x 256: 82), 2048 rows 256 of 256 x 256 (108 us; 128 x 128: 137).
+// The block whose estimated time is least.  256 CUs take a round of up to 256
+// workgroups in `one`, of up to 512 in `two` (two on a CU; twice `one` where the LDS
+// holds one), in units of 0.01 us per 128 k, plus `fixed` for the first copies and
+// the stores, all measured on 8192 x 8192, 2048 x 7168 and 7168 x 2048 weights.  So
+// 33 rows of 8192 x 8192 take 256 workgroups of 48 x 32 (15.3 us; 256 of 32 x 64:
+// 16.1, 768 of 16 x 32: 21), 256 rows 256 of 128 x 64 (30 us; 512 of 64 x 64: 37,
+// 128 of 128 x 128: 44), 1024 rows 512 of 128 x 128 (70 us; 128 of 256 x 256: 82),
+// 2048 rows 256 of 256 x 256 (108 us; 1024 of 128 x 128: 137).  Up to 256
+// workgroups, which have a CU each, have longer or more stages on the way: one row
+// of 2048 x 7168 6.0 us and 6.9 without, 64 rows of 8192 x 8192 17.5 and 18.6, 100
+// rows 20.4 and 21.8, 256 rows 30.0 and 32.4, 512 rows 46 and 56.
 struct Choice {
   int rows, cols, one, two, fixed;
   hipError_t (*few)(const Args&, hipStream_t);    // up to 256 workgroups
@@ -443,20 +447,17 @@ struct Choice {
 };
 
 const Choice kChoices[] = {
-    {16, 32, 12, 20, 150, run_tile<1, 1, 8, 1, 1, 512, 3>, run_tile<1, 1, 8, 1, 1, 512, 3>},
-    {32, 64, 25, 40, 200, run_tile<1, 2, 4, 2, 1, 256, 3>, run_tile<1, 2, 4, 2, 1, 256, 3>},
-    {64, 64, 31, 53, 200, run_tile<2, 2, 2, 2, 1, 128, 4>, run_tile<2, 2, 2, 2, 1, 128, 4>},
-    {128, 64, 48, 78, 300, run_tile<2, 2, 1, 4, 1, 128, 3>, run_tile<2, 2, 1, 4, 1, 128, 3>},
-    // (one workgroup per CU: a third stage on its way, 46 us for 512 x 8192 x 8192 and 56 without)
+    {16, 32, 12, 20, 150, run_tile<1, 1, 8, 1, 1, 1024, 3>, run_tile<1, 1, 8, 1, 1, 512, 3>},
+    {32, 32, 13, 26, 150, run_tile<1, 1, 8, 2, 1, 512, 3>, run_tile<1, 1, 8, 2, 1, 512, 3>},
+    {48, 32, 21, 42, 200, run_tile<1, 1, 8, 3, 1, 512, 3>, run_tile<1, 1, 8, 3, 1, 512, 3>},
+    {32, 64, 22, 40, 200, run_tile<1, 2, 4, 2, 1, 512, 3>, run_tile<1, 2, 4, 2, 1, 256, 3>},
+    {64, 64, 31, 53, 200, run_tile<2, 2, 2, 2, 1, 256, 4>, run_tile<2, 2, 2, 2, 1, 128, 4>},
+    {128, 64, 41, 78, 400, run_tile<2, 2, 2, 4, 1, 256, 3>, run_tile<2, 2, 1, 4, 1, 128, 3>},
     {128, 128, 70, 106, 500, run_tile<2, 2, 1, 4, 2, 128, 3>, run_tile<2, 2, 1, 4, 2, 128, 2>},
     {256, 256, 166, 332, 800, run_big, run_big},
 };
 
-}  // namespace
-
-hipError_t launch_gemm_w8a8(const uint8_t* a, const float* sa, int64_t M, const uint8_t* w, const float* sw, int64_t N,
-                            int64_t K, uint16_t* C, int64_t ldc, hipStream_t stream) {
-  Args p{a, sa, w, sw, C, M, N, K, ldc, (reinterpret_cast<uintptr_t>(C) & 15) == 0 && (ldc % 8 == 0 || M == 1), 0, 0};
+const Choice& choose(int64_t M, int64_t N, int64_t K, int64_t& tm, int64_t& tn) {
   const Choice* best = nullptr;
   int64_t least = 0;
   for (const Choice& c : kChoices) {
@@ -468,11 +469,30 @@ hipError_t launch_gemm_w8a8(const uint8_t* a, const float* sa, int64_t M, const 
       least = t;
     }
   }
-  const int64_t tm = (M + best->rows - 1) / best->rows, tn = (N + best->cols - 1) / best->cols;
+  tm = (M + best->rows - 1) / best->rows;
+  tn = (N + best->cols - 1) / best->cols;
+  return *best;
+}
+
+}  // namespace
+
+void w8a8_plan(int64_t M, int64_t N, int64_t K, int32_t& rows, int32_t& cols, int64_t& workgroups) {
+  int64_t tm = 0, tn = 0;
+  const Choice& c = choose(M, N, K, tm, tn);
+  rows = c.rows;
+  cols = c.cols;
+  workgroups = tm * tn;
+}
+
+hipError_t launch_gemm_w8a8(const uint8_t* a, const float* sa, int64_t M, const uint8_t* w, const float* sw, int64_t N,
+                            int64_t K, uint16_t* C, int64_t ldc, hipStream_t stream) {
+  Args p{a, sa, w, sw, C, M, N, K, ldc, (reinterpret_cast<uintptr_t>(C) & 15) == 0 && (ldc % 8 == 0 || M == 1), 0, 0};
+  int64_t tm = 0, tn = 0;
+  const Choice& c = choose(M, N, K, tm, tn);
   if (tm * tn >= (int64_t)1 << 23) return hipErrorInvalidConfiguration;   // 2^32 threads: no C that large exists
   p.tm = (uint32_t)tm;
   p.tn = (uint32_t)tn;
-  return (tm * tn <= 256 ? best->few : best->run)(p, stream);
+  return (tm * tn <= 256 ? c.few : c.run)(p, stream);
 }
 
 }  // namespace q4

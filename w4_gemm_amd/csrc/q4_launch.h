@@ -173,6 +173,9 @@ struct NormGradArgs {
 size_t rmsnorm_backward_workspace(int64_t rows, int64_t cols);
 hipError_t launch_rmsnorm_backward(const NormGradArgs& a, float* dweight, int accumulate, hipStream_t stream);
 
+// The block of C that a workgroup of it makes, and how many there are.
+void w8a8_plan(int64_t M, int64_t N, int64_t K, int32_t& rows, int32_t& cols, int64_t& workgroups);
+
 // A router's balance loss (moe_balance.hip): 1 <= E <= 1024.
 struct BalanceArgs {
   const float* logits;       // [T][ld]
