@@ -39,19 +39,14 @@ def _norm_weight(weight: torch.Tensor, cols: int) -> int:
     return kind
 
 
-def _rows(t: Optional[torch.Tensor], name: str, rows: int, cols: int) -> int:
-    """Checks a bf16 matrix of at least `rows` rows of exactly `cols` columns
+def _rows(t: Optional[torch.Tensor], name: str, shape) -> int:
+    """Checks a bf16 matrix of at least shape[0] rows of exactly shape[1] columns
     (None: no such argument); its leading dimension."""
     if t is None:
         return 0
-    if isinstance(t, torch.Tensor) and t.dtype is BF16:
-        shape = t.shape
-        if len(shape) == 2:     # the usual case, with few looks at the tensor
-            r, c = shape
-            step, unit = t.stride()
-            if r > 1 and r >= rows and c == cols and unit == 1 and step >= c:
-                return step
-    _matrix(t, name, BF16, rows, cols, exact_cols=True)
+    if isinstance(t, torch.Tensor) and t.dtype is BF16 and t.shape == shape and t.is_contiguous():
+        return shape[1]       # the usual case, with few looks at the tensor
+    _matrix(t, name, BF16, *shape, exact_cols=True)
     return _ld(t)
 
 
@@ -64,12 +59,13 @@ def q4_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residua
     for q4_gemm.  weight [cols] in bf16 or float32.  h may be x or residual."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be a 2-D bf16 tensor")
-    rows, cols = x.shape
-    ldx, ldr = _rows(x, "x", rows, cols), _rows(residual, "residual", rows, cols)
+    shape = x.shape
+    rows, cols = shape
+    ldx, ldr = _rows(x, "x", shape), _rows(residual, "residual", shape)
     wt = _norm_weight(weight, cols)
     if h is not None and residual is None:
         raise ValueError("h is written only with a residual")
-    ldh, ldy = _rows(h, "h", rows, cols), _rows(y, "y", rows, cols)
+    ldh, ldy = _rows(h, "h", shape), _rows(y, "y", shape)
     if y_q is not None:
         _q4(y_q, "y_q")
         if y_q.fmt not in (FP8_ROW, INT8_ROW):
@@ -79,11 +75,9 @@ def q4_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residua
     with _place(stream, ("x", x), ("weight", weight), ("residual", residual), ("h", h), ("y", y),
                 ("y_q", y_q)) as (dev, s):
         if residual is not None and h is None:
-            h = torch.empty(rows, cols, dtype=BF16, device=dev)
-            ldh = _ld(h)
+            h, ldh = torch.empty(shape, dtype=BF16, device=dev), cols
         if y is None and y_q is None:
-            y = torch.empty(rows, cols, dtype=BF16, device=dev)
-            ldy = _ld(y)
+            y, ldy = torch.empty(shape, dtype=BF16, device=dev), cols
         if rows and cols:
             d = y_q.packed() if y_q is not None else None
             _check(lib().q4_rmsnorm(x.data_ptr(), ldx, _ptr(residual), ldr, weight.data_ptr(), wt, eps, rows, cols,
@@ -101,12 +95,13 @@ def q4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
     weight_grad=False: none (None is returned).  dx may be dh or dy."""
     if not isinstance(dy, torch.Tensor) or dy.dim() != 2:
         raise ValueError("dy must be a 2-D bf16 tensor")
-    rows, cols = dy.shape
-    lddy = _rows(dy, "dy", rows, cols)
+    shape = dy.shape
+    rows, cols = shape
+    lddy = _rows(dy, "dy", shape)
     wt = _norm_weight(weight, cols)
-    ldh, lddh, lddx = _rows(h, "h", rows, cols), _rows(dh, "dh", rows, cols), _rows(dx, "dx", rows, cols)
-    if h.shape[0] != rows:
-        raise ValueError(f"h must have {rows} rows like dy (got {h.shape[0]})")
+    ldh, lddh, lddx = _rows(h, "h", shape), _rows(dh, "dh", shape), _rows(dx, "dx", shape)
+    if h is None or h.shape[0] != rows:
+        raise ValueError(f"h must have {rows} rows like dy (got {None if h is None else h.shape[0]})")
     if dweight is not None:
         if not weight_grad:
             raise ValueError("dweight given with weight_grad=False")
@@ -116,8 +111,7 @@ def q4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
     with _place(stream, ("dy", dy), ("h", h), ("weight", weight), ("dh", dh), ("dx", dx),
                 ("dweight", dweight)) as (dev, s):
         if dx is None:
-            dx = torch.empty(rows, cols, dtype=BF16, device=dev)
-            lddx = _ld(dx)
+            dx, lddx = torch.empty(shape, dtype=BF16, device=dev), cols
         ws, need = None, 0
         if weight_grad:
             if dweight is None:
