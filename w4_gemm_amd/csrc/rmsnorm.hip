@@ -322,10 +322,16 @@ void norm(const NormArgs& a, int kind, hipStream_t stream) {
   else norm_kind<WAVES, CH, false>(a, kind, stream);
 }
 
+// Workgroups of the gradient, of one row (four of up to 2048 columns) at a time:
+// enough for the loads, few enough that their sums are little beside the rows.  512
+// where each has four turns and more (8192 x 8192: 92 us, 256 of them 103), else
+// one for two turns, between 128 and 256 (512 x 8192: 16.9 us with 256 and 20.8
+// with 512; 256 x 8192: 13.8 with 128 and 15.4 with 256).
 int64_t grad_blocks(int64_t rows, int64_t cols) {
-  const int64_t per = cols <= 2048 ? 4 : 1;
-  const int64_t b = (rows + per - 1) / per;
-  return b < kGradBlocks ? b : kGradBlocks;
+  const int64_t per = cols <= 2048 ? 4 : 1, turns = (rows + per - 1) / per;
+  if (turns >= 4 * kGradBlocks) return kGradBlocks;
+  if (turns <= 128) return turns;
+  return turns >= 512 ? 256 : turns <= 256 ? 128 : turns / 2;
 }
 
 template <int WAVES, int CH>
