@@ -1,6 +1,7 @@
 """w4_gemm_amd -- 4-bit absmax block quantization (INT4 g128, MXFP4, NVFP4)
 and the W4 matmuls that consume it (W4A16, W4A4, W4A8 with per-token FP8
-activations), as hand-written HIP kernels for gfx950.
+activations), and W8A8 beside them, as hand-written HIP kernels for gfx950.
+w4_gemm_amd/block.py has what stands around the products.
 
 This module is the thin Python binding of libq4.so's C ABI (include/q4.h):
 the functions have the same names and only marshal arguments -- torch

@@ -90,6 +90,14 @@ __device__ __forceinline__ void block_of(const Args& p, int rows, int64_t& bm, i
 // its copies of stage u + 2: A's in the first half, into the place that W of stage
 // u - 1 left, W's in the second, into that of A of stage u, which every wave has
 // read by then.  One barrier per stage, in its middle.
+// 4096 x 8192 x 8192: 205 to 217 us, 2.5 to 2.7 POPS, where the instruction alone on
+// random registers makes 3.4 to 3.6 and the matrix pipe is busy in 78% of a CU's
+// cycles: bound by power, which holds the XCDs at 1.3 to 1.9 GHz (codes over the whole
+// range 242 us, at 1.30 to 1.37 GHz); a block's stores are 8 of its 122 us.  No faster: eight waves of
+// 64 x 128 (two per SIMD), stages of 64 k in four places (lines of 64 bytes: 7%
+// slower), lines asked for three to five stages ahead, groups of 2, 8 or 16 block
+// rows per XCD (1, 0 and 9% slower).  16 x 16 x 64 products do not fit: the compiler
+// moves accumulators about.
 // Fragments of 32 rows: lane l supplies row l % 32, k = 16 (l / 32) .. +15.  The
 // weight's row for index i of a tile is 16 (i / 16) + 8 (i / 4 % 2) +
 // 4 (i / 8 % 2) + i % 4, which leaves twice 8 consecutive columns in a lane.
