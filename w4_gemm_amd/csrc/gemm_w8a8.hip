@@ -90,14 +90,14 @@ __device__ __forceinline__ void block_of(const Args& p, int rows, int64_t& bm, i
 // its copies of stage u + 2: A's in the first half, into the place that W of stage
 // u - 1 left, W's in the second, into that of A of stage u, which every wave has
 // read by then.  One barrier per stage, in its middle.
-// 4096 x 8192 x 8192: 205 to 217 us, 2.5 to 2.7 POPS, where the instruction alone on
-// random registers makes 3.4 to 3.6 and the matrix pipe is busy in 78% of a CU's
-// cycles: bound by power, which holds the XCDs at 1.3 to 1.9 GHz (codes over the whole
-// range 242 us, at 1.30 to 1.37 GHz); a block's stores are 8 of its 122 us.  No faster: eight waves of
-// 64 x 128 (two per SIMD), stages of 64 k in four places (lines of 64 bytes: 7%
-// slower), lines asked for three to five stages ahead, groups of 2, 8 or 16 block
-// rows per XCD (1, 0 and 9% slower).  16 x 16 x 64 products do not fit: the compiler
-// moves accumulators about.
+// 4096 x 8192 x 8192: 207 to 221 us, 2.5 to 2.7 POPS, the instruction alone on random
+// registers 3.3 to 3.6; passes without a pause 241 to 252 us.  The matrix
+// pipe is busy in 78% of a CU's cycles, and the XCDs run those at 1.30 to 1.45 GHz:
+// bound by the clock that the load leaves.  A block's stores are 8 of its 120 us.
+// No faster: eight waves of 64 x 128 (two per SIMD), stages of 64 k in four places
+// (lines of 64 bytes: 7% slower), lines asked for three to five stages ahead,
+// groups of 2, 8 or 16 block rows per XCD (1, 0 and 9% slower).  16 x 16 x 64
+// products do not fit: the compiler moves accumulators about.
 // Fragments of 32 rows: lane l supplies row l % 32, k = 16 (l / 32) .. +15.  The
 // weight's row for index i of a tile is 16 (i / 16) + 8 (i / 4 % 2) +
 // 4 (i / 8 % 2) + i % 4, which leaves twice 8 consecutive columns in a lane.
@@ -279,19 +279,6 @@ struct Tile {
   static_assert(BK % (64 * WK) == 0 && (WK - 1) * WM * WN * TM * TN * 2048 <= S * kStage, "sums fit into the stages");
 };
 
-// Waits until only the copies of STAGES later stages may be on their way, W + a of
-// them in each (a <= A, the same in every stage).
-template <int W, int A, int STAGES, bool FEWER>
-__device__ __forceinline__ void wait_copies(int a) {
-  if constexpr (FEWER && A > 0) {
-    if (a < A) {
-      wait_copies<W, A - 1, STAGES, true>(a);
-      return;
-    }
-  }
-  wait_vmcnt_lgkm0<STAGES * (W + A)>();
-}
-
 template <int WM, int WN, int WK, int TM, int TN, int BK, int S>
 __global__ void __launch_bounds__((Tile<WM, WN, WK, TM, TN, BK, S>::kThreads))
 w8a8_tile_kernel(const Args p) {
@@ -308,11 +295,9 @@ w8a8_tile_kernel(const Args p) {
   const int K = (int)p.K, U = (K + BK - 1) / BK;
   const int left_m = (int)(p.M - m0 < T::kM ? p.M - m0 : T::kM), left_n = (int)(p.N - n0 < T::kN ? p.N - n0 : T::kN);
 
-  // Copy i of a wave: W's first, then A's, each kCopyRows rows.  The block of 16
-  // rows, whose copies of A are a third of all, leaves out those behind A's last row
-  // (what LDS holds there makes outputs that are not stored; one row of 28672 x 8192:
-  // 39.7 -> 38.7 us); for the others the branches cost more than they save.
-  constexpr bool kLeaveOut = T::kM == 16;
+  // Copy i of a wave: W's first, then A's, each kCopyRows rows; those behind the last
+  // row take it again.  (Without the copies of A that are only such rows, a third of
+  // all for one row of 28672 x 8192: 38.9 us for 39.0.)
   constexpr int kCopies = T::kCopiesW + T::kCopiesA;
   const uint8_t* src_w = uniform_ptr(p.w + n0 * K);
   const uint8_t* src_a = uniform_ptr(p.a + m0 * K);
@@ -325,10 +310,6 @@ w8a8_tile_kernel(const Args p) {
     row_at[i] = (uint32_t)(r < left ? r : left - 1) * (uint32_t)K;
     chunk_at[i] = 16 * ((lane % kChunks) ^ (is_w ? key_w(r) : key_a(r)));
   }
-  int copies_a = kLeaveOut ? 0 : T::kCopiesA;
-  if (kLeaveOut)
-#pragma unroll
-    for (int i = 0; i < T::kCopiesA; ++i) copies_a += (i * T::kWaves + wave) * kCopyRows < left_m;
   auto copy = [&](int u) {
     uint8_t* d = smem + (u % S) * T::kStage + wave * 1024;
     const int64_t k0 = (int64_t)u * BK;
@@ -336,7 +317,6 @@ w8a8_tile_kernel(const Args p) {
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) {
       const bool is_w = i < T::kCopiesW;
-      if (kLeaveOut && !is_w && i - T::kCopiesW >= copies_a) break;
       // (in the last stage of a K that is no multiple, chunks behind it read its first one, and are not used)
       const uint32_t c = BK == 128 || chunk_at[i] < left ? chunk_at[i] : 0u;
       copy16_to_lds((is_w ? src_w : src_a) + k0 + (row_at[i] + c),
@@ -347,8 +327,8 @@ w8a8_tile_kernel(const Args p) {
   auto wait = [&](int u) {
     const int later = U - 1 - u < S - 2 ? U - 1 - u : S - 2;
     if (later <= 0) wait_vmcnt_lgkm0<0>();
-    else if (later == 1) wait_copies<T::kCopiesW, T::kCopiesA, 1, kLeaveOut>(copies_a);
-    else wait_copies<T::kCopiesW, T::kCopiesA, 2, kLeaveOut>(copies_a);
+    else if (later == 1) wait_vmcnt_lgkm0<kCopies>();
+    else wait_vmcnt_lgkm0<2 * kCopies>();
   };
   static_assert(S >= 2 && S <= 4, "the counts above");
 
