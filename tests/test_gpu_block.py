@@ -156,3 +156,36 @@ def test_a_stream_that_is_named():
         assert all(torch.equal(p, q) for p, q in zip(g, want_g))
         assert torch.equal(n, want_n) and torch.equal(n2, want_n) and all(torch.equal(p, q) for p, q in zip(c, want_c))
         assert torch.equal(A2.codes, A.codes) and torch.equal(C2, C)
+
+
+@pytest.mark.parametrize("allocates", [True, False])
+def test_a_handle_of_zero_is_the_default_stream(allocates):
+    """stream=0 inside another stream's context: the default stream, not a new one."""
+    from w4_gemm_amd.grad import _place
+    x = torch.ones(8, device="cuda")
+    with torch.cuda.stream(torch.cuda.Stream()):
+        with _place(0, ("x", x), allocates=allocates) as (_, s):
+            assert s == torch.cuda.default_stream().cuda_stream == 0
+            if allocates:
+                assert torch.cuda.current_stream().cuda_stream == 0
+
+
+def test_stream_zero_is_in_order_with_the_default_stream():
+    """Fills on the default stream, then calls with stream=0 and with nothing between: each sees the fill before it."""
+    src = torch.zeros(4096, 2048, dtype=BF16, device="cuda")
+    dst, back = q4.empty_q4("int8_row", 4096, 2048), torch.empty(4096, 2048, dtype=F32, device="cuda")
+    grads = [torch.empty(1 << 24, device="cuda")]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(1, 9):
+        for _ in range(8):
+            src.fill_(float(i))
+            grads[0].fill_(float(i))
+        q4.q4_quantize(src, dst, stream=0)
+        q4.q4_dequant(dst, back, stream=0)
+        norm = q4.q4_grad_norm(grads, stream=0)
+        got.append((back.amin(), back.amax(), norm))
+    torch.cuda.synchronize()
+    for i, (lo, hi, norm) in enumerate(got, 1):
+        assert abs(lo.item() - i) <= i * 2.0 ** -22 and abs(hi.item() - i) <= i * 2.0 ** -22
+        assert norm.item() == i * 4096.0

@@ -348,7 +348,7 @@ def _quantize(src, dst, nv_global_in, stream) -> Q4Tensor:
     _matrix(src, "src", torch.bfloat16, dst.rows, dst.cols)
     if nv_global_in is not None:
         _vector(nv_global_in, "nv_global_in", torch.float32, 1)
-    with _place(stream, ("src", src), ("dst", dst), ("nv_global_in", nv_global_in)) as (_, s):
+    with _place(stream, ("src", src), ("dst", dst), ("nv_global_in", nv_global_in), allocates=False) as (_, s):
         _check(lib().q4_quantize(src.data_ptr(), src.stride(0), dst.packed(), _ptr(nv_global_in), s), "q4_quantize")
     return dst
 
@@ -391,7 +391,7 @@ def q4_dequant(src: Q4Tensor, dst: torch.Tensor, stream=None) -> torch.Tensor:
         raise ValueError("dst must be bf16 or float32")
     _matrix(dst, "dst", dst.dtype, src.rows, src.cols)
     _q4(src, "src")
-    with _place(stream, ("src", src), ("dst", dst)) as (_, s):
+    with _place(stream, ("src", src), ("dst", dst), allocates=False) as (_, s):
         _check(lib().q4_dequant(src.packed(), dst.data_ptr(), dt, dst.stride(0), s), "q4_dequant")
     return dst
 
@@ -422,7 +422,7 @@ def q4_gemm(A, W: Q4Tensor, C: torch.Tensor, stream=None) -> torch.Tensor:
         _matrix(A, "A", torch.bfloat16, 0, W.cols, exact_cols=True)
         M = A.shape[0]
     _matrix(C, "C", torch.bfloat16, M, W.rows)
-    with _place(stream, ("W", W), ("A", A), ("C", C)) as (_, s):
+    with _place(stream, ("W", W), ("A", A), ("C", C), allocates=False) as (_, s):
         if isinstance(A, Q4Tensor):
             st = lib().q4_gemm(A.rows, None, 0, A.packed(), W.packed(), C.data_ptr(), C.stride(0), s)
         else:

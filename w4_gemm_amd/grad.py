@@ -86,10 +86,11 @@ def _one_device(args) -> int:
     return where
 
 
-def _place(stream, *args):
+def _place(stream, *args, allocates: bool = True):
     """Checks that every (name, tensor) is on the GPU, all on one; `with` it the
     call is on that device and the stream it runs on, as (device, stream) ready
-    for torch and for the library."""
+    for torch and for the library.  allocates=False: the call makes no tensor, so
+    torch need not be told of a stream on the current device."""
     where = _one_device(args)
     if where < 0:
         for name, t in args:
@@ -108,11 +109,16 @@ def _place(stream, *args):
         if where == _current_device():
             return _Here(where, _raw_stream(where))
         return _There(where, None)
+    here = not allocates and where == _current_device()
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=where)
+        handle = int(stream)
+        if here:
+            return _Here(where, handle)
+        # (torch takes a handle of 0, the default stream, for none and makes a stream)
+        stream = torch.cuda.ExternalStream(handle, device=where) if handle else torch.cuda.default_stream(where)
     elif stream.device.index != where:
         raise ValueError(f"stream must be of cuda:{where} (got {stream.device})")
-    return _There(where, stream)
+    return _Here(where, stream.cuda_stream) if here else _There(where, stream)
 
 
 def _ptr(t: Optional[torch.Tensor]):
