@@ -635,7 +635,8 @@ q4_status q4_grouped_gemm_wgrad(const void* dC_bf16, int64_t lddc, const void* A
  * that sizes and alignment alone decide; a norm past fp32's range is inf in norm
  * and as it is for the factor.  A NaN or an infinity among the gradients makes
  * norm NaN or inf, as arithmetic has it: every output is then NaN, or 0 where g
- * is finite and the norm inf.
+ * is finite and the norm inf.  The factor and the product are made in 64 bits,
+ * and the product rounded to fp32 and, for bf16, from there.
  * q4_grad_clip takes the norm from norm_in (e.g. one combined over ranks), or
  * with norm_in NULL makes it in the same call and writes it to norm_out (which
  * may be NULL; not written with norm_in).  out: host array of n pointers of the

@@ -189,3 +189,47 @@ def test_stream_zero_is_in_order_with_the_default_stream():
     for i, (lo, hi, norm) in enumerate(got, 1):
         assert abs(lo.item() - i) <= i * 2.0 ** -22 and abs(hi.item() - i) <= i * 2.0 ** -22
         assert norm.item() == i * 4096.0
+
+
+def test_calls_at_once():
+    """Two threads with a stream each, every call with a workspace or a shared counter: the results of one alone."""
+    import threading
+    sizes = [(700, 2048), (900, 4096)]
+    g = torch.Generator().manual_seed(5)
+    sets = []
+    for rows, cols in sizes:
+        x, dy = (torch.randn(rows, cols, generator=g).to(BF16).cuda() for _ in range(2))
+        logits = torch.randn(9000, 200, generator=g).cuda()
+        ids, _ = q4.q4_moe_topk(logits, 4)
+        grads = [torch.randn(n, generator=g).cuda() for n in (rows * cols, 5, 70001)]
+        sets.append((x, dy, torch.rand(cols, generator=g).cuda(), logits, ids, grads))
+
+    def calls(x, dy, w, logits, ids, grads):
+        out = [torch.empty_like(t) for t in grads]
+        a = q4.empty_q4("int8_row", *x.shape)
+        q4.q4_rmsnorm(x, w, EPS, y_q=a)
+        C = q4.q4_gemm(a, a, torch.empty(x.shape[0], x.shape[0], dtype=BF16, device="cuda"))
+        return (*q4.q4_rmsnorm_backward(dy, x, w, EPS), *q4.q4_moe_balance(logits, ids),
+                q4.q4_grad_clip(grads, 1.0, out=out), *out, C)
+
+    want = [[t.clone() for t in calls(*s)] for s in sets]
+    torch.cuda.synchronize()
+    bad, errors = [], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()) as _:
+                for _ in range(20):
+                    got = calls(*sets[i])
+                    bad.append(sum((p != q).sum() for p, q in zip(got, want[i])))
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:   # (shown in the test's own thread)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors and len(bad) == 40 and all(int(b) == 0 for b in bad)

@@ -234,7 +234,8 @@ moe_balance_kernel(const BalanceArgs a) {
 // per four of them and 64th of the sums, then 16 threads per expert.  The last
 // workgroup to end (the ticket was cleared by the first kernel) adds their parts
 // of the loss, in their order.  256 workgroups' sums of 256 experts: 8 us, latency
-// (10 us in a single workgroup).
+// (10 us in a single workgroup; both kernels 22.9 us, 23.7 with 32 experts per
+// workgroup and 23.5 with 16, of 1024 experts 27.2, 29.2 and 32.4).
 constexpr int kFinishExperts = 64;
 constexpr int kFinishMost = 1024 / kFinishExperts;   // workgroups
 __global__ void __launch_bounds__(kThreads)
