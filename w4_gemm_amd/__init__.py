@@ -340,25 +340,28 @@ def q4_quantize(src: torch.Tensor, dst: Q4Tensor, nv_global_in: Optional[torch.T
                 stream=None) -> Q4Tensor:
     """Quantize bf16 src [rows, >= cols] (row stride src.stride(0)) into dst."""
     _q4(dst, "dst")
-    return _quantize(src, dst, nv_global_in, stream)
-
-
-def _quantize(src, dst, nv_global_in, stream) -> Q4Tensor:
-    """q4_quantize into a tensor whose buffers are as they should be."""
     _matrix(src, "src", torch.bfloat16, dst.rows, dst.cols)
     if nv_global_in is not None:
         _vector(nv_global_in, "nv_global_in", torch.float32, 1)
     with _place(stream, ("src", src), ("dst", dst), ("nv_global_in", nv_global_in), allocates=False) as (_, s):
-        _check(lib().q4_quantize(src.data_ptr(), src.stride(0), dst.packed(), _ptr(nv_global_in), s), "q4_quantize")
+        return _quantize(src, dst, nv_global_in, s)
+
+
+def _quantize(src, dst, nv_global_in, s) -> Q4Tensor:
+    """q4_quantize of arguments that are as they should be, on a stream's handle."""
+    _check(lib().q4_quantize(src.data_ptr(), src.stride(0), dst.packed(), _ptr(nv_global_in), s), "q4_quantize")
     return dst
 
 
 def quantize(src: torch.Tensor, fmt, nv_global_in: Optional[torch.Tensor] = None,
              stream=None, layout=LAYOUT_ROWS) -> Q4Tensor:
-    """Allocate a Q4Tensor on src's device and quantize src into it."""
-    dst = empty_q4(fmt, src.shape[0], src.shape[1], device=src.get_device() if src.is_cuda else src.device,
-                   layout=layout)
-    return _quantize(src, dst, nv_global_in, stream)
+    """Allocate a Q4Tensor on src's device, as the stream's own memory, and quantize src into it."""
+    _matrix(src, "src", torch.bfloat16, 0, 0)
+    if nv_global_in is not None:
+        _vector(nv_global_in, "nv_global_in", torch.float32, 1)
+    rows, cols = src.shape
+    with _place(stream, ("src", src), ("nv_global_in", nv_global_in)) as (dev, s):
+        return _quantize(src, empty_q4(fmt, rows, cols, device=dev, layout=layout), nv_global_in, s)
 
 
 def q4_relayout(src: Q4Tensor, dst: Q4Tensor, stream=None) -> Q4Tensor:
