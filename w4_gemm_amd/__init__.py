@@ -9,6 +9,13 @@ tensors supply device memory and the current HIP stream, every step of the
 computation runs in the library's kernels.  There is no CPU fallback: if the
 library cannot be loaded, every call raises.  No call records itself for
 torch's differentiation (w4_gemm_amd/grad.py has the gradients).
+
+All tensors of a call are on one GPU (ValueError otherwise), which need not be
+the current one: the call runs there, on that device's current stream or on the
+`stream` that is named (an object, which has to be of that device, or a handle; 0:
+the default stream).  What a call allocates, outputs and what it holds in
+between, is that stream's memory; a caller that names another stream than the
+current one orders the two, as with torch's own operators.
 """
 from __future__ import annotations
 
@@ -167,17 +174,6 @@ def _stream(stream):
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
-
-
-def _on_gpu(*args):
-    """Every tensor argument (or Q4Tensor buffer) is on the GPU.  Checked
-    after the shapes, so that the shape checks can be tested on the CPU."""
-    for name, t in args:
-        if t is None:
-            continue
-        for part, x in _parts(t):
-            if x is not None and not x.is_cuda:
-                raise ValueError(f"{name}{part} must be a GPU tensor (got device {x.device})")
 
 
 def _parts(t):
@@ -371,17 +367,22 @@ def q4_relayout(src: Q4Tensor, dst: Q4Tensor, stream=None) -> Q4Tensor:
     _q4(dst, "dst")
     if src.fmt != dst.fmt or (src.rows, src.cols) != (dst.rows, dst.cols):
         raise ValueError("src and dst must have the same format and shape")
-    _on_gpu(("src", src), ("dst", dst))
-    a, b = src.c(), dst.c()
-    _check(lib().q4_relayout(ctypes.byref(a), ctypes.byref(b), _stream(stream)), "q4_relayout")
+    with _place(stream, ("src", src), ("dst", dst), allocates=False) as (_, s):
+        return _relayout(src, dst, s)
+
+
+def _relayout(src, dst, s) -> Q4Tensor:
+    """q4_relayout of arguments that are as they should be, on a stream's handle."""
+    _check(lib().q4_relayout(src.packed(), dst.packed(), s), "q4_relayout")
     return dst
 
 
 def relayout(src: Q4Tensor, layout=LAYOUT_TILED, stream=None) -> Q4Tensor:
-    """Allocate a tensor of src's format and shape in `layout` and move src
-    into it."""
-    dst = empty_q4(src.fmt, src.rows, src.cols, device=src.codes.device, layout=layout)
-    return q4_relayout(src, dst, stream)
+    """Allocate a tensor of src's format and shape in `layout`, as the
+    stream's own memory, and move src into it."""
+    _q4(src, "src")
+    with _place(stream, ("src", src)) as (dev, s):
+        return _relayout(src, empty_q4(src.fmt, src.rows, src.cols, device=dev, layout=layout), s)
 
 
 def q4_dequant(src: Q4Tensor, dst: torch.Tensor, stream=None) -> torch.Tensor:
@@ -404,10 +405,9 @@ def q4_gemv(W: Q4Tensor, x: torch.Tensor, y: torch.Tensor, stream=None) -> torch
     _q4(W, "W")
     _matrix(x, "x", torch.bfloat16, 0, W.cols, exact_cols=True)
     _matrix(y, "y", torch.bfloat16, x.shape[0], W.rows)
-    _on_gpu(("W", W), ("x", x), ("y", y))
-    desc = W.c()
-    _check(lib().q4_gemv(ctypes.byref(desc), _ptr(x), x.shape[0], x.stride(0), _ptr(y),
-                         y.stride(0), _stream(stream)), "q4_gemv")
+    with _place(stream, ("W", W), ("x", x), ("y", y), allocates=False) as (_, s):
+        _check(lib().q4_gemv(W.packed(), x.data_ptr(), x.shape[0], x.stride(0), y.data_ptr(), y.stride(0), s),
+               "q4_gemv")
     return y
 
 
@@ -454,16 +454,13 @@ def q4_gemm_quantized(A, W: Q4Tensor, C: Q4Tensor, nv_global_in: Optional[torch.
         raise ValueError(f"C must be {M} x {W.rows} (got {C.rows} x {C.cols})")
     if nv_global_in is not None:
         _vector(nv_global_in, "nv_global_in", torch.float32, 1)
-    _on_gpu(("W", W), ("A", A), ("C", C), ("nv_global_in", nv_global_in))
-    wd, cd = W.c(), C.c()
-    if isinstance(A, Q4Tensor):
-        ad = A.c()
-        st = lib().q4_gemm_quantized(M, None, 0, ctypes.byref(ad), ctypes.byref(wd), ctypes.byref(cd),
-                                     _ptr(nv_global_in), _stream(stream))
-    else:
-        st = lib().q4_gemm_quantized(M, _ptr(A), A.stride(0), None, ctypes.byref(wd), ctypes.byref(cd),
-                                     _ptr(nv_global_in), _stream(stream))
-    _check(st, "q4_gemm_quantized")
+    with _place(stream, ("W", W), ("A", A), ("C", C), ("nv_global_in", nv_global_in), allocates=False) as (_, s):
+        if isinstance(A, Q4Tensor):
+            st = lib().q4_gemm_quantized(M, None, 0, A.packed(), W.packed(), C.packed(), _ptr(nv_global_in), s)
+        else:
+            st = lib().q4_gemm_quantized(M, A.data_ptr(), A.stride(0), None, W.packed(), C.packed(),
+                                         _ptr(nv_global_in), s)
+        _check(st, "q4_gemm_quantized")
     return C
 
 
@@ -482,11 +479,10 @@ def q4_grouped_gemm(A: torch.Tensor, gather: torch.Tensor, offsets: torch.Tensor
         _vector(gather, "gather", torch.int32, 0)
     P = C.shape[0] if gather is None else gather.numel()
     _matrix(C, "C", torch.bfloat16, P, N)
-    _on_gpu(("W", W), ("A", A), ("gather", gather), ("offsets", offsets), ("C", C))
-    wd = W.c()
-    _check(lib().q4_grouped_gemm(_ptr(A), A.stride(0), A.shape[0], _ptr(gather), _ptr(offsets),
-                                 E, P, ctypes.byref(wd), N, _ptr(C), C.stride(0),
-                                 _stream(stream)), "q4_grouped_gemm")
+    with _place(stream, ("W", W), ("A", A), ("gather", gather), ("offsets", offsets), ("C", C),
+                allocates=False) as (_, s):
+        _check(lib().q4_grouped_gemm(A.data_ptr(), A.stride(0), A.shape[0], _ptr(gather), offsets.data_ptr(), E, P,
+                                     W.packed(), N, C.data_ptr(), C.stride(0), s), "q4_grouped_gemm")
     return C
 
 
@@ -504,17 +500,15 @@ def q4_moe_route(logits: torch.Tensor, k: int, stream=None) -> Routing:
     """Top-k routing with softmax gates and the expert-major dispatch order
     for fp32 router logits [T, E] (unit column stride)."""
     _matrix(logits, "logits", torch.float32, 0, 0)
-    _on_gpu(("logits", logits))
     T, E = logits.shape
-    dev = logits.device
-    r = Routing(torch.empty((T, k), dtype=torch.int32, device=dev),
-                torch.empty((T, k), dtype=torch.float32, device=dev),
-                torch.empty(E + 1, dtype=torch.int32, device=dev),
-                torch.empty(T * k, dtype=torch.int32, device=dev),
-                torch.empty((T, k), dtype=torch.int32, device=dev))
-    _check(lib().q4_moe_route(_ptr(logits), logits.stride(0) if T else E, T, E, k, _ptr(r.ids), _ptr(r.weights),
-                              _ptr(r.offsets), _ptr(r.gather), _ptr(r.inv), _stream(stream)),
-           "q4_moe_route")
+    with _place(stream, ("logits", logits)) as (dev, s):
+        r = Routing(torch.empty((T, k), dtype=torch.int32, device=dev),
+                    torch.empty((T, k), dtype=torch.float32, device=dev),
+                    torch.empty(E + 1, dtype=torch.int32, device=dev),
+                    torch.empty(T * k, dtype=torch.int32, device=dev),
+                    torch.empty((T, k), dtype=torch.int32, device=dev))
+        _check(lib().q4_moe_route(logits.data_ptr(), logits.stride(0) if T else E, T, E, k, _ptr(r.ids),
+                                  _ptr(r.weights), _ptr(r.offsets), _ptr(r.gather), _ptr(r.inv), s), "q4_moe_route")
     return r
 
 
@@ -522,12 +516,12 @@ def q4_swiglu(gu: torch.Tensor, inter: int, h: Optional[torch.Tensor] = None, st
     """h = silu(gu[:, :inter]) * gu[:, inter:2*inter] (bf16)."""
     _matrix(gu, "gu", torch.bfloat16, 0, 2 * inter)
     P = gu.shape[0]
-    if h is None:
-        h = torch.empty((P, inter), dtype=torch.bfloat16, device=gu.device)
-    _matrix(h, "h", torch.bfloat16, P, inter)
-    _on_gpu(("gu", gu), ("h", h))
-    _check(lib().q4_swiglu(_ptr(gu), gu.stride(0), P, inter, _ptr(h), h.stride(0), _stream(stream)),
-           "q4_swiglu")
+    if h is not None:
+        _matrix(h, "h", torch.bfloat16, P, inter)
+    with _place(stream, ("gu", gu), ("h", h)) as (dev, s):
+        if h is None:
+            h = torch.empty((P, inter), dtype=torch.bfloat16, device=dev)
+        _check(lib().q4_swiglu(gu.data_ptr(), gu.stride(0), P, inter, h.data_ptr(), h.stride(0), s), "q4_swiglu")
     return h
 
 
@@ -539,12 +533,13 @@ def q4_moe_combine(y: torch.Tensor, r: Routing, out: Optional[torch.Tensor] = No
     _vector(r.weights, "r.weights", torch.float32, T * k)
     _matrix(y, "y", torch.bfloat16, T * k, 0)
     N = y.shape[1]
-    if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=y.device)
-    _matrix(out, "out", torch.bfloat16, T, N)
-    _on_gpu(("y", y), ("r.inv", r.inv), ("r.weights", r.weights), ("out", out))
-    _check(lib().q4_moe_combine(_ptr(y), y.stride(0), _ptr(r.inv), _ptr(r.weights), T, k, N, _ptr(out),
-                                out.stride(0), _stream(stream)), "q4_moe_combine")
+    if out is not None:
+        _matrix(out, "out", torch.bfloat16, T, N)
+    with _place(stream, ("y", y), ("r.inv", r.inv), ("r.weights", r.weights), ("out", out)) as (dev, s):
+        if out is None:
+            out = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+        _check(lib().q4_moe_combine(y.data_ptr(), y.stride(0), r.inv.data_ptr(), r.weights.data_ptr(), T, k, N,
+                                    out.data_ptr(), out.stride(0), s), "q4_moe_combine")
     return out
 
 
@@ -563,11 +558,11 @@ def q4_grouped_gemm_swiglu(A: torch.Tensor, gather: Optional[torch.Tensor], offs
         _vector(gather, "gather", torch.int32, 0)
     P = H.shape[0] if gather is None else gather.numel()
     _matrix(H, "H", torch.bfloat16, P, inter)
-    _on_gpu(("W", W), ("A", A), ("gather", gather), ("offsets", offsets), ("H", H))
-    wd = W.c()
-    _check(lib().q4_grouped_gemm_swiglu(_ptr(A), A.stride(0), A.shape[0], _ptr(gather), _ptr(offsets), E, P,
-                                        ctypes.byref(wd), inter, _ptr(H), H.stride(0), _stream(stream)),
-           "q4_grouped_gemm_swiglu")
+    with _place(stream, ("W", W), ("A", A), ("gather", gather), ("offsets", offsets), ("H", H),
+                allocates=False) as (_, s):
+        _check(lib().q4_grouped_gemm_swiglu(A.data_ptr(), A.stride(0), A.shape[0], _ptr(gather), offsets.data_ptr(), E,
+                                            P, W.packed(), inter, H.data_ptr(), H.stride(0), s),
+               "q4_grouped_gemm_swiglu")
     return H
 
 
@@ -580,8 +575,8 @@ def q4_read_probe(src: torch.Tensor, sink: torch.Tensor, stream=None) -> None:
     if nbytes % 1024:
         raise ValueError("src must hold a multiple of 1024 bytes")
     _vector(sink, "sink", torch.int32, 1)
-    _on_gpu(("src", src), ("sink", sink))
-    _check(lib().q4_read_probe(_ptr(src), nbytes, _ptr(sink), _stream(stream)), "q4_read_probe")
+    with _place(stream, ("src", src), ("sink", sink), allocates=False) as (_, s):
+        _check(lib().q4_read_probe(src.data_ptr(), nbytes, sink.data_ptr(), s), "q4_read_probe")
 
 
 PROBE_KINDS = {"fp4": 0, "bf16": 1, "fp16": 2, "fp8": 3, "fp4_copy": 4, "fp4_mix": 5, "bf16_mix": 6}
@@ -602,10 +597,10 @@ def q4_mfma_probe(kind: str, iters: int, sink: torch.Tensor, seed: int = 1, stre
     if not isinstance(iters, int) or iters < 0 or iters > (1 << 24):
         raise ValueError("iters must be an int in [0, 2^24]")
     _vector(sink, "sink", torch.int32, PROBE_MIX_SINK if PROBE_KINDS[kind] >= 4 else 1)
-    _on_gpu(("sink", sink))
     flops = ctypes.c_double(0.0)
-    _check(lib().q4_mfma_probe(PROBE_KINDS[kind], iters, seed & 0xFFFFFFFF, _ptr(sink), ctypes.byref(flops),
-                               _stream(stream)), "q4_mfma_probe")
+    with _place(stream, ("sink", sink), allocates=False) as (_, s):
+        _check(lib().q4_mfma_probe(PROBE_KINDS[kind], iters, seed & 0xFFFFFFFF, sink.data_ptr(), ctypes.byref(flops), s),
+               "q4_mfma_probe")
     return flops.value
 
 
@@ -626,18 +621,20 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, k: int, W_gu: Q4Tensor, W_d
     interleave_gate_up order (then q4_grouped_gemm_swiglu makes h directly);
     W_down has K rows per expert.  Returns (out [T, K] bf16, Routing)."""
     T, K = x.shape
-    r = q4_moe_route(logits, k, stream)
     P = T * k
-    if fused:
-        h = torch.empty((P, inter), dtype=torch.bfloat16, device=x.device)
-        q4_grouped_gemm_swiglu(x, r.gather, r.offsets, W_gu, inter, h, stream)
-    else:
-        gu = torch.empty((P, 2 * inter), dtype=torch.bfloat16, device=x.device)
-        q4_grouped_gemm(x, r.gather, r.offsets, W_gu, 2 * inter, gu, stream)
-        h = q4_swiglu(gu, inter, stream=stream)
-    y = torch.empty((P, K), dtype=torch.bfloat16, device=x.device)
-    q4_grouped_gemm(h, None, r.offsets, W_down, K, y, stream)
-    return q4_moe_combine(y, r, stream=stream), r
+    with _place(stream, ("x", x), ("logits", logits), ("W_gu", W_gu), ("W_down", W_down)) as (dev, _):
+        # (here the stream is the current one: the tensors in between are its memory)
+        r = q4_moe_route(logits, k)
+        if fused:
+            h = torch.empty((P, inter), dtype=torch.bfloat16, device=dev)
+            q4_grouped_gemm_swiglu(x, r.gather, r.offsets, W_gu, inter, h)
+        else:
+            gu = torch.empty((P, 2 * inter), dtype=torch.bfloat16, device=dev)
+            q4_grouped_gemm(x, r.gather, r.offsets, W_gu, 2 * inter, gu)
+            h = q4_swiglu(gu, inter)
+        y = torch.empty((P, K), dtype=torch.bfloat16, device=dev)
+        q4_grouped_gemm(h, None, r.offsets, W_down, K, y)
+        return q4_moe_combine(y, r), r
 
 
 from .grad import (  # noqa: E402  (uses the helpers above)
