@@ -496,8 +496,9 @@ q4_status q4_moe_topk_backward(const float* logits, int64_t ld, int64_t T, int32
  *     slopes[e] = coef * E * c[e] / (k * n^2)                      (fp32)
  *     loss      = sum_e slopes[e] * P[e]                           (fp32 [1])
  * so loss = coef for choices and probabilities spread evenly, and 0 (slopes too)
- * with n = 0.  Choices with ids outside 0 .. E-1 are in no c[e].  Sums over
- * tokens in 64 bits, in an order that the sizes alone decide.
+ * with n = 0.  Choices with ids outside 0 .. E-1 are in no c[e].  Probabilities
+ * are fp32 (0 below 2^-126 of the token's largest), their sums over tokens in 64
+ * bits, in an order that the sizes alone decide.
  * Backward (the counts have no gradient), with p the softmax of token t:
  *     dlogits[t][e] (+)= dloss * p[e] * (slopes[e] - sum_e' p[e'] slopes[e'])
  * 0 for tokens that do not count; dloss fp32 [1] on the device, NULL: 1;

@@ -8,11 +8,12 @@
 //   slope[e] = coef E c[e] / (k n^2)        loss = sum_e slope[e] P[e]
 //   dlogits[t][e] = dloss p[e] (slope[e] - sum_e' p[e'] slope[e'])
 //
-// (the counts are whole numbers and have no gradient).  Workgroups walk over the
-// tokens and write their sums of p, their counts and their tokens to the
-// workspace; a second kernel adds those in order, in 64 bits, so the results do
-// not vary.  Where there is little to read, one workgroup does it all in one
-// launch.
+// (the counts are whole numbers and have no gradient).  p is fp32; every sum of it
+// over tokens is in 64 bits from the first addition on: in fp32 those of a lane, some
+// thousands in a row of nearly equal values, would lose 2^-16 at 2^24 tokens.
+// Workgroups walk over the tokens and write their sums of p, their counts and their
+// tokens to the workspace; a second kernel adds those in order, so the results do
+// not vary.  Where there is little to read, one workgroup does it all in one launch.
 #include "q4_launch.h"
 #include "q4_wave.h"
 
@@ -137,7 +138,7 @@ moe_balance_kernel(const BalanceArgs a) {
   __shared__ uint32_t count[1024];
   __shared__ uint32_t tokens;
   __shared__ double part[kWaves];
-  extern __shared__ float side[];            // [kWaves][E]
+  extern __shared__ double side[];           // [kWaves][E]
   for (int e = threadIdx.x; e < E; e += kThreads) count[e] = 0u;
   if (threadIdx.x == 0) tokens = 0u;
   __syncthreads();
@@ -146,9 +147,9 @@ moe_balance_kernel(const BalanceArgs a) {
 #pragma unroll
   for (int j = 0; j < kIds; ++j)
     id_at[j] = (uint32_t)(lane / LPT * k + (sub + LPT * j < k ? sub + LPT * j : 0));
-  float sum[PER];
+  double sum[PER];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) sum[i] = 0.0f;
+  for (int i = 0; i < PER; ++i) sum[i] = 0.0;
   uint32_t seen = 0;
   auto use = [&](float (&v)[PER], const uint32_t (&id)[kIds], bool here) {
 #pragma unroll
@@ -158,7 +159,7 @@ moe_balance_kernel(const BalanceArgs a) {
     mine.keep(v, here);
     const float by = exponentials<LPT, PER>(v);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) sum[i] = __builtin_fmaf(v[i], by, sum[i]);
+    for (int i = 0; i < PER; ++i) sum[i] += (double)(v[i] * by);
   };
   const int T = (int)a.T;                    // (below 2^26)
   const int step = (int)gridDim.x * kWaves * kTokens;
@@ -211,10 +212,10 @@ moe_balance_kernel(const BalanceArgs a) {
     if constexpr (ONE) {
       double p = 0.0;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) p += (double)side[w * E + e];
+      for (int w = 0; w < kWaves; ++w) p += side[w * E + e];
       l = finish_expert(a, e, p, count[e], tokens);
     } else {
-      float s = 0.0f;
+      double s = 0.0;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) s += side[w * E + e];
       a.sums[(int64_t)blockIdx.x * padded(E) + e] = s;
@@ -256,12 +257,13 @@ moe_balance_finish_kernel(const BalanceArgs a, int blocks) {
     for (int i = 0; i < (kBlocks + kSlices - 1) / kSlices; ++i) {
       const int b = slice + i * kSlices;
       if (b >= blocks) break;
-      const float4 s = *reinterpret_cast<const float4*>(a.sums + (int64_t)b * row + e0 + 4 * quad);
+      const double2 s = *reinterpret_cast<const double2*>(a.sums + (int64_t)b * row + e0 + 4 * quad);
+      const double2 s2 = *reinterpret_cast<const double2*>(a.sums + (int64_t)b * row + e0 + 4 * quad + 2);
       const int4 n = *reinterpret_cast<const int4*>(a.part_counts + (int64_t)b * row + e0 + 4 * quad);
-      p[0] += (double)s.x;
-      p[1] += (double)s.y;
-      p[2] += (double)s.z;
-      p[3] += (double)s.w;
+      p[0] += s.x;
+      p[1] += s.y;
+      p[2] += s2.x;
+      p[3] += s2.y;
       c[0] += n.x;
       c[1] += n.y;
       c[2] += n.z;
@@ -393,9 +395,9 @@ bool wide(const void* p, int64_t ld, int E) {
 
 template <int LPT, int PER, bool WIDE, bool ONE>
 hipError_t balance_as(const BalanceArgs& a, unsigned blocks, hipStream_t stream) {
-  const size_t side = (size_t)a.E * kWaves * 4;
-  if (side > 32768) {   // (with the kernel's own LDS past 64 KB at the most experts)
-    const hipError_t attr = set_max_lds<&moe_balance_kernel<LPT, PER, WIDE, ONE>>(65536);
+  const size_t side = (size_t)a.E * kWaves * 8;
+  if (side > 32768) {   // (with the kernel's own LDS past 64 KB from 481 experts on)
+    const hipError_t attr = set_max_lds<&moe_balance_kernel<LPT, PER, WIDE, ONE>>(131072);
     if (attr != hipSuccess) return attr;
   }
   moe_balance_kernel<LPT, PER, WIDE, ONE><<<blocks, kThreads, side, stream>>>(a);
@@ -428,14 +430,14 @@ hipError_t balance_of(const BalanceArgs& a, unsigned blocks, hipStream_t stream)
 
 size_t moe_balance_workspace(int64_t T, int32_t E) {
   const unsigned b = balance_blocks(T, E);
-  return b > 1 ? kFinishMost * 8 + (size_t)b * ((size_t)padded(E) * 8 + 4) + 4 : 0;
+  return b > 1 ? kFinishMost * 8 + (size_t)b * ((size_t)padded(E) * 12 + 4) + 4 : 0;
 }
 
 hipError_t launch_moe_balance(BalanceArgs a, void* workspace, hipStream_t stream) {
   const unsigned blocks = balance_blocks(a.T, a.E);
   if (blocks == 1) return balance_of<true>(a, 1, stream);
   a.parts = static_cast<double*>(workspace);
-  a.sums = reinterpret_cast<float*>(a.parts + kFinishMost);
+  a.sums = a.parts + kFinishMost;
   a.part_counts = reinterpret_cast<int32_t*>(a.sums + (size_t)blocks * padded(a.E));
   a.part_tokens = a.part_counts + (size_t)blocks * padded(a.E);
   a.ticket = reinterpret_cast<uint32_t*>(a.part_tokens + blocks);

@@ -187,8 +187,7 @@ struct BalanceArgs {
   float* loss;               // [1]
   int32_t* counts;           // [E]
   float* slopes;             // [E]
-  double* parts;             // (of the workspace, set by the launch)
-  float* sums;
+  double *parts, *sums;      // (of the workspace, set by the launch)
   int32_t *part_counts, *part_tokens;
   uint32_t* ticket;
 };
