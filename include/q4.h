@@ -333,7 +333,10 @@ q4_status q4_gemm_quantized(int64_t M, const void* A_bf16, int64_t lda, const q4
  *   pointer and leading dimension).  Other overlaps are not allowed.
  * A row with an infinity or a NaN, or whose sum of squares reaches 2^128, gives
  * NaN throughout (in 8 bits: the scale NaN, codes without meaning), and so does a
- * row of zeros with eps = 0.  Other rows are not touched by it.
+ * row of zeros with eps = 0.  Other rows are not touched by it.  Small rows are what
+ * the formula says down to bf16's least number, also where their squares are below
+ * fp32's range (eps = 0, or as small).  Weights are meant to be below 2^64: h * weight
+ * is a product in fp32, for such rows of 2^80 h.
  */
 q4_status q4_rmsnorm(const void* x_bf16, int64_t ldx, const void* residual_bf16, int64_t ldr, const void* weight,
                      int w_dtype, float eps, int64_t rows, int64_t cols, void* h_bf16, int64_t ldh, void* y_bf16,

@@ -21,6 +21,8 @@
 #include "q4_mma.h"
 #include "q4_row8.h"
 
+#include <type_traits>
+
 namespace q4 {
 namespace {
 
@@ -41,18 +43,30 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&v)[8]) {
   return make_uint4(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]), pk_bf16(v[6], v[7]));
 }
 
-// 1 / sqrt(mean + eps); NaN where the sum of squares is no number below 2^128,
-// so that a row whose squares overflow is not taken for zeros.
-__device__ __forceinline__ float row_rstd(float ss, int cols, float eps) {
-  return ss <= 3.402823466e+38f ? 1.0f / __builtin_sqrtf(ss / (float)cols + eps) : u2f(0x7FC00000u);
+// mean(h^2) + eps, and 1 / sqrt of it; NaN where the sum of squares is no number below
+// 2^128, so that a row whose squares overflow is not taken for zeros.
+__device__ __forceinline__ float row_mean(float ss, int cols, float eps) {
+  return ss <= 3.402823466e+38f ? ss / (float)cols + eps : u2f(0x7FC00000u);
 }
+__device__ __forceinline__ float row_rstd(float mean) { return 1.0f / __builtin_sqrtf(mean); }
+
+// Rows so small that their squares vanish or lose bits in fp32 (with eps as small as
+// they are): below kLeastMean the sums are made again from 2^80 h and 2^160 eps, and r
+// then is 2^-80 of itself.  |h| is 2^-133 at least and sqrt(cols) 2^-30 < 2^-22 at most
+// there, so that squares of 2^80 h are 2^-106 at least, their mean is 2^-121 at least
+// and their sum, 32768 2^100 at most, far below 2^128.  Scales by powers of two commute
+// with every step: a row that either way holds gets the same results bit for bit.  In a
+// mean of 2^-60 and more, squares below fp32's normal range are less than 2^-66 of it.
+constexpr float kLeastMean = 0x1p-60f, kRaise = 0x1p80f;
+template <bool RAISED>
+__device__ __forceinline__ float raised(float v) { return RAISED ? v * kRaise : v; }
 
 // KIND: kRowInt8, kRowE4m3, or -1 for no output in 8 bits.  PAST: rows are read and h
 // is written past the caches (kPastForward values and more: 16385 x 8192 in 143 us,
 // 6.6 TB/s, 164 without; 4096 x 8192, which they hold, 39 us and 42 with it).  The
 // codes are not: the product reads them next, and 8 bytes at a time they gain nothing.
 template <int WAVES, int CH, int KIND, bool WF32, bool PAST>
-__global__ void __launch_bounds__(64 * (WAVES < 4 ? 4 : WAVES))
+__global__ void __launch_bounds__(64 * (WAVES < 4 ? 4 : WAVES), WAVES == 16 ? 8 : 1)   // (two workgroups per CU)
 rmsnorm_kernel(const NormArgs p) {
   constexpr int kRows = WAVES < 4 ? 4 / WAVES : 1;
   const int tid = threadIdx.x % (64 * WAVES), in = threadIdx.x / (64 * WAVES);
@@ -95,41 +109,52 @@ rmsnorm_kernel(const NormArgs p) {
     }
   }
   float hw[CH][8];
-  float ss = 0.0f;
-  uint32_t most = 0;
-#pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int k0 = (tid + 64 * WAVES * i) * 8;
-    if (k0 < cols) {
-      float a[8], w[8];
-      unpack_bf16x8(v[i], a);
-      load_weight8<WF32>(p.w, k0, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        ss = __builtin_fmaf(a[j], a[j], ss);
-        hw[i][j] = a[j] * w[j];
-      }
-      if (KIND >= 0) most = max_bits8(hw[i], most);
-    }
-  }
-  ss = lanes_sum(ss);
-  if (KIND >= 0) most = lanes_max_bits(most);
-  if constexpr (WAVES > 1) {
-    __shared__ float sum[WAVES];
-    __shared__ uint32_t top[WAVES];
-    if ((tid & 63) == 0) {
-      sum[tid >> 6] = ss;
-      top[tid >> 6] = most;
-    }
-    __syncthreads();
+  float ss, mean;
+  uint32_t most;
+  __shared__ float sum[2][WAVES];
+  __shared__ uint32_t top[2][WAVES];
+  auto sums = [&](auto raise) {
+    constexpr bool kRaised = decltype(raise)::value;
     ss = 0.0f;
+    most = 0;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
-      ss += sum[w];
-      most = top[w] > most ? top[w] : most;
+    for (int i = 0; i < CH; ++i) {
+      const int k0 = (tid + 64 * WAVES * i) * 8;
+      if (k0 < cols) {
+        float a[8], w[8];
+        unpack_bf16x8(kRaised ? load16<PAST>((p.residual ? p.h + r * p.ldh : x) + k0) : v[i], a);
+        load_weight8<WF32>(p.w, k0, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          a[j] = raised<kRaised>(a[j]);
+          ss = __builtin_fmaf(a[j], a[j], ss);
+          hw[i][j] = a[j] * w[j];
+        }
+        if (KIND >= 0) most = max_bits8(hw[i], most);
+      }
     }
-  }
-  const float rstd = row_rstd(ss, cols, p.eps);
+    ss = lanes_sum(ss);
+    if (KIND >= 0) most = lanes_max_bits(most);
+    if constexpr (WAVES > 1) {
+      if ((tid & 63) == 0) {
+        sum[kRaised][tid >> 6] = ss;
+        top[kRaised][tid >> 6] = most;
+      }
+      __syncthreads();
+      ss = 0.0f;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) {
+        ss += sum[kRaised][w];
+        most = top[kRaised][w] > most ? top[kRaised][w] : most;
+      }
+    }
+    mean = row_mean(ss, cols, raised<kRaised>(raised<kRaised>(p.eps)));
+  };
+  sums(std::false_type());
+  // (the same for all of a row; read again from where it stands, so that ordinary rows
+  // need no registers for it)
+  if (mean < kLeastMean) sums(std::true_type());
+  const float rstd = row_rstd(mean);
   float f = 0.0f;
   if constexpr (KIND >= 0) {
     const float a = u2f(most) * rstd;              // the largest |y|
@@ -185,7 +210,7 @@ rmsnorm_backward_kernel(const NormGradArgs p) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
   }
-  __shared__ float part[2][2][WAVES];
+  __shared__ float part[3][2][WAVES];
   int turn = 0;
   for (int64_t r = (int64_t)blockIdx.x * kRows + in; r < p.rows; r += (int64_t)gridDim.x * kRows, turn ^= 1) {
     uint4 vd[CH], vh[CH], vr[CH];
@@ -196,38 +221,50 @@ rmsnorm_backward_kernel(const NormGradArgs p) {
       vh[i] = load16<PAST>(p.h + r * p.ldh + at);
       if (p.dh) vr[i] = load16<PAST>(p.dh + r * p.lddh + at);
     }
-    float ss = 0.0f, c = 0.0f;
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      if ((tid + kThreads * i) * 8 < cols) {
-        float d[8], h[8];
-        unpack_bf16x8(vd[i], d);
-        unpack_bf16x8(vh[i], h);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          ss = __builtin_fmaf(h[j], h[j], ss);
-          c = __builtin_fmaf(d[j] * w[i][j], h[j], c);
-        }
-      }
-    }
-    ss = lanes_sum(ss);
-    c = lanes_sum(c);
-    if constexpr (WAVES > 1) {
-      // two sets in turn: a wave writes the next row's while others read this one's
-      if ((tid & 63) == 0) {
-        part[turn][0][tid >> 6] = ss;
-        part[turn][1][tid >> 6] = c;
-      }
-      __syncthreads();
+    // (a row whose mean is below kLeastMean comes round again, with `up` 2^80)
+    float ss, c, mean, up = 1.0f, half = 1.0f;
+    for (int set = turn;; set = 2) {
       ss = c = 0.0f;
 #pragma unroll
-      for (int v = 0; v < WAVES; ++v) {
-        ss += part[turn][0][v];
-        c += part[turn][1][v];
+      for (int i = 0; i < CH; ++i) {
+        if ((tid + kThreads * i) * 8 < cols) {
+          float d[8], h[8];
+          unpack_bf16x8(vd[i], d);
+          unpack_bf16x8(vh[i], h);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            h[j] *= up;
+            ss = __builtin_fmaf(h[j], h[j], ss);
+            c = __builtin_fmaf(d[j] * w[i][j], h[j], c);
+          }
+        }
       }
+      ss = lanes_sum(ss);
+      c = lanes_sum(c);
+      if constexpr (WAVES > 1) {
+        // two sets in turn: a wave writes the next row's while others read this one's (the
+        // third: between two rows that come round again there is a row's barrier)
+        if ((tid & 63) == 0) {
+          part[set][0][tid >> 6] = ss;
+          part[set][1][tid >> 6] = c;
+        }
+        __syncthreads();
+        ss = c = 0.0f;
+#pragma unroll
+        for (int v = 0; v < WAVES; ++v) {
+          ss += part[set][0][v];
+          c += part[set][1][v];
+        }
+      }
+      mean = row_mean(ss, cols, p.eps * up * up);
+      if (!(mean < kLeastMean) || set == 2) break;
+      up = kRaise;
+      half = 0x1p40f;
     }
-    const float rstd = row_rstd(ss, cols, p.eps);
+    const float rstd = row_rstd(mean);
     const float t = c / (float)cols * rstd * rstd;
+    // r is rstd times `up`, past fp32's range where h is least: half of the 80 on either side of a product
+    const float by = rstd * half;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int k0 = (tid + kThreads * i) * 8;
@@ -238,7 +275,8 @@ rmsnorm_backward_kernel(const NormGradArgs p) {
         if (p.dh) unpack_bf16x8(vr[i], o);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float e = rstd * __builtin_fmaf(-t, h[j], d[j] * w[i][j]);
+          h[j] *= up;
+          const float e = by * __builtin_fmaf(-t, h[j], d[j] * w[i][j]) * half;
           o[j] = p.dh ? o[j] + e : e;
           dw[i][j] = __builtin_fmaf(d[j], h[j] * rstd, dw[i][j]);
         }
