@@ -122,6 +122,14 @@ grad_square_kernel(const Table t, double* __restrict__ sums) {
   if (threadIdx.x == 0) sums[blockIdx.x] = s;
 }
 
+// Sums of squares up to which every workgroup of the clipping adds them for itself:
+// those of one full launch.  More are added once, by a launch of one workgroup, and the
+// clipping reads its norm, since all workgroups of all launches would read the sums of
+// all launches, a time with the square of the tensors' number.  Tensors of 256 KB, in
+// a graph: 20 take 10.3 us and would take 11.5 with that launch, 129 29.6 (29.2 without
+// it), 300 59.3 (61.7), 20000 3.8 ms (14.7).
+constexpr int kOwnSums = kBlocks;
+
 // The norm from the workgroups' sums, added by every caller in the same order.
 __device__ __forceinline__ double norm_of(const double* sums, int count) {
   double s = 0.0;
@@ -129,10 +137,13 @@ __device__ __forceinline__ double norm_of(const double* sums, int count) {
   return sqrt(block_sum(s));
 }
 
+// norm, whole: either may be NULL.
 __global__ void __launch_bounds__(kThreads)
-grad_norm_kernel(const double* __restrict__ sums, int count, float* __restrict__ norm) {
+grad_norm_kernel(const double* __restrict__ sums, int count, float* __restrict__ norm, double* __restrict__ whole) {
   const double n = norm_of(sums, count);
-  if (threadIdx.x == 0) *norm = (float)n;
+  if (threadIdx.x != 0) return;
+  if (norm) *norm = (float)n;
+  if (whole) *whole = n;
 }
 
 // The factor stays in 64 bits: where the norm passes fp32's range it is itself
@@ -178,13 +189,15 @@ __device__ __forceinline__ void scale(const uint8_t* p, uint8_t* o, int64_t at, 
 // Read and written past the caches (3.9 GB each way in 1333 us, 5.8 TB/s; 1424
 // without; from the last chunk to the first, to find what the squares read last in
 // the memory-side cache: no faster).
-// GIVEN: the norm is the caller's; otherwise every workgroup makes it from the
-// sums (in the same order, so the same one) and the first writes it down.
-template <bool GIVEN>
+// FROM: the norm is the caller's, was made from the sums (and lies at `sums`), or
+// every workgroup makes it from them (in the same order, so the same one) and the
+// first writes it down.
+enum { kFromCaller, kFromWhole, kFromSums };
+template <int FROM>
 __global__ void __launch_bounds__(kThreads)
 grad_clip_kernel(const Table t, const double* __restrict__ sums, int count, const float* __restrict__ given,
                  float max_norm, float* __restrict__ norm, int in_place) {
-  const double n = GIVEN ? (double)*given : norm_of(sums, count);
+  const double n = FROM == kFromCaller ? (double)*given : FROM == kFromWhole ? *sums : norm_of(sums, count);
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
   double by = (double)max_norm / (n + 1e-6);
   if (by > 1.0) by = 1.0;               // (NaN stays NaN)
@@ -246,7 +259,8 @@ hipError_t squares_of_all(const GradList& g, double* sums, int* count, hipStream
 
 }  // namespace
 
-size_t grad_workspace(int64_t n) { return (size_t)((n + kTensors - 1) / kTensors) * kBlocks * 8; }
+// The sums of every launch and, behind them, the norm in 64 bits.
+size_t grad_workspace(int64_t n) { return n ? (size_t)((n + kTensors - 1) / kTensors) * kBlocks * 8 + 8 : 0; }
 
 // Chunks are counted in 32 bits.
 bool grad_fits(const GradList& g) {
@@ -264,31 +278,38 @@ hipError_t launch_grad_norm(const GradList& g, float* norm, double* sums, hipStr
   int count = 0;
   const hipError_t e = squares_of_all(g, sums, &count, stream);
   if (e != hipSuccess) return e;
-  grad_norm_kernel<<<1, kThreads, 0, stream>>>(sums, count, norm);
+  grad_norm_kernel<<<1, kThreads, 0, stream>>>(sums, count, norm, nullptr);
   return hipGetLastError();
 }
 
 hipError_t launch_grad_clip(const GradList& g, void* const* out, const float* given, float max_norm, float* norm,
                             double* sums, hipStream_t stream) {
   int count = 0;
+  auto kernel = grad_clip_kernel<kFromCaller>;
   if (!given) {
-    const hipError_t e = squares_of_all(g, sums, &count, stream);
+    hipError_t e = squares_of_all(g, sums, &count, stream);
     if (e != hipSuccess) return e;
+    kernel = grad_clip_kernel<kFromSums>;
+    if (count > kOwnSums || count == 0) {   // (no launch of the clipping writes the norm of no values)
+      double* whole = count ? sums + count : nullptr;
+      if (norm || count) grad_norm_kernel<<<1, kThreads, 0, stream>>>(sums, count, norm, whole);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      kernel = grad_clip_kernel<kFromWhole>;
+      sums = whole;
+      norm = nullptr;
+    }
   }
-  bool written = false;
   for (int64_t from = 0; from < g.n; from += kTensors) {
     Table t;
     const int64_t chunks = fill(t, g, from, out);
     if (!chunks) continue;
-    auto kernel = given ? grad_clip_kernel<true> : grad_clip_kernel<false>;
-    kernel<<<blocks_of(chunks), kThreads, 0, stream>>>(t, sums, count, given, max_norm, written ? nullptr : norm,
-                                                       out == nullptr);
-    written = true;
+    kernel<<<blocks_of(chunks), kThreads, 0, stream>>>(t, sums, count, given, max_norm, norm, out == nullptr);
+    norm = nullptr;   // (written by the first)
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (!written && norm && !given) grad_norm_kernel<<<1, kThreads, 0, stream>>>(sums, 0, norm);
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 }  // namespace q4
