@@ -647,7 +647,8 @@ q4_status q4_grouped_gemm_wgrad(const void* dC_bf16, int64_t lddc, const void* A
  * same counts and types, or NULL: in place (nothing is written where the factor
  * is 1).  An out[i] may be grads[i] itself; otherwise outputs must overlap
  * neither each other nor any gradient (Q4_ERR_ALIGN: also a tensor that is
- * listed twice).  max_norm >= 0, inf for no limit.
+ * listed twice), and no output a norm, which workgroups read while others write
+ * (nor norm_out a gradient).  max_norm >= 0, inf for no limit.
  * workspace: 16-byte aligned, of the size the query gives (not read with
  * norm_in); the contents need not be kept.
  */

@@ -139,8 +139,8 @@ q4_status check_grad_workspace(int64_t n, const void* workspace, size_t bytes) {
 }
 
 // What is written overlaps nothing else: outputs (the gradients themselves in
-// place) neither each other nor a gradient that is not their own.
-q4_status check_apart(const q4::GradList& g, void* const* out) {
+// place) neither each other nor a gradient that is not their own, and neither norm.
+q4_status check_apart(const q4::GradList& g, void* const* out, const float* norm_in, const float* norm_out) {
   struct Span {
     uintptr_t from, to;
     bool written;
@@ -161,6 +161,8 @@ q4_status check_apart(const q4::GradList& g, void* const* out) {
     add(g.data[i], bytes, own);
     if (!own) add(out[i], bytes, true);
   }
+  if (norm_in) add(norm_in, 4, false);
+  else if (norm_out) add(norm_out, 4, true);
   if (!sorted) std::sort(spans.get(), spans.get() + m, [](const Span& a, const Span& b) { return a.from < b.from; });
   uintptr_t read_to = 0, write_to = 0;   // ends of what lies before, read only and written
   for (size_t i = 0; i < m; ++i) {
@@ -759,7 +761,7 @@ q4_status q4_grad_clip(int64_t n, const void* const* grads, const int64_t* count
     st = check_grad_workspace(n, workspace, workspace_bytes);
     if (st != Q4_OK) return st;
   }
-  st = check_apart(g, out);
+  st = check_apart(g, out, norm_in, norm_out);
   if (st != Q4_OK) return st;
   return hip_status(q4::launch_grad_clip(g, out, norm_in, max_norm, norm_in ? nullptr : norm_out,
                                          static_cast<double*>(workspace), as_stream(stream)));
