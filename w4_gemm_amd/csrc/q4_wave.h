@@ -22,11 +22,6 @@ struct AddOp {
     return __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b));
   }
 };
-struct MaxOp {   // fp32, NaN passed over
-  __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const {
-    return __builtin_bit_cast(uint32_t, fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)));
-  }
-};
 struct MaxBitsOp {
   __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return a > b ? a : b; }
 };
@@ -53,10 +48,6 @@ __device__ __forceinline__ uint32_t reduce_lanes(uint32_t v, OP op) {
 template <int LANES = 64>
 __device__ __forceinline__ float lanes_sum(float v) {
   return __builtin_bit_cast(float, reduce_lanes<LANES>(__builtin_bit_cast(uint32_t, v), AddOp()));
-}
-template <int LANES = 64>
-__device__ __forceinline__ float lanes_max(float v) {
-  return __builtin_bit_cast(float, reduce_lanes<LANES>(__builtin_bit_cast(uint32_t, v), MaxOp()));
 }
 template <int LANES = 64>
 __device__ __forceinline__ uint32_t lanes_max_bits(uint32_t v) {
