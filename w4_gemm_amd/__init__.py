@@ -74,6 +74,19 @@ class _Q4TensorC(ctypes.Structure):
 
 _PACK = struct.Struct("=iiqqQQQ").pack    # the fields of _Q4TensorC
 
+
+class _Descriptor:
+    """Type of the library's q4_tensor arguments: a structure's bytes
+    (Q4Tensor.packed()), a reference to one, or None."""
+    _size = ctypes.sizeof(_Q4TensorC)
+    _reference = ctypes.POINTER(_Q4TensorC).from_param
+
+    @classmethod
+    def from_param(cls, value):
+        if value is None or (type(value) is bytes and len(value) == cls._size):
+            return value
+        return cls._reference(value)
+
 _LIB = None
 
 
@@ -85,7 +98,7 @@ def _lib_handle():
             _build.build()
         L = ctypes.CDLL(LIB_PATH)
         i64, vp, i32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32
-        P = vp      # a descriptor: byref of a _Q4TensorC, or its bytes
+        P = _Descriptor
         sz, SZ, I32P = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(i32)
         sig = {
             "q4_version": ([], ctypes.c_int),
