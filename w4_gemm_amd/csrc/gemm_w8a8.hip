@@ -9,8 +9,11 @@
 // Both operands are row-major.  Their rows are copied to LDS by direct
 // global->LDS loads (1 KB per wave instruction, whole 128-byte lines of a row),
 // the 16-byte chunk c of row r to place c ^ key(r): a copy permutes chunks within
-// a line, a fragment read meets eight rows of different keys at once, and so
-// neither side has bank conflicts.
+// a line, and a fragment read meets eight rows of different keys at once.  So neither
+// side has bank conflicts where a row is one line of 128 bytes (BK = 128, and the large
+// blocks); longer rows begin at multiples of 256 bytes, a key of three bits keeps a
+// read in one half of the banks, and each has 4 conflicts (1.4e6 in the 28672 x 8192
+// product of one token, 0.7e6 in 33 x 8192 x 8192).
 //
 // v_mfma_i32_16x16x64_i8: lane l supplies row l % 16, k = 16 (l / 16) .. +15 of
 // both operands.  The weight is the instruction's row operand, so a lane ends

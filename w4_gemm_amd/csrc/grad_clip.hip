@@ -101,8 +101,9 @@ __device__ __forceinline__ double squares(const uint8_t* p, int64_t at, int64_t 
   return s;
 }
 
-// PAST: read past the caches, where the gradients are more than they hold (3.9 GB in
-// 537 us, 7.2 TB/s, 609 without); fewer are read again from there by the clipping.
+// PAST: read past the caches, where the gradients are more than they hold (3.88 GB in
+// 545 to 590 us, 6.6 to 7.1 TB/s, 662 without where it took 586 with); fewer are read
+// again from there by the clipping.
 template <bool PAST>
 __global__ void __launch_bounds__(kThreads)
 grad_square_kernel(const Table t, double* __restrict__ sums) {
@@ -186,8 +187,8 @@ __device__ __forceinline__ void scale(const uint8_t* p, uint8_t* o, int64_t at, 
   }
 }
 
-// Read and written past the caches (3.9 GB each way in 1333 us, 5.8 TB/s; 1424
-// without; from the last chunk to the first, to find what the squares read last in
+// Read and written past the caches (3.88 GB each way in 1376 us, 5.6 TB/s, 1436
+// without in turn on one card; 1395 to 1452 behind the squares; from the last chunk to the first, to find what the squares read last in
 // the memory-side cache: no faster).
 // FROM: the norm is the caller's, was made from the sums (and lies at `sums`), or
 // every workgroup makes it from them (in the same order, so the same one) and the

@@ -124,8 +124,9 @@ __device__ __forceinline__ double block_loss(double l, double (&part)[kWaves]) {
 }
 
 // ONE: a single workgroup, which finishes by itself.  Bound by its VALU instructions,
-// 75 a token in 60% of its cycles, and by the loads of its first turns: 65537 tokens
-// of 256 experts in 16.7 us, 4.1 TB/s (eight turns together: 18 us).
+// 83 a token in 61% of its cycles (8 of them for sums in 64 bits: 16.3 us without, and
+// 18 with eight turns together), and by the loads of its first turns: 65537 tokens of
+// 256 experts in 17.4 us, 4.0 TB/s.
 template <int LPT, int PER, bool WIDE, bool ONE>
 __global__ void __launch_bounds__(kThreads)
 moe_balance_kernel(const BalanceArgs a) {
@@ -234,9 +235,10 @@ moe_balance_kernel(const BalanceArgs a) {
 // The workgroups' sums, added in order: a workgroup per 64 experts, in it a thread
 // per four of them and 64th of the sums, then 16 threads per expert.  The last
 // workgroup to end (the ticket was cleared by the first kernel) adds their parts
-// of the loss, in their order.  256 workgroups' sums of 256 experts: 8 us, latency
-// (10 us in a single workgroup; both kernels 22.9 us, 23.7 with 32 experts per
-// workgroup and 23.5 with 16, of 1024 experts 27.2, 29.2 and 32.4).
+// of the loss, in their order.  256 workgroups' sums of 256 experts: 8.5 us, latency: a
+// thread's turns are waited for one by one, since each may be the last (10 us in a single
+// workgroup; with sums of fp32 both kernels 22.9 us, 23.7 with 32 experts per workgroup
+// and 23.5 with 16, of 1024 experts 27.2, 29.2 and 32.4).
 constexpr int kFinishExperts = 64;
 constexpr int kFinishMost = 1024 / kFinishExperts;   // workgroups
 __global__ void __launch_bounds__(kThreads)
@@ -310,7 +312,7 @@ moe_balance_finish_kernel(const BalanceArgs a, int blocks) {
 }
 
 // The gradient: the same softmax again, from the logits alone.  65537 tokens of 256
-// experts in 21.8 us, 6.2 TB/s: bound by HBM.
+// experts in 20 to 22 us, 6.1 to 6.9 TB/s: bound by HBM.
 template <int LPT, int PER, bool WIDE>
 __global__ void __launch_bounds__(kBackThreads)
 moe_balance_backward_kernel(const BalanceGradArgs a) {

@@ -14,8 +14,9 @@
 //
 // A row is held in registers by 1, 4 or 16 waves (lane i of them has the chunks
 // of eight values i, i + 64 WAVES, ...) and read once.  Bound by HBM: 16385 x 8192 with
-// a residual and 8-bit codes in 143 us, 6.6 TB/s, its gradient (16384 rows) in 179 us,
-// 6.0 TB/s, and 7 us for the weight's sum; one row in 3.5 us, all latency.
+// a residual and 8-bit codes in 143 to 146 us, 6.4 to 6.6 TB/s, its gradient (16384 rows)
+// in 172 to 186 us on several cards, 5.8 to 6.2 TB/s, and 7 us for the weight's sum; one
+// row in 3.2 to 3.7 us, all latency.
 #include "q4_launch.h"
 #include "q4_layout.h"
 #include "q4_mma.h"
@@ -62,9 +63,9 @@ template <bool RAISED>
 __device__ __forceinline__ float raised(float v) { return RAISED ? v * kRaise : v; }
 
 // KIND: kRowInt8, kRowE4m3, or -1 for no output in 8 bits.  PAST: rows are read and h
-// is written past the caches (kPastForward values and more: 16385 x 8192 in 143 us,
-// 6.6 TB/s, 164 without; 4096 x 8192, which they hold, 39 us and 42 with it).  The
-// codes are not: the product reads them next, and 8 bytes at a time they gain nothing.
+// is written past the caches (kPastForward values and more: 16385 x 8192 in 144 us, 163
+// without; 4096 x 8192, which they hold, 36.8 us and 42.6 with it).  The codes are not:
+// the product reads them next, and 8 bytes at a time they gain nothing.
 template <int WAVES, int CH, int KIND, bool WF32, bool PAST>
 __global__ void __launch_bounds__(64 * (WAVES < 4 ? 4 : WAVES), WAVES == 16 ? 8 : 1)   // (two workgroups per CU)
 rmsnorm_kernel(const NormArgs p) {
@@ -171,7 +172,9 @@ rmsnorm_kernel(const NormArgs p) {
       *reinterpret_cast<uint2*>(p.codes + r * cols + k0) = int8_pack8(hw[i], f);
     } else if constexpr (KIND == kRowE4m3) {
       const uint2 q = e4m3_pack8(hw[i], f);
-      if (p.tiled) {   // even elements in one word, odd ones in the next
+      // even elements in one word, odd ones in the next.  (4 bytes at a time, of a line that
+      // eight rows share: 4096 x 8192 in 52 us, 36 in rows; 16384 rows 219 and 144.)
+      if (p.tiled) {
         *reinterpret_cast<uint32_t*>(p.codes + fp8_tiled_dword(r, k0, cols, 0)) = __builtin_amdgcn_perm(q.y, q.x, 0x06040200u);
         *reinterpret_cast<uint32_t*>(p.codes + fp8_tiled_dword(r, k0, cols, 1)) = __builtin_amdgcn_perm(q.y, q.x, 0x07050301u);
       } else {
@@ -193,8 +196,11 @@ rmsnorm_kernel(const NormArgs p) {
 // together and nothing but h need be kept from the forward pass.  Workgroups
 // walk over rows with dw of their columns in registers; each writes its sum to
 // the workspace, and a second kernel adds those in order.  PAST: rows are read past
-// the caches (kPastBackward values and more: 16384 x 8192 in 182 us, 205 without;
-// 512 x 8192 in 19 us, 21 with it); dx, which is read next, is not written so.
+// the caches (kPastBackward values and more; without the weight's gradient 16385 x 8192
+// in 161 us, 192 without; 4096 x 8192 in 45 and 43, 512 x 8192 in 8.3 both ways); dx,
+// which is read next, is not written so.  Above 8192 columns the 1024 threads have 128
+// registers each and want more (129 to 161 spilled within the loop): 4096 x 16384 in
+// 386 us with the weight's sum, five times what its bytes take.
 template <int WAVES, int CH, bool WF32, bool PAST>
 __global__ void __launch_bounds__(64 * (WAVES < 4 ? 4 : WAVES))
 rmsnorm_backward_kernel(const NormGradArgs p) {
@@ -312,7 +318,8 @@ rmsnorm_backward_kernel(const NormGradArgs p) {
 }
 
 // dw[k] (+)= sum over the workgroups' sums: 32 columns by 32 slices per
-// workgroup, a slice's loads on the way together, the slices' sums added in order.
+// workgroup, the slices' sums added in order.  512 of them of 8192 columns, 17 MB, in
+// 7 us: a slice's loads are each under a condition and so waited for one by one.
 constexpr int kGradBlocks = 512;
 __global__ void __launch_bounds__(1024)
 rmsnorm_weight_sum_kernel(const float* __restrict__ partial, int blocks, int cols, float* __restrict__ dw,
