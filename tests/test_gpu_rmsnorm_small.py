@@ -140,3 +140,27 @@ def test_zeros_without_eps_stay_without_numbers():
         assert (y[[1, 3]] == 1).all() and torch.isfinite(q.scales[[1, 3]]).all()
     dx, _ = q4.q4_rmsnorm_backward(torch.ones_like(x).cuda(), x.cuda(), w, 0.0)
     assert torch.isnan(dx[[0, 2]]).all() and torch.isfinite(dx[1]).all()
+
+
+def test_among_more_rows_than_the_caches_hold():
+    """Small rows where rows are read and h is written past the caches: a small row's sums read h again."""
+    rows, cols = 6200, 8192
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x, res = (torch.randn(rows, cols, device="cuda", generator=g).to(BF16) for _ in range(2))
+    x[1::3] *= 1e-25
+    res[1::3] *= 1e-25
+    w = (1 + 0.2 * torch.randn(cols, device="cuda", generator=g)).to(BF16)
+    pick = [0, 1, 2, 4, 3000, 3001, 6196, 6199]
+    assert sum(r % 3 == 1 for r in pick) == 5
+    for fmt in ("int8_row", "fp8_row"):
+        y, q = both(x, w, 0.0, fmt, res)
+        h = q4.q4_rmsnorm(x, w, 0.0, residual=res)[0]
+        ys, qs = both(x[pick], w, 0.0, fmt, res[pick])
+        assert torch.equal(h, (x.float() + res.float()).to(BF16))
+        assert torch.equal(y[pick], ys) and torch.equal(q.codes[pick], qs.codes) and torch.equal(q.scales[pick], qs.scales)
+        near(ys, ob.rmsnorm(n64(h[pick]), n64(w), 0.0), 2.0 ** -8 + FP32)
+        assert torch.isfinite(y).all() and torch.isfinite(q.scales).all()
+    dy = torch.randn(rows, cols, device="cuda", generator=g).to(BF16) * 2.0 ** -20
+    dx, dw = q4.q4_rmsnorm_backward(dy, h, w, 0.0)
+    assert torch.equal(dx[pick], q4.q4_rmsnorm_backward(dy[pick], h[pick], w, 0.0)[0])
+    assert torch.isfinite(dx).all() and torch.isfinite(dw).all()

@@ -148,10 +148,12 @@ q4_status check_apart(const q4::GradList& g, void* const* out, const float* norm
   const std::unique_ptr<Span[]> spans(new (std::nothrow) Span[2 * (size_t)g.n + 1]);
   if (!spans) return Q4_ERR_SHAPE;
   size_t m = 0;
-  bool sorted = true;
+  bool sorted = true, on_norm = false;
+  const uintptr_t norm = reinterpret_cast<uintptr_t>(norm_in ? norm_in : norm_out);
   auto add = [&](const void* p, uintptr_t bytes, bool written) {
     const uintptr_t from = reinterpret_cast<uintptr_t>(p);
     sorted = sorted && (m == 0 || spans[m - 1].from <= from);
+    on_norm = on_norm || ((written || !norm_in) && norm && norm < from + bytes && from < norm + 4);
     spans[m++] = Span{from, from + bytes, written};
   };
   for (int64_t i = 0; i < g.n; ++i) {
@@ -161,8 +163,7 @@ q4_status check_apart(const q4::GradList& g, void* const* out, const float* norm
     add(g.data[i], bytes, own);
     if (!own) add(out[i], bytes, true);
   }
-  if (norm_in) add(norm_in, 4, false);
-  else if (norm_out) add(norm_out, 4, true);
+  if (on_norm) return Q4_ERR_ALIGN;
   if (!sorted) std::sort(spans.get(), spans.get() + m, [](const Span& a, const Span& b) { return a.from < b.from; });
   uintptr_t read_to = 0, write_to = 0;   // ends of what lies before, read only and written
   for (size_t i = 0; i < m; ++i) {
