@@ -87,6 +87,7 @@ class _Descriptor:
             return value
         return cls._reference(value)
 
+
 _LIB = None
 
 
