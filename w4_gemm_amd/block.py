@@ -228,7 +228,8 @@ def q4_grad_clip(grads: Sequence[torch.Tensor], max_norm: float, norm: Optional[
     """Scales the gradients by min(1, max_norm / (norm + 1e-6)), in place or
     into the tensors `out`, and returns the norm (float32 scalar on their
     device): the one given (e.g. combined over ranks), or that of these
-    gradients, made in the same call.  No tensor may be listed twice."""
+    gradients, made in the same call.  No tensor may be listed twice, nor may a
+    given norm lie in one that is written."""
     grads = list(grads)
     if not grads:
         raise ValueError("grads must hold at least one tensor")
